@@ -407,6 +407,88 @@ mq_status mq_kv_quant_bf16(const uint16_t* x, uint8_t* codes, float* params, int
                            int32_t bits, void* stream);
 
 /*
+ * RMS norm with the residual's addition and 8-bit output, in front of the
+ * 8-bit linear layers.
+ * Source: pymllm Setup and Usage, Overview (the quantized linear schemes sit
+ * among 16-bit activations) and section "W8A8 first-run JIT compilation" (an
+ * activation quantizer in front of the scaled matmul); the pages do not fuse
+ * it with the norm that produces those activations, this entry does.
+ *     h[m,k] = rne16(x[m,k] + residual[m,k])           (h = x without a residual)
+ *     r[m]   = fl32(1 / sqrt(sum_k h[m,k]^2 / K + eps))  in binary64
+ *     v[m,k] = fl32(fl32(h[m,k] * r[m]) * weight[k])
+ *   int8:  s_tok[m] = fl32(max_k |v[m,k]| / 127),
+ *          xq[m,k]  = clamp(rne(fl32(v[m,k] / s_tok[m])), -127, 127)
+ *          (the codes and scales mq_quant_per_token_int8 gives for v)
+ *   fp8:   block b holds k = 128 b .. 128 b + 127 (the last may be short),
+ *          s_x[b,m] = fl32(max_{k in b} |v[m,k]| / 448),
+ *          xq[m,k]  = e4m3_rne(clamp(fl32(v[m,k] / s_x[b,m]), -448, 448))
+ * with a scale of 0 giving codes 0. e4m3 is the OCP 8-bit format without
+ * infinities (largest value 448). The squares are added in binary64, so codes
+ * and scales do not depend on the order of the sum (bit-exact to this
+ * definition but for rows whose r lies within 2^-50 of a rounding border).
+ *
+ *   x, residual  [M, K] fp16   in   (residual may be NULL, with h)
+ *   weight       [K]    fp16   in
+ *   h            [M, K] fp16   out  (NULL without a residual; may be the
+ *                                    residual's own buffer, updated in place)
+ *   xq           [M, K] int8 / e4m3 bytes, out
+ *   s_tok        [M] fp32, out;  s_x  [ceil(K/128), M] fp32, out (one row per
+ *                block, the tokens side by side, as mq_fp8_block_mm reads it)
+ * Requires: 0 <= M < 2^22; 16 <= K <= 65536, K % 16 == 0; 0 <= eps <= 1 (else
+ * MQ_ERR_UNSUPPORTED); 16-byte aligned pointers (scales 4-byte). Inputs, and
+ * the sums h, must be finite. _bf16: x, residual, weight and h are bf16.
+ */
+mq_status mq_rmsnorm_int8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, double eps, uint16_t* h,
+                          int8_t* xq, float* s_tok, int64_t M, int64_t K, void* stream);
+mq_status mq_rmsnorm_int8_bf16(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, double eps,
+                               uint16_t* h, int8_t* xq, float* s_tok, int64_t M, int64_t K, void* stream);
+mq_status mq_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, double eps, uint16_t* h,
+                         uint8_t* xq, float* s_x, int64_t M, int64_t K, void* stream);
+mq_status mq_rmsnorm_fp8_bf16(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, double eps,
+                              uint16_t* h, uint8_t* xq, float* s_x, int64_t M, int64_t K, void* stream);
+
+/*
+ * FP8 linear layer: e4m3 codes with one binary32 scale per block of 128.
+ * The third 8-bit scheme beside W8A8_INT8; the pages name the runtime's
+ * schemes but give no fp8 layout, so this is the common one: activations
+ * scaled per token and 128 values of K, weights per 128 x 128 tile.
+ *
+ * mq_quant_fp8_blocks: xq and s_x of x as in mq_rmsnorm_fp8 with v = x.
+ * mq_fp8_block_mm: with block b = k / 128,
+ *     y[m,n] = fp16_rne( sum_b fl32(s_x[b,m] * s_w[n/128,b]) * (sum_{k in b} xq[m,k] * wq[n,k]) )
+ *   in binary32, but for the fp8 matrix unit's own sum of 8 neighbouring
+ *   products, which drops what lies below 2^-13 of the largest of them. The
+ *   blocks are added in order, in a fixed number of contiguous ranges:
+ *   deterministic.
+ * mq_fp8_linear: mq_quant_fp8_blocks, then mq_fp8_block_mm, bit for bit; codes
+ *   and scales in `workspace`.
+ *
+ *   x     [M, K] fp16   in
+ *   xq    [M, K] e4m3 bytes;  s_x [ceil(K/128), M] fp32
+ *   wq    [N, K] e4m3 bytes, in (one row per output channel)
+ *   s_w   [ceil(N/128), ceil(K/128)] fp32, in
+ *   y     [M, N] fp16   out
+ *   workspace  >= mq_fp8_linear_workspace_bytes(M, K) bytes, 16-byte aligned,
+ *              not overlapping any operand; contents on entry do not matter;
+ *              calls sharing it must be ordered.
+ * Requires: 0 <= M, N <= 2^26, M * N <= 2^36; 16 <= K <= 2^20, K % 16 == 0;
+ * the quantizer M * ceil(K/128) < 2^27; x, xq, wq, y 16-byte aligned; scales
+ * 4-byte. N need not be a multiple of anything. Codes must not be NaN. _bf16:
+ * x and y are bf16.
+ */
+mq_status mq_quant_fp8_blocks(const uint16_t* x, uint8_t* xq, float* s_x, int64_t M, int64_t K, void* stream);
+mq_status mq_quant_fp8_blocks_bf16(const uint16_t* x, uint8_t* xq, float* s_x, int64_t M, int64_t K, void* stream);
+mq_status mq_fp8_block_mm(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
+                          int64_t M, int64_t N, int64_t K, void* stream);
+mq_status mq_fp8_block_mm_bf16(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
+                               int64_t M, int64_t N, int64_t K, void* stream);
+size_t mq_fp8_linear_workspace_bytes(int64_t M, int64_t K);
+mq_status mq_fp8_linear(const uint16_t* x, const uint8_t* wq, const float* s_w, uint16_t* y, int64_t M, int64_t N,
+                        int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* s_w, uint16_t* y, int64_t M, int64_t N,
+                             int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Checkpoint-layout adapter: one-time conversions of 4-bit checkpoint
  * tensors into the layouts above.
  * Source: the LMDeploy overview (sections 4.1 and 5.5) loads 4-bit

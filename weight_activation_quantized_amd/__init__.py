@@ -24,19 +24,26 @@ Entry points (same names as the C ABI, without the ``mq_`` prefix):
 
     kv_quant(x, bits)                                -> (codes, params) per (token, head) row
 
+    rmsnorm_int8(x, weight, eps, residual)           -> (xq, s_tok[, h]): RMS norm of x (+ residual), int8 per token
+    rmsnorm_fp8(x, weight, eps, residual)            -> (xq, s_x[, h]): the same, e4m3 with a scale per 128 values
+    quant_fp8_blocks(x)                              -> (xq, s_x): e4m3 codes, s_x [ceil(K/128), M]
+    fp8_block_mm(xq, s_x, wq, s_w)                   -> y (fp16, or bf16 with out_dtype)
+
     int4_reorder(words, order)                       -> words in the library's field order
     int4_transpose(words, order)                     -> [B, A/8] from a 4-bit [A, B] packed along B
     u16_transpose(scales)                            -> [B, A] (fp16 scales [N, K/G] -> [K/G, N])
 
-and two compositions used by a model's linear layer:
+and the compositions used by a model's linear layer:
 
     w4a16_linear(x, qweight, scales, qzeros, group)  GEMV for M <= 64 (decode layout if qweight_blocked
                                                      is given), else GEMM
     w8a8_linear(x, wq, s_ch)                         quantize x (fp16 or bf16) per token, then scaled GEMM
                                                      (one fused kernel for 1-4 tokens, see mq.h; a workspace otherwise)
     w8a8_linear_noalloc(x, wq, s_ch)                 the same (fp16) with the library's own scratch: no allocation
+    fp8_linear(x, wq, s_w)                           e4m3 codes of x per 128 values, then the block-scaled product
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -49,6 +56,7 @@ __all__ = [
     "w8a8_linear_workspace_bytes", "w4a16_gemm_workspace_bytes", "kv_quant",
     "AWQ_FIELD_ORDER", "int4_reorder", "int4_transpose", "u16_transpose",
     "w8a8_linear_noalloc", "NOALLOC_SCRATCH_BYTES",
+    "rmsnorm_int8", "rmsnorm_fp8", "quant_fp8_blocks", "fp8_block_mm", "fp8_linear", "fp8_linear_workspace_bytes",
 ]
 
 # The in-tree build; MQ_LIBRARY names another build of the same library (for
@@ -76,6 +84,7 @@ _lib = None
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_RMSNORM = [_P, _P, _P, ctypes.c_double, _P, _P, _P, _I64, _I64, _P]
 _PROTOTYPES = {
     "mq_abi_version": (ctypes.c_int, []),
     "mq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -106,6 +115,17 @@ _PROTOTYPES = {
     "mq_w4a16_gemv_bf16": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
     "mq_w4a16_gemv_blocked_bf16": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P,
                                                   ctypes.c_size_t, _P]),
+    "mq_rmsnorm_int8": (ctypes.c_int, _RMSNORM),
+    "mq_rmsnorm_int8_bf16": (ctypes.c_int, _RMSNORM),
+    "mq_rmsnorm_fp8": (ctypes.c_int, _RMSNORM),
+    "mq_rmsnorm_fp8_bf16": (ctypes.c_int, _RMSNORM),
+    "mq_quant_fp8_blocks": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _P]),
+    "mq_quant_fp8_blocks_bf16": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _P]),
+    "mq_fp8_block_mm": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "mq_fp8_block_mm_bf16": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "mq_fp8_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "mq_fp8_linear": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
+    "mq_fp8_linear_bf16": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
 }
 
 
@@ -153,6 +173,12 @@ def _dev_tensor(t, name, dtype, ndim):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
+
+
+def _same_device(first, *rest):
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one call takes one GPU's")
 
 
 def _stream_of(t, stream):
@@ -457,6 +483,157 @@ def kv_quant(x, bits=8, codes=None, params=None, stream=None):
         fn = library().mq_kv_quant_bf16 if x.dtype == torch.bfloat16 else library().mq_kv_quant
         _check(fn(x.data_ptr(), codes.data_ptr(), params.data_ptr(), rows, D, bits, _stream_of(x, stream)))
     return codes, params
+
+
+def _scope(t, stream):
+    """Where a call's outputs and workspace are allocated and its kernels are
+    launched: the given stream (memory from its own pool), else the current
+    stream of t's GPU."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream on {stream.device}, tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() == t.device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _rmsnorm(x, weight, eps, residual, out, s_out, h_out, stream, fp8):
+    torch = _torch()
+    dt = _half_dtype(x, "x")
+    _dev_tensor(x, "x", dt, 2)
+    _dev_tensor(weight, "weight", dt, 1)
+    M, K = x.shape
+    if weight.shape[0] != K:
+        raise ValueError("weight must be [K]")
+    if residual is not None:
+        _dev_tensor(residual, "residual", dt, 2)
+        if residual.shape != x.shape:
+            raise ValueError("residual must have x's shape")
+    elif h_out is not None:
+        raise ValueError("h_out needs a residual")
+    lib, bf = library(), dt == torch.bfloat16
+    if fp8:
+        fn = lib.mq_rmsnorm_fp8_bf16 if bf else lib.mq_rmsnorm_fp8
+    else:
+        fn = lib.mq_rmsnorm_int8_bf16 if bf else lib.mq_rmsnorm_int8
+    with _scope(x, stream):
+        xq = _out(out, (M, K), torch.float8_e4m3fn if fp8 else torch.int8, x, "out")
+        s = _out(s_out, (_blocks(K), M) if fp8 else (M,), torch.float32, x, "s_out")
+        h, rp, hp = None, None, None
+        if residual is not None:
+            h = _out(h_out, (M, K), dt, x, "h_out")
+            rp, hp = residual.data_ptr(), h.data_ptr()
+        _same_device(x, weight, residual, xq, s, h)
+        _check(fn(x.data_ptr(), rp, weight.data_ptr(), eps, hp, xq.data_ptr(), s.data_ptr(), M, K,
+                  _stream_of(x, stream)))
+    return (xq, s) if residual is None else (xq, s, h)
+
+
+def rmsnorm_int8(x, weight, eps=1e-6, residual=None, out=None, s_out=None, h_out=None, stream=None):
+    """RMS norm of x (+ residual) [M, K] with int8 codes per token, the input
+    of ``w8a8_scaled_mm``: (xq int8 [M, K], s_tok fp32 [M]) and, with a
+    residual, h = x + residual in x's dtype (``h_out=residual`` updates the
+    residual stream in place)."""
+    return _rmsnorm(x, weight, eps, residual, out, s_out, h_out, stream, False)
+
+
+def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, out=None, s_out=None, h_out=None, stream=None):
+    """RMS norm of x (+ residual) [M, K] with e4m3 codes and a scale per 128
+    values, the input of ``fp8_block_mm``: (xq float8_e4m3fn [M, K], s_x fp32
+    [ceil(K/128), M]) and, with a residual, h as in ``rmsnorm_int8``."""
+    return _rmsnorm(x, weight, eps, residual, out, s_out, h_out, stream, True)
+
+
+def quant_fp8_blocks(x, out=None, s_out=None, stream=None):
+    """e4m3 codes of fp16 or bf16 x [M, K] with a scale per token and 128
+    values: (xq float8_e4m3fn [M, K], s_x fp32 [ceil(K/128), M])."""
+    torch = _torch()
+    dt = _half_dtype(x, "x")
+    _dev_tensor(x, "x", dt, 2)
+    M, K = x.shape
+    fn = library().mq_quant_fp8_blocks_bf16 if dt == torch.bfloat16 else library().mq_quant_fp8_blocks
+    with _scope(x, stream):
+        xq = _out(out, (M, K), torch.float8_e4m3fn, x, "out")
+        s = _out(s_out, (_blocks(K), M), torch.float32, x, "s_out")
+        _same_device(x, xq, s)
+        _check(fn(x.data_ptr(), xq.data_ptr(), s.data_ptr(), M, K, _stream_of(x, stream)))
+    return xq, s
+
+
+def _fp8_weights(wq, s_w, K):
+    torch = _torch()
+    _dev_tensor(wq, "wq", torch.float8_e4m3fn, 2)
+    _dev_tensor(s_w, "s_w", torch.float32, 2)
+    N = wq.shape[0]
+    if wq.shape[1] != K or tuple(s_w.shape) != (_blocks(N), _blocks(K)):
+        raise ValueError("wq must be [N, K] and s_w [ceil(N/128), ceil(K/128)]")
+    return N
+
+
+def fp8_block_mm(xq, s_x, wq, s_w, out=None, stream=None, out_dtype=None):
+    """y[M, N] = xq[M, K] . wq[N, K]^T, both e4m3 with a scale per block of 128
+    (s_x [ceil(K/128), M], s_w [ceil(N/128), ceil(K/128)]), in fp16 (default)
+    or bf16 (``out_dtype=torch.bfloat16``, or a bf16 ``out``)."""
+    torch = _torch()
+    _dev_tensor(xq, "xq", torch.float8_e4m3fn, 2)
+    _dev_tensor(s_x, "s_x", torch.float32, 2)
+    M, K = xq.shape
+    if tuple(s_x.shape) != (_blocks(K), M):
+        raise ValueError("s_x must be [ceil(K/128), M]")
+    N = _fp8_weights(wq, s_w, K)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.float16
+    if out_dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("out_dtype must be float16 or bfloat16")
+    fn = library().mq_fp8_block_mm_bf16 if out_dtype == torch.bfloat16 else library().mq_fp8_block_mm
+    with _scope(xq, stream):
+        y = _out(out, (M, N), out_dtype, xq, "out")
+        _same_device(xq, s_x, wq, s_w, y)
+        _check(fn(xq.data_ptr(), s_x.data_ptr(), wq.data_ptr(), s_w.data_ptr(), y.data_ptr(), M, N, K,
+                  _stream_of(xq, stream)))
+    return y
+
+
+def _workspace(workspace, need, like):
+    """(pointer, bytes, tensor) of the caller's workspace, or of a fresh one."""
+    torch = _torch()
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    if workspace is None:
+        return None, 0, None
+    if not isinstance(workspace, torch.Tensor) or workspace.device.type != "cuda" or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def fp8_linear_workspace_bytes(M, K):
+    """Workspace bytes ``fp8_linear`` needs (codes and scales of x)."""
+    return int(library().mq_fp8_linear_workspace_bytes(M, K))
+
+
+def fp8_linear(x, wq, s_w, out=None, workspace=None, stream=None):
+    """FP8 linear layer from fp16 or bf16 x (y in x's dtype): e4m3 codes of x
+    per 128 values, then the block-scaled product. Bit-identical to
+    ``fp8_block_mm(*quant_fp8_blocks(x), wq, s_w, out_dtype=x.dtype)``."""
+    torch = _torch()
+    dt = _half_dtype(x, "x")
+    _dev_tensor(x, "x", dt, 2)
+    M, K = x.shape
+    N = _fp8_weights(wq, s_w, K)
+    fn = library().mq_fp8_linear_bf16 if dt == torch.bfloat16 else library().mq_fp8_linear
+    with _scope(x, stream):
+        y = _out(out, (M, N), dt, x, "out")
+        ws_ptr, ws_bytes, workspace = _workspace(workspace, fp8_linear_workspace_bytes(M, K), x)
+        _same_device(x, wq, s_w, y, workspace)
+        _check(fn(x.data_ptr(), wq.data_ptr(), s_w.data_ptr(), y.data_ptr(), M, N, K, ws_ptr, ws_bytes,
+                  _stream_of(x, stream)))
+    return y
 
 
 # Field order of AWQ-style checkpoint words: field j holds element

@@ -23,7 +23,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["mq_api.cpp", "quant_int8.hip", "w8a8_gemm.hip", "w8a8_gemv.hip", "w4a16_gemv.hip",
            "w4a16_gemv_blocked.hip", "w4a16_gemv_blocked_prescaled.hip", "w4a16_gemm.hip", "kv_quant.hip",
-           "int4_layout.hip", "w8a8_noalloc.hip"]
+           "int4_layout.hip", "w8a8_noalloc.hip", "norm_quant.hip", "fp8_block_mm.hip", "fp8_block_gemv.hip"]
 
 ARCH = "gfx950"
 FLAGS = [
@@ -44,8 +44,11 @@ FLAGS = [
 # destination (otherwise they share one AGPR quad and wait on each other's
 # copy-out). The decode-layout GEMV's one-tile kernel reads its per-group
 # sums with VALU operations (no copies out of AGPRs); its kernel for 17-64
-# tokens lives in its own file, built without this flag.
+# tokens lives in its own file, built without this flag. The e4m3 products
+# scale every block's MFMA result with VALU operations.
 SOURCE_FLAGS = {
+    "fp8_block_mm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "fp8_block_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "w4a16_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "w4a16_gemv_blocked.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }

@@ -44,6 +44,28 @@ hipError_t launch_w8a8_gemv_fused(const uint16_t* x, const int8_t* wq, const flo
 constexpr size_t kNoallocScratchBytes = 33816576;  // MQ_NOALLOC_SCRATCH_BYTES
 hipError_t noalloc_scratch(void** ptr);
 
+// RMS norm of x (+ residual, the sum stored in h) [M, K] with 8-bit output:
+// int8 codes and one scale per row, or, when fp8, e4m3 codes and one scale per
+// 128 values, scales [ceil(K / 128), M]. residual and h are NULL together; h
+// may be residual itself. Rows stay in registers: K <= kRmsnormMaxK.
+constexpr int64_t kRmsnormMaxK = 65536;
+hipError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, double eps,
+                                uint16_t* h, uint8_t* codes, float* scales, int64_t M, int64_t K, bool fp8, bool bf16,
+                                hipStream_t stream);
+
+// e4m3 codes [M, K] of x and one scale per 128 values, scales [ceil(K / 128), M].
+hipError_t launch_quant_fp8_blocks(const uint16_t* x, uint8_t* codes, float* scales, int64_t M, int64_t K, bool bf16,
+                                   hipStream_t stream);
+
+// y[M, N] = xq[M, K] . wq[N, K]^T, both e4m3 with scales per block of 128
+// (s_x [ceil(K / 128), M], s_w [ceil(N / 128), ceil(K / 128)]); the decode
+// form for M <= kFp8GemvMaxM.
+constexpr int64_t kFp8GemvMaxM = 64;
+hipError_t launch_fp8_block_mm(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
+                               int64_t M, int64_t N, int64_t K, bool bf16, hipStream_t stream);
+hipError_t launch_fp8_block_gemv(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
+                                 int64_t M, int64_t N, int64_t K, bool bf16, hipStream_t stream);
+
 // Online KV-cache quantization of rows x [rows, head_dim] fp16 to codes
 // (uint8 [rows, head_dim] for 8 bits, packed [rows, head_dim/2] for 4) and
 // params fp32 [rows, 2] = (scale, min); head_dim a power of two in [8, 512];

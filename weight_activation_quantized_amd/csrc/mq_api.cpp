@@ -571,4 +571,178 @@ MQ_W4A16_ENTRY(mq_w4a16_gemv_blocked, w4a16_gemv_blocked_impl, false, qweight_bl
 MQ_W4A16_ENTRY(mq_w4a16_gemv_blocked_bf16, w4a16_gemv_blocked_impl, true, qweight_blocked)
 #undef MQ_W4A16_ENTRY
 
+// ---- RMS norm with 8-bit output, e4m3 codes and product -------------------
+
+static size_t blocks_of(int64_t n) { return static_cast<size_t>((n + 127) / 128); }
+
+static mq_status rmsnorm_impl(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, double eps,
+                              uint16_t* h, void* codes, float* scales, int64_t M, int64_t K, bool fp8, bool bf16,
+                              void* stream) {
+  MQ_TRY(check_mk(M, K, 16, mq::kRmsnormMaxK, 16));
+  if (M >= (int64_t{1} << 22)) return fail(MQ_ERR_SHAPE, "M=%lld must be below 2^22", (long long)M);
+  if (!(eps >= 0.0 && eps <= 1.0)) return fail(MQ_ERR_UNSUPPORTED, "eps=%g must lie in [0, 1]", eps);
+  MQ_TRY(need(x, M * K, "x"));
+  MQ_TRY(need(weight, K, "weight"));
+  MQ_TRY(need(codes, M * K, "xq"));
+  MQ_TRY(need(scales, M, "the scales"));
+  if (M > 0 && (residual == nullptr) != (h == nullptr))
+    return fail(MQ_ERR_NULL, "residual and h are given together or not at all");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(h, 16))
+    return fail(MQ_ERR_ALIGN, "x, residual, weight and h must be 16-byte aligned");
+  if (!aligned(codes, 16)) return fail(MQ_ERR_ALIGN, "xq must be 16-byte aligned");
+  if (!aligned(scales, 4)) return fail(MQ_ERR_ALIGN, "the scales must be 4-byte aligned");
+  const size_t n = static_cast<size_t>(M * K), ns = static_cast<size_t>(M) * (fp8 ? blocks_of(K) : 1) * 4;
+  // h may be the residual itself (each value is read before it is replaced,
+  // by the same lane); any other overlap is an error.
+  const bool in_place = h == residual;
+  const Range in[] = {{x, n * 2, "x"},
+                      {in_place ? nullptr : residual, in_place || residual == nullptr ? 0 : n * 2, "residual"},
+                      {weight, static_cast<size_t>(K) * 2, "weight"}};
+  const Range out[] = {{h, h ? n * 2 : 0, "h"}, {codes, n, "xq"}, {scales, ns, "the scales"}};
+  MQ_TRY(check_alias(in, out));
+  if (M == 0) return ok();
+  return hip_status(mq::launch_rmsnorm_quant(x, residual, weight, eps, h, static_cast<uint8_t*>(codes), scales, M, K, fp8,
+                                             bf16, as_stream(stream)),
+                    "rmsnorm launch");
+}
+
+mq_status mq_rmsnorm_int8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, double eps, uint16_t* h,
+                          int8_t* xq, float* s_tok, int64_t M, int64_t K, void* stream) {
+  return rmsnorm_impl(x, residual, weight, eps, h, xq, s_tok, M, K, false, false, stream);
+}
+
+mq_status mq_rmsnorm_int8_bf16(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, double eps,
+                               uint16_t* h, int8_t* xq, float* s_tok, int64_t M, int64_t K, void* stream) {
+  return rmsnorm_impl(x, residual, weight, eps, h, xq, s_tok, M, K, false, true, stream);
+}
+
+mq_status mq_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, double eps, uint16_t* h,
+                         uint8_t* xq, float* s_x, int64_t M, int64_t K, void* stream) {
+  return rmsnorm_impl(x, residual, weight, eps, h, xq, s_x, M, K, true, false, stream);
+}
+
+mq_status mq_rmsnorm_fp8_bf16(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, double eps,
+                              uint16_t* h, uint8_t* xq, float* s_x, int64_t M, int64_t K, void* stream) {
+  return rmsnorm_impl(x, residual, weight, eps, h, xq, s_x, M, K, true, true, stream);
+}
+
+// one 16-lane group per block of 128: the launch holds 16 M ceil(K / 128) < 2^32 work-items
+static mq_status check_fp8_rows(int64_t M, int64_t K) {
+  MQ_TRY(check_mk(M, K, 16, kMaxK, 16));
+  if (M * static_cast<int64_t>(blocks_of(K)) >= (int64_t{1} << 27))
+    return fail(MQ_ERR_SHAPE, "M * ceil(K / 128) = %lld must be below 2^27", (long long)(M * (int64_t)blocks_of(K)));
+  return MQ_OK;
+}
+
+static mq_status quant_fp8_impl(const uint16_t* x, uint8_t* xq, float* s_x, int64_t M, int64_t K, bool bf16,
+                                void* stream) {
+  MQ_TRY(check_fp8_rows(M, K));
+  MQ_TRY(need(x, M * K, "x"));
+  MQ_TRY(need(xq, M * K, "xq"));
+  MQ_TRY(need(s_x, M, "s_x"));
+  if (!aligned(x, 16) || !aligned(xq, 16)) return fail(MQ_ERR_ALIGN, "x and xq must be 16-byte aligned");
+  if (!aligned(s_x, 4)) return fail(MQ_ERR_ALIGN, "s_x must be 4-byte aligned");
+  const Range in[] = {{x, static_cast<size_t>(M * K) * 2, "x"}};
+  const Range out[] = {{xq, static_cast<size_t>(M * K), "xq"}, {s_x, static_cast<size_t>(M) * blocks_of(K) * 4, "s_x"}};
+  MQ_TRY(check_alias(in, out));
+  if (M == 0) return ok();
+  return hip_status(mq::launch_quant_fp8_blocks(x, xq, s_x, M, K, bf16, as_stream(stream)), "quant_fp8_blocks launch");
+}
+
+mq_status mq_quant_fp8_blocks(const uint16_t* x, uint8_t* xq, float* s_x, int64_t M, int64_t K, void* stream) {
+  return quant_fp8_impl(x, xq, s_x, M, K, false, stream);
+}
+
+mq_status mq_quant_fp8_blocks_bf16(const uint16_t* x, uint8_t* xq, float* s_x, int64_t M, int64_t K, void* stream) {
+  return quant_fp8_impl(x, xq, s_x, M, K, true, stream);
+}
+
+constexpr int64_t kMaxFp8Dim = int64_t{1} << 26;    // M, N of the e4m3 product (launch size)
+constexpr int64_t kMaxFp8Out = int64_t{1} << 36;    // M * N of it
+
+static mq_status check_fp8_mm(int64_t M, int64_t N, int64_t K) {
+  MQ_TRY(check_mk(M, K, 16, kMaxK, 16));
+  if (M > kMaxFp8Dim) return fail(MQ_ERR_SHAPE, "M=%lld out of range", (long long)M);
+  if (N < 0 || N > kMaxFp8Dim) return fail(MQ_ERR_SHAPE, "N=%lld out of range", (long long)N);
+  if (M * N > kMaxFp8Out || K * N > kMaxElems) return fail(MQ_ERR_SHAPE, "problem too large");
+  return MQ_OK;
+}
+
+static mq_status fp8_mm_impl(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
+                             int64_t M, int64_t N, int64_t K, bool bf16, void* stream) {
+  MQ_TRY(check_fp8_mm(M, N, K));
+  MQ_TRY(need(xq, M * K, "xq"));
+  MQ_TRY(need(s_x, M, "s_x"));
+  MQ_TRY(need(wq, N * K, "wq"));
+  MQ_TRY(need(s_w, N, "s_w"));
+  MQ_TRY(need(y, M * N, "y"));
+  if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(y, 16))
+    return fail(MQ_ERR_ALIGN, "xq, wq and y must be 16-byte aligned");
+  if (!aligned(s_x, 4) || !aligned(s_w, 4)) return fail(MQ_ERR_ALIGN, "s_x and s_w must be 4-byte aligned");
+  const Range in[] = {{xq, static_cast<size_t>(M * K), "xq"},
+                      {s_x, static_cast<size_t>(M) * blocks_of(K) * 4, "s_x"},
+                      {wq, static_cast<size_t>(N * K), "wq"},
+                      {s_w, blocks_of(N) * blocks_of(K) * 4, "s_w"}};
+  const Range out[] = {{y, static_cast<size_t>(M * N) * 2, "y"}};
+  MQ_TRY(check_alias(in, out));
+  if (M == 0 || N == 0) return ok();
+  return hip_status(mq::launch_fp8_block_mm(xq, s_x, wq, s_w, y, M, N, K, bf16, as_stream(stream)),
+                    "fp8_block_mm launch");
+}
+
+mq_status mq_fp8_block_mm(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
+                          int64_t M, int64_t N, int64_t K, void* stream) {
+  return fp8_mm_impl(xq, s_x, wq, s_w, y, M, N, K, false, stream);
+}
+
+mq_status mq_fp8_block_mm_bf16(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
+                               int64_t M, int64_t N, int64_t K, void* stream) {
+  return fp8_mm_impl(xq, s_x, wq, s_w, y, M, N, K, true, stream);
+}
+
+size_t mq_fp8_linear_workspace_bytes(int64_t M, int64_t K) {
+  if (M < 1 || M > kMaxFp8Dim || K < 16 || K > kMaxK || K % 16 || M * K > kMaxElems) return 0;
+  return (static_cast<size_t>(M * K) + 255) / 256 * 256 + static_cast<size_t>(M) * blocks_of(K) * 4;
+}
+
+static mq_status fp8_linear_impl(const uint16_t* x, const uint8_t* wq, const float* s_w, uint16_t* y, int64_t M,
+                                 int64_t N, int64_t K, void* workspace, size_t workspace_bytes, bool bf16,
+                                 void* stream) {
+  MQ_TRY(check_fp8_mm(M, N, K));
+  MQ_TRY(check_fp8_rows(M, K));
+  MQ_TRY(need(x, M * K, "x"));
+  MQ_TRY(need(wq, N * K, "wq"));
+  MQ_TRY(need(s_w, N, "s_w"));
+  MQ_TRY(need(y, M * N, "y"));
+  if (!aligned(x, 16) || !aligned(wq, 16) || !aligned(y, 16))
+    return fail(MQ_ERR_ALIGN, "x, wq and y must be 16-byte aligned");
+  if (!aligned(s_w, 4)) return fail(MQ_ERR_ALIGN, "s_w must be 4-byte aligned");
+  const size_t ws = mq_fp8_linear_workspace_bytes(M, K);
+  if (ws > 0 && (!workspace || workspace_bytes < ws))
+    return fail(MQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", ws,
+                workspace ? workspace_bytes : static_cast<size_t>(0));
+  if (!aligned(workspace, 16)) return fail(MQ_ERR_ALIGN, "workspace must be 16-byte aligned");
+  const Range in[] = {{x, static_cast<size_t>(M * K) * 2, "x"},
+                      {wq, static_cast<size_t>(N * K), "wq"},
+                      {s_w, blocks_of(N) * blocks_of(K) * 4, "s_w"}};
+  const Range out[] = {{y, static_cast<size_t>(M * N) * 2, "y"}, {workspace, ws, "workspace"}};
+  MQ_TRY(check_alias(in, out));
+  if (M == 0 || N == 0) return ok();
+  uint8_t* xq = static_cast<uint8_t*>(workspace);
+  float* s_x = reinterpret_cast<float*>(xq + (static_cast<size_t>(M * K) + 255) / 256 * 256);
+  MQ_TRY(hip_status(mq::launch_quant_fp8_blocks(x, xq, s_x, M, K, bf16, as_stream(stream)), "fp8_linear quant launch"));
+  return hip_status(mq::launch_fp8_block_mm(xq, s_x, wq, s_w, y, M, N, K, bf16, as_stream(stream)),
+                    "fp8_linear mm launch");
+}
+
+mq_status mq_fp8_linear(const uint16_t* x, const uint8_t* wq, const float* s_w, uint16_t* y, int64_t M, int64_t N,
+                        int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  return fp8_linear_impl(x, wq, s_w, y, M, N, K, workspace, workspace_bytes, false, stream);
+}
+
+mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* s_w, uint16_t* y, int64_t M, int64_t N,
+                             int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  return fp8_linear_impl(x, wq, s_w, y, M, N, K, workspace, workspace_bytes, true, stream);
+}
+
 }  // extern "C"
