@@ -489,6 +489,89 @@ mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* 
                              int64_t K, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Paged KV cache in e4m3, one scale per page and head: append and attention.
+ * Source: LMDeploy toolkit overview, section 2.4 "KV Cache online
+ * quantization" (the cache is quantized as it is written, without
+ * calibration, and read by the attention). mq_kv_quant above gives rows their
+ * own scale and minimum; here a block of tokens shares one scale, so that the
+ * attention reads codes and little else. Layout (the library's own):
+ *
+ *   k_cache   [num_pages, Hkv, page, D]  e4m3 bytes
+ *   v_cache   [num_pages, Hkv, D, page]  e4m3 bytes (a page's V is transposed)
+ *   k_scales, v_scales  [num_pages, Hkv] fp32
+ *   block_table [B, table_width] int32   page numbers of each sequence, in order
+ *   cu_q      [B + 1] int32   row of each sequence's first new token in k, v, q
+ *                             (ascending; cu_q[B] <= T; rows outside
+ *                             [cu_q[0], cu_q[B]) belong to no sequence)
+ *   kv_lens   [B] int32       tokens of each sequence in the cache, the new
+ *                             ones of this call (its last ones) included
+ * token t of sequence b is row t % page of page block_table[b, t / page].
+ * Sequences' lengths are read on the GPU only, so one captured graph serves
+ * changing lengths; max_q_len (host) must be at least the largest number of
+ * new tokens of a sequence and table_width * page at least the longest
+ * sequence. Sequences may share pages that no call writes to.
+ *
+ * mq_kv8_append writes the new tokens' k and v. For a page with a = largest
+ * |value| among its new tokens (K and V apart, per head):
+ *     s_new = 2^e, the smallest with a <= 448 * 2^e, -100 <= e <= 120
+ *     s     = s_new if the page holds no older token, else max(s_old, s_new)
+ *     new codes    e4m3_rne(clamp(fl32(x / s), -448, 448))
+ *     older codes  unchanged if s = s_old, else e4m3_rne(code * s_old / s)
+ * Bit-exact to that. Bytes of the page that belong to no token yet, and
+ * everything else, stay as they are. Each page written must belong to one
+ * sequence only. A page number outside [0, num_pages), or a token past
+ * table_width * page, is skipped.
+ *
+ * mq_kv8_attention: for every row r of sequence b with n new tokens and every
+ * query head hq (kv head hq * Hkv / Hq), with i = r - cu_q[b] and L = kv_lens[b]:
+ *     out[r, hq] = sum_{t <= L - n + i} p_t v_t,   p = softmax(softmax_scale * q . k_t)
+ * (causal: the new tokens are the last n). A row that sees no key (L = 0, or
+ * fewer tokens cached than new) is 0; rows of no sequence are left as they
+ * are. Keys whose page number is outside [0, num_pages) count for nothing, as
+ * do bytes past a sequence's last token, whatever they hold. Scores, softmax
+ * statistics and sums are binary32, weights (at most 1) are rounded once to
+ * fp16 for the second product, the output once. Scales must lie in
+ * [2^-100, 2^120] (as the append leaves them; V scales are held to that
+ * range), codes of a sequence's tokens must not be NaN, and q must be finite.
+ * Keys of long sequences are split over workgroups, their parts joined by a
+ * second kernel in a fixed order: deterministic.
+ *
+ *   k, v, q   [T, heads, D] fp16, rows `*_stride` values apart (a multiple of
+ *             8, at least heads * D: slices of a fused projection's output)
+ *   out       [T, Hq, D] fp16, dense
+ *   workspace >= mq_kv8_attention_workspace_bytes(...) bytes (0: may be NULL),
+ *             16-byte aligned, overlapping no operand; contents on entry do
+ *             not matter; calls sharing it must be ordered.
+ * Requires: D in {64, 128}, page in {16, 32, 64, 128} (else
+ * MQ_ERR_UNSUPPORTED); 0 <= T <= 2^26; 0 <= B <= 65535; 1 <= Hkv <= Hq <=
+ * 1024, Hq % Hkv == 0; num_pages >= 1; 1 <= table_width * page <= 2^30;
+ * max_q_len >= 1; for the append B * Hkv * (max_q_len / page + 2) below about
+ * 2^23; q, k, v, caches, out 16-byte aligned, the rest 4-byte. _bf16: k, v, q
+ * and out are bf16.
+ */
+mq_status mq_kv8_append(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, uint8_t* k_cache,
+                        uint8_t* v_cache, float* k_scales, float* v_scales, const int32_t* block_table,
+                        const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int64_t B, int64_t Hkv, int64_t D,
+                        int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len, void* stream);
+mq_status mq_kv8_append_bf16(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, uint8_t* k_cache,
+                             uint8_t* v_cache, float* k_scales, float* v_scales, const int32_t* block_table,
+                             const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int64_t B, int64_t Hkv, int64_t D,
+                             int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len, void* stream);
+size_t mq_kv8_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
+                                        int64_t table_width, int64_t max_q_len);
+mq_status mq_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+                           const float* k_scales, const float* v_scales, const int32_t* block_table, const int32_t* cu_q,
+                           const int32_t* kv_lens, uint16_t* out, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                           int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len, float softmax_scale,
+                           void* workspace, size_t workspace_bytes, void* stream);
+mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+                                const float* k_scales, const float* v_scales, const int32_t* block_table,
+                                const int32_t* cu_q, const int32_t* kv_lens, uint16_t* out, int64_t T, int64_t B,
+                                int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t num_pages, int64_t table_width,
+                                int64_t max_q_len, float softmax_scale, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
  * Checkpoint-layout adapter: one-time conversions of 4-bit checkpoint
  * tensors into the layouts above.
  * Source: the LMDeploy overview (sections 4.1 and 5.5) loads 4-bit

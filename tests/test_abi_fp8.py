@@ -85,3 +85,74 @@ def test_wrappers_refuse_before_the_library():
         mq.quant_fp8_blocks(x.float())
     with pytest.raises(TypeError):
         mq.fp8_linear([1], None, None)
+
+
+class Cache:
+    """Arguments of the cache entry points with fake, far-apart addresses."""
+    sizes = dict(T=10, B=3, Hkv=2, D=128, page=16, P=20, width=8, mq=4)
+    at = {n: 0x10_0000_0000 * (i + 20) for i, n in enumerate(
+        ["k", "v", "q", "kc", "vc", "ks", "vs", "table", "cu", "lens", "out", "ws"])}
+
+
+def _append(lib, **kw):
+    a = {**Cache.sizes, **Cache.at, "sk": None, "sv": None, **kw}
+    sk = a["Hkv"] * a["D"] if a["sk"] is None else a["sk"]
+    sv = a["Hkv"] * a["D"] if a["sv"] is None else a["sv"]
+    return lib.mq_kv8_append(a["k"], a["v"], sk, sv, a["kc"], a["vc"], a["ks"], a["vs"], a["table"], a["cu"], a["lens"],
+                             a["T"], a["B"], a["Hkv"], a["D"], a["page"], a["P"], a["width"], a["mq"], None)
+
+
+def _attention(lib, **kw):
+    a = {**Cache.sizes, **Cache.at, "sq": None, "Hq": 8, "scale": 0.1, "n": 1 << 40, **kw}
+    sq = a["Hq"] * a["D"] if a["sq"] is None else a["sq"]
+    return lib.mq_kv8_attention(a["q"], sq, a["kc"], a["vc"], a["ks"], a["vs"], a["table"], a["cu"], a["lens"], a["out"],
+                                a["T"], a["B"], a["Hq"], a["Hkv"], a["D"], a["page"], a["P"], a["width"], a["mq"],
+                                a["scale"], a["ws"], a["n"], None)
+
+
+@pytest.mark.parametrize("call", [_append, _attention])
+def test_kv8_cache_arguments(lib, call):
+    for n in ("kc", "vc", "ks", "vs", "table", "cu", "lens"):
+        assert call(lib, **{n: None}) == NULL, n
+    for D in (0, 32, 96, 256):
+        assert call(lib, D=D) == UNSUP
+    for page in (0, 8, 48, 256):
+        assert call(lib, page=page) == UNSUP
+    assert call(lib, T=-1) == SHAPE and call(lib, T=(1 << 26) + 1) == SHAPE
+    assert call(lib, B=-1) == SHAPE and call(lib, B=65536) == SHAPE
+    assert call(lib, Hkv=0) == SHAPE and call(lib, Hkv=1025) == SHAPE
+    assert call(lib, P=0) == SHAPE and call(lib, width=0) == SHAPE and call(lib, width=(1 << 26) + 1) == SHAPE
+    assert call(lib, mq=0) == SHAPE
+    assert call(lib, kc=Cache.at["kc"] + 8) == ALIGN and call(lib, vc=Cache.at["vc"] + 1) == ALIGN
+    for n in ("ks", "vs", "table", "cu", "lens"):
+        assert call(lib, **{n: Cache.at[n] + 2}) == ALIGN, n
+    assert call(lib, T=0, k=None, v=None, q=None, out=None) == OK and call(lib, B=0, table=None, cu=None, lens=None) == OK
+
+
+def test_kv8_append_arguments(lib):
+    assert _append(lib, k=None) == NULL and _append(lib, v=None) == NULL
+    assert _append(lib, sk=255) == SHAPE and _append(lib, sv=260) == SHAPE and _append(lib, sk=-256) == SHAPE
+    assert _append(lib, k=Cache.at["k"] + 8) == ALIGN and _append(lib, v=Cache.at["v"] + 2) == ALIGN
+    assert _append(lib, k=Cache.at["kc"] + 64) == ALIAS and _append(lib, vc=Cache.at["kc"] + 1024) == ALIAS
+    assert _append(lib, ks=Cache.at["vs"] + 4) == ALIAS and _append(lib, lens=Cache.at["ks"]) == ALIAS
+    # the last row's end reaches the cache through the stride alone
+    assert _append(lib, k=Cache.at["kc"] - 10 * 256 * 2, sk=512) == ALIAS
+    assert _append(lib, B=65535, Hkv=128, D=64, T=1 << 20, mq=1 << 20, width=1) == SHAPE
+
+
+def test_kv8_attention_arguments(lib):
+    ws = lib.mq_kv8_attention_workspace_bytes
+    assert _attention(lib, q=None) == NULL and _attention(lib, out=None) == NULL
+    assert _attention(lib, Hq=7) == SHAPE and _attention(lib, Hq=0) == SHAPE and _attention(lib, Hq=2048) == SHAPE
+    assert _attention(lib, sq=1000) == SHAPE and _attention(lib, q=Cache.at["q"] + 4) == ALIGN
+    assert _attention(lib, scale=float("nan")) == UNSUP and _attention(lib, scale=float("inf")) == UNSUP
+    assert _attention(lib, out=Cache.at["q"] + 512) == ALIAS and _attention(lib, out=Cache.at["kc"]) == ALIAS
+    assert _attention(lib, out=Cache.at["out"] + 8) == ALIGN
+    # a long sequence needs a workspace
+    need = ws(1, 1, 8, 2, 128, 64, 1000, 1)
+    assert need > 0
+    long = dict(T=1, B=1, page=64, width=1000, mq=1)
+    assert _attention(lib, **long, ws=None) == WS and _attention(lib, **long, n=need - 1) == WS
+    assert _attention(lib, **long, ws=Cache.at["ws"] + 8) == ALIGN and _attention(lib, **long, ws=Cache.at["kc"]) == ALIAS
+    assert _attention(lib, **long, ws=Cache.at["out"]) == ALIAS
+    assert ws(1, 1, 7, 2, 128, 64, 1000, 1) == 0 and ws(1, 1, 8, 2, 96, 64, 1000, 1) == 0 and ws(0, 1, 8, 2, 128, 64, 9, 1) == 0

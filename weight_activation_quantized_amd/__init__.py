@@ -28,6 +28,13 @@ Entry points (same names as the C ABI, without the ``mq_`` prefix):
     rmsnorm_fp8(x, weight, eps, residual)            -> (xq, s_x[, h]): the same, e4m3 with a scale per 128 values
     quant_fp8_blocks(x)                              -> (xq, s_x): e4m3 codes, s_x [ceil(K/128), M]
     fp8_block_mm(xq, s_x, wq, s_w)                   -> y (fp16, or bf16 with out_dtype)
+    kv8_append(k, v, <cache>, <batch>, max_q_len)    writes new tokens into the paged e4m3 cache
+    kv8_attention(q, <cache>, <batch>, max_q_len)    -> out [T, Hq, D]: causal attention over that cache
+    kv8_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len) -> int
+
+    (<cache>: k_cache [P, Hkv, page, D] and v_cache [P, Hkv, D, page], e4m3, with
+    k_scales and v_scales [P, Hkv]; <batch>: block_table [B, width], cu_q [B + 1]
+    and kv_lens [B], int32 on the GPU.)
 
     int4_reorder(words, order)                       -> words in the library's field order
     int4_transpose(words, order)                     -> [B, A/8] from a 4-bit [A, B] packed along B
@@ -57,6 +64,7 @@ __all__ = [
     "AWQ_FIELD_ORDER", "int4_reorder", "int4_transpose", "u16_transpose",
     "w8a8_linear_noalloc", "NOALLOC_SCRATCH_BYTES",
     "rmsnorm_int8", "rmsnorm_fp8", "quant_fp8_blocks", "fp8_block_mm", "fp8_linear", "fp8_linear_workspace_bytes",
+    "kv8_append", "kv8_attention", "kv8_attention_workspace_bytes",
 ]
 
 # The in-tree build; MQ_LIBRARY names another build of the same library (for
@@ -85,6 +93,8 @@ _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _RMSNORM = [_P, _P, _P, ctypes.c_double, _P, _P, _P, _I64, _I64, _P]
+_KV8_APPEND = [_P, _P, _I64, _I64] + [_P] * 7 + [_I64] * 8 + [_P]
+_KV8_ATTENTION = [_P, _I64] + [_P] * 8 + [_I64] * 9 + [ctypes.c_float, _P, ctypes.c_size_t, _P]
 _PROTOTYPES = {
     "mq_abi_version": (ctypes.c_int, []),
     "mq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -125,6 +135,11 @@ _PROTOTYPES = {
     "mq_fp8_block_mm_bf16": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
     "mq_fp8_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "mq_fp8_linear": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
+    "mq_kv8_append": (ctypes.c_int, _KV8_APPEND),
+    "mq_kv8_append_bf16": (ctypes.c_int, _KV8_APPEND),
+    "mq_kv8_attention_workspace_bytes": (ctypes.c_size_t, [_I64] * 8),
+    "mq_kv8_attention": (ctypes.c_int, _KV8_ATTENTION),
+    "mq_kv8_attention_bf16": (ctypes.c_int, _KV8_ATTENTION),
     "mq_fp8_linear_bf16": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
 }
 
@@ -634,6 +649,96 @@ def fp8_linear(x, wq, s_w, out=None, workspace=None, stream=None):
         _check(fn(x.data_ptr(), wq.data_ptr(), s_w.data_ptr(), y.data_ptr(), M, N, K, ws_ptr, ws_bytes,
                   _stream_of(x, stream)))
     return y
+
+
+def _kv8_rows(t, name, dtype, D):
+    """Rows [T, heads, D] of a 16-bit tensor, dense within a row: their stride in values."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU (got {t.device})")
+    if t.dim() != 3 or t.shape[2] != D:
+        raise ValueError(f"{name} must be [T, heads, {D}] (got shape {tuple(t.shape)})")
+    T, H, _ = t.shape
+    if T == 0:
+        return H * D
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: a token's heads must lie side by side (strides {t.stride()})")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens):
+    torch = _torch()
+    _dev_tensor(k_cache, "k_cache", torch.float8_e4m3fn, 4)
+    _dev_tensor(v_cache, "v_cache", torch.float8_e4m3fn, 4)
+    _dev_tensor(k_scales, "k_scales", torch.float32, 2)
+    _dev_tensor(v_scales, "v_scales", torch.float32, 2)
+    _dev_tensor(block_table, "block_table", torch.int32, 2)
+    _dev_tensor(cu_q, "cu_q", torch.int32, 1)
+    _dev_tensor(kv_lens, "kv_lens", torch.int32, 1)
+    P, H, page, D = k_cache.shape
+    if tuple(v_cache.shape) != (P, H, D, page):
+        raise ValueError("k_cache must be [P, Hkv, page, D] and v_cache [P, Hkv, D, page]")
+    if tuple(k_scales.shape) != (P, H) or tuple(v_scales.shape) != (P, H):
+        raise ValueError("k_scales and v_scales must be [P, Hkv]")
+    B, width = block_table.shape
+    if cu_q.shape[0] != B + 1 or kv_lens.shape[0] != B:
+        raise ValueError("cu_q must be [B + 1] and kv_lens [B] for block_table [B, width]")
+    _same_device(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens)
+    pointers = (k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr())
+    return P, H, page, D, B, width, pointers
+
+
+def kv8_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, stream=None):
+    """Write the new tokens k, v [T, Hkv, D] (fp16 or bf16, rows may be slices
+    of a wider tensor) into the paged e4m3 cache: k_cache [P, Hkv, page, D],
+    v_cache [P, Hkv, D, page], scales [P, Hkv], all updated in place. Sequence
+    b's rows are cu_q[b] .. cu_q[b + 1]; kv_lens[b] counts its tokens with
+    them; block_table[b] names its pages."""
+    dt = _half_dtype(k, "k")
+    P, H, page, D, B, width, pointers = _kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens)
+    ks, vs = _kv8_rows(k, "k", dt, D), _kv8_rows(v, "v", dt, D)
+    if k.shape != v.shape or k.shape[1] != H:
+        raise ValueError("k and v must be [T, Hkv, D]")
+    _same_device(k_cache, k, v)
+    bf = dt == _torch().bfloat16
+    fn = library().mq_kv8_append_bf16 if bf else library().mq_kv8_append
+    with _scope(k_cache, stream):
+        _check(fn(k.data_ptr(), v.data_ptr(), ks, vs, *pointers, k.shape[0], B, H, D, page, P, width, max_q_len,
+                  _stream_of(k_cache, stream)))
+
+
+def kv8_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len):
+    """Workspace bytes ``kv8_attention`` needs (0 if none)."""
+    return int(library().mq_kv8_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len))
+
+
+def kv8_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, softmax_scale=None,
+                  out=None, workspace=None, stream=None):
+    """Causal attention of q [T, Hq, D] (fp16 or bf16, rows may be slices of a
+    wider tensor) over the cache of ``kv8_append`` -> out [T, Hq, D] in q's
+    dtype: a sequence's rows are its last tokens, each sees the keys up to its
+    own. ``softmax_scale`` defaults to D ** -0.5. Rows of no sequence are left
+    as they are (unset in a fresh ``out``)."""
+    torch = _torch()
+    dt = _half_dtype(q, "q")
+    P, H, page, D, B, width, pointers = _kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens)
+    qs = _kv8_rows(q, "q", dt, D)
+    T, Hq = q.shape[0], q.shape[1]
+    if softmax_scale is None:
+        softmax_scale = D ** -0.5
+    lib = library()
+    fn = lib.mq_kv8_attention_bf16 if dt == torch.bfloat16 else lib.mq_kv8_attention
+    with _scope(q, stream):
+        o = _out(out, (T, Hq, D), dt, q, "out")
+        need = kv8_attention_workspace_bytes(T, B, Hq, H, D, page, width, max_q_len)
+        ws_ptr, ws_bytes, workspace = _workspace(workspace, need, q)
+        _same_device(q, k_cache, o, workspace)
+        _check(fn(q.data_ptr(), qs, *pointers, o.data_ptr(), T, B, Hq, H, D, page, P, width, max_q_len, softmax_scale,
+                  ws_ptr, ws_bytes, _stream_of(q, stream)))
+    return o
 
 
 # Field order of AWQ-style checkpoint words: field j holds element

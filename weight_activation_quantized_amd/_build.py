@@ -23,7 +23,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["mq_api.cpp", "quant_int8.hip", "w8a8_gemm.hip", "w8a8_gemv.hip", "w4a16_gemv.hip",
            "w4a16_gemv_blocked.hip", "w4a16_gemv_blocked_prescaled.hip", "w4a16_gemm.hip", "kv_quant.hip",
-           "int4_layout.hip", "w8a8_noalloc.hip", "norm_quant.hip", "fp8_block_mm.hip", "fp8_block_gemv.hip"]
+           "int4_layout.hip", "w8a8_noalloc.hip", "norm_quant.hip", "fp8_block_mm.hip", "fp8_block_gemv.hip",
+           "kv8_append.hip", "kv8_attention.hip"]
 
 ARCH = "gfx950"
 FLAGS = [
@@ -45,9 +46,11 @@ FLAGS = [
 # copy-out). The decode-layout GEMV's one-tile kernel reads its per-group
 # sums with VALU operations (no copies out of AGPRs); its kernel for 17-64
 # tokens lives in its own file, built without this flag. The e4m3 products
-# scale every block's MFMA result with VALU operations.
+# scale every block's MFMA result with VALU operations, and the attention's
+# scores and sums are VALU operands too.
 SOURCE_FLAGS = {
     "fp8_block_mm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    "kv8_attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "fp8_block_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "w4a16_gemv.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
     "w4a16_gemv_blocked.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],

@@ -1,0 +1,670 @@
+// Causal attention over the paged e4m3 KV cache, for gfx950: single new tokens
+// (decode) and prompts.
+//
+//   o[row] = sum_t p_t v_t,  p = softmax over the keys t <= position of the row
+//   of softmax_scale * (q . k_t),  k_t = code * k_scale(page, head), v_t likewise
+//
+// Both forms compute S^T = K Q^T and O^T = V^T P^T: a lane of the result then
+// holds one query row (its maximum and sum are lane values), and S^T's
+// registers are, as they stand, the B operand of the second product. That
+// needs two free choices. Which token a row of the K tile is can be chosen
+// (each lane just reads another row of the page), and it is chosen so that a
+// lane's scores belong to consecutive tokens. And V pages are stored
+// transposed, so that the 8 or 16 consecutive tokens of one dimension that a
+// lane needs are one load.
+//
+// Codes are widened exactly: K to the type of q, V to fp16. Scores and their
+// statistics are binary32. The page's V scale joins the exponent: with
+//   x_t = score_t log2(e) + log2(v_scale_t),   m = max x_t,   w_t = 2^(x_t - m) <= 1
+// the second product is sum w_t code_t in units of 2^m whatever the scales of
+// the pages are, and the sum of the weights is sum w_t / v_scale_t. w is
+// rounded once, to fp16 (11 bits; bf16 would lose three more and gains
+// nothing, as w <= 1).
+//
+// Keys that a row does not see get the weight 0 by a select, and V codes
+// behind the last token are cleared, so whatever a page holds there (NaN codes
+// too) counts for nothing; so do pages whose number is not one of the pool's.
+// A row that sees no key is 0.
+#include "device_common.h"
+#include "launch.h"
+
+namespace mq {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kNegInf = -__builtin_inff();
+// Scales outside what the append writes would carry sums out of binary32.
+constexpr float kMinScale = 0x1p-100f, kMaxScale = 0x1p120f;
+
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+// 8 e4m3 codes as 8 fp16 or bf16 values (exact).
+template <bool kBf16>
+__device__ __forceinline__ f16x8 widen(uint32_t lo, uint32_t hi) {
+  if constexpr (kBf16) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+    const u32x4 w = {__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
+                     __builtin_bit_cast(uint32_t, d)};
+    return __builtin_bit_cast(f16x8, w);
+  } else {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false);
+    const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true);
+    return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  }
+}
+
+__device__ __forceinline__ f16x8 to_f16(f32x8 v) { return __builtin_convertvector(v, f16x8); }
+
+// 16 codes of which only the first n count: the others become 0.
+__device__ __forceinline__ u32x4 first_bytes(u32x4 v, int n) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int k = n - 4 * w;
+    v[w] = k >= 4 ? v[w] : k <= 0 ? 0u : v[w] & ((1u << (8 * k)) - 1u);
+  }
+  return v;
+}
+
+__device__ __forceinline__ float held_scale(float s) { return fminf(fmaxf(s, kMinScale), kMaxScale); }
+
+// A sequence as the kernels see it.
+struct Seq {
+  int row0, n, len, seen;  // first row, new tokens, tokens, tokens that the table can hold
+};
+
+__device__ __forceinline__ Seq sequence(const Kv8Cache& c, int b) {
+  Seq s;
+  s.row0 = max(c.cu[b], 0);
+  s.n = max(min(min(c.cu[b + 1], c.tokens) - s.row0, c.max_q_len), 0);
+  s.len = c.lens[b];
+  s.seen = static_cast<int>(min(static_cast<int64_t>(max(s.len, 0)), static_cast<int64_t>(c.table_width) * c.page));
+  return s;
+}
+
+// Tiles of 64 keys that split `z` of `splits` takes of a sequence: [first,
+// first + count). Every split gets the same number, at least `least`.
+struct Span {
+  int first, end;
+};
+__device__ __forceinline__ Span tiles_of(int tiles, int splits, int z, int least) {
+  const int per = max((tiles + splits - 1) / splits, least);
+  Span s;
+  s.first = min(static_cast<int>(min(static_cast<int64_t>(z) * per, static_cast<int64_t>(tiles))), tiles);
+  s.end = min(s.first + per, tiles);
+  return s;
+}
+
+// The workspace of a split call: for every split and row (token, head) its
+// maximum and sum, then its unnormalised output.
+struct Parts {
+  float* ml;  // [splits, rows, 2]
+  float* o;   // [splits, rows, head_dim]
+};
+
+// ---------------------------------------------------------------------------
+// Decode: the rows of one kv head (its query heads times the new tokens) stand
+// in tiles of 16. A workgroup of four wavefronts takes one such tile and a
+// range of keys, a wavefront every fourth tile of 64 keys. Bound by the cache
+// read: K and V go from memory straight into registers (16-byte loads, whole
+// 64-byte pieces of a page row), K of the next tile is requested as soon as
+// this tile's scores are formed, V as soon as its product is, and several
+// wavefronts per SIMD keep the loads of a compute unit outstanding.
+// v_mfma_16x16x32: lane (i = lane % 16, h = lane / 16). Row i of K tile j is
+// token 16 (i / 4) + 4 j + i % 4, so lane (i, h) ends up with the scores of
+// row i of Q for tokens 16 h .. 16 h + 15, in order.
+// ---------------------------------------------------------------------------
+
+template <int D, bool kBf16>
+__global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint16_t* __restrict__ q, int64_t q_stride,
+                                                         uint16_t* __restrict__ out, Parts parts, int group,
+                                                         int row_tiles, int splits, float scale_log2) {
+  constexpr int kKs = D / 32, kDt = D / 16;  // k-steps of a score, 16-dimension tiles of the output
+  __shared__ float so[4][16][D + 4];
+  __shared__ float sm[4][16], sl[4][16];
+
+  const int split = static_cast<int>(blockIdx.x) % splits;
+  const int head = static_cast<int>(blockIdx.y) % c.kv_heads, rt = static_cast<int>(blockIdx.y) / c.kv_heads;
+  const int b = static_cast<int>(blockIdx.z);
+  const Seq seq = sequence(c, b);
+  const int rows = seq.n * group;
+  if (16 * rt >= rows) return;  // uniform: the whole workgroup leaves
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, h = lane >> 4;
+  const int heads = c.kv_heads * group;
+
+  // This lane's query row: token tq of the sequence, head g of the group.
+  const int r = 16 * rt + i;
+  const bool live = r < rows;
+  const int tq = live ? r / group : 0, g = live ? r - tq * group : 0;
+  const int limit = live ? min(seq.len - seq.n + tq, seq.seen - 1) : -1;  // last key the row sees
+  const uint16_t* const qrow = q + static_cast<int64_t>(seq.row0 + tq) * q_stride + (head * group + g) * D;
+  f16x8 qf[kKs];
+#pragma unroll
+  for (int ks = 0; ks < kKs; ++ks) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (live) v = *reinterpret_cast<const u32x4*>(qrow + 64 * (ks / 2) + 16 * h + 8 * (ks % 2));
+    qf[ks] = __builtin_bit_cast(f16x8, v);
+  }
+
+  // Keys that some row of this tile sees, in tiles of 64, and this split's.
+  const int last_t = min(16 * rt + 15, rows - 1) / group;
+  const int top = min(seq.len - seq.n + last_t, seq.seen - 1);  // the row tile's last key
+  const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, 4);
+  const int32_t* const table = c.table + static_cast<size_t>(b) * c.table_width;
+
+  f32x4 o[kDt];
+#pragma unroll
+  for (int d = 0; d < kDt; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = kNegInf, l = 0.f;
+
+  // Lane (i, h) reads K rows of the 16 tokens with i / 4 and V of those with h;
+  // 16 tokens lie within one page. Where there is no page (behind the last
+  // key, or its number is not one of the pool's) page 0 is read and counts for
+  // nothing. Page numbers are requested a tile before the codes they lead to.
+  auto page_id = [&](int tile, int part) {
+    const int t = 64 * tile + 16 * part;
+    return tile < span.end && t <= top ? table[t >> c.page_shift] : -1;
+  };
+  auto known = [&](int id) { return id >= 0 && id < c.num_pages; };
+  auto load_k = [&](int tile, int id, u32x4 (&kc)[4][kKs / 2]) {
+    const int at = ((64 * tile + 16 * (i >> 2)) & (c.page - 1)) + (i & 3);
+    const uint8_t* const base =
+        c.k + ((static_cast<size_t>(known(id) ? id : 0) * c.kv_heads + head) * c.page + at) * D + 16 * h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int x = 0; x < kKs / 2; ++x)
+        kc[j][x] = *reinterpret_cast<const u32x4*>(base + 4 * j * D + 64 * x);
+  };
+  auto load_v = [&](int tile, int id, u32x4 (&vc)[kDt]) {
+    const int at = (64 * tile + 16 * h) & (c.page - 1);
+    const uint8_t* const base =
+        c.v + ((static_cast<size_t>(known(id) ? id : 0) * c.kv_heads + head) * D + i) * c.page + at;
+#pragma unroll
+    for (int d = 0; d < kDt; ++d) vc[d] = *reinterpret_cast<const u32x4*>(base + static_cast<size_t>(16 * d) * c.page);
+  };
+
+  u32x4 kc[4][kKs / 2], vc[kDt];
+  int tile = span.first + wave;
+  int kid = page_id(tile, i >> 2), vid = page_id(tile, h);            // this tile's pages
+  int kid1 = page_id(tile + 4, i >> 2), vid1 = page_id(tile + 4, h);  // and the next one's
+  float ksc = 0.f, vsc = 1.f;
+  if (tile < span.end) {
+    load_k(tile, kid, kc);
+    const size_t unit = static_cast<size_t>(known(vid) ? vid : 0) * c.kv_heads + head;
+    ksc = c.k_scales[unit];
+    vsc = c.v_scales[unit];
+    load_v(tile, vid, vc);
+  }
+  for (; tile < span.end; tile += 4) {
+    const int kid2 = page_id(tile + 8, i >> 2), vid2 = page_id(tile + 8, h);
+    f32x4 s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int ks = 0; ks < kKs; ++ks) {
+        const u32x4 w = kc[j][ks / 2];
+        const f16x8 kf = ks % 2 ? widen<kBf16>(w[2], w[3]) : widen<kBf16>(w[0], w[1]);
+        s[j] = mfma_16x16x32<kBf16>(kf, qf[ks], s[j]);
+      }
+    }
+    const bool more = tile + 4 < span.end;
+    if (more) load_k(tile + 4, kid1, kc);
+    const float vs = held_scale(vsc);
+    const float f = ksc * scale_log2, lv = __builtin_amdgcn_logf(vs), iv = 1.f / vs;
+    float nks = 0.f, nvs = 1.f;
+    if (more) {
+      const size_t unit = static_cast<size_t>(known(vid1) ? vid1 : 0) * c.kv_heads + head;
+      nks = c.k_scales[unit];
+      nvs = c.v_scales[unit];
+    }
+
+    // Tokens 64 tile + 16 h + 4 j + e of this lane: seen up to `limit`.
+    const int t0 = 64 * tile + 16 * h;
+    const int see = known(vid) ? limit - t0 : -1;
+    float x[16];
+    float mt = kNegInf;
+    if (__any(see < 15)) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e] = e <= see ? fmaf(s[e / 4][e % 4], f, lv) : kNegInf;
+        mt = fmaxf(mt, x[e]);
+      }
+      const int count = known(vid) ? top - t0 + 1 : 0;
+#pragma unroll
+      for (int d = 0; d < kDt; ++d) vc[d] = first_bytes(vc[d], count);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e] = fmaf(s[e / 4][e % 4], f, lv);
+        mt = fmaxf(mt, x[e]);
+      }
+    }
+    mt = fmaxf(mt, __shfl_xor(mt, 16, kWave));
+    mt = fmaxf(mt, __shfl_xor(mt, 32, kWave));
+    const float mn = fmaxf(m, mt);
+    const float base = mn == kNegInf ? 0.f : mn;
+    const float shrink = __builtin_amdgcn_exp2f(m - base);  // 0 for the first keys
+    m = mn;
+    f32x8 w[2];
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float p = __builtin_amdgcn_exp2f(x[e] - base);
+      w[e / 8][e % 8] = p;
+      sum += p;
+    }
+    l = fmaf(sum, iv, l * shrink);
+    const f16x8 p0 = to_f16(w[0]), p1 = to_f16(w[1]);
+#pragma unroll
+    for (int d = 0; d < kDt; ++d) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][e] *= shrink;
+      o[d] = mfma_16x16x32<false>(widen<false>(vc[d][0], vc[d][1]), p0, o[d]);
+      o[d] = mfma_16x16x32<false>(widen<false>(vc[d][2], vc[d][3]), p1, o[d]);
+    }
+    if (more) load_v(tile + 4, vid1, vc);
+    vid = vid1;
+    kid1 = kid2;
+    vid1 = vid2;
+    ksc = nks;
+    vsc = nvs;
+  }
+  l += __shfl_xor(l, 16, kWave);
+  l += __shfl_xor(l, 32, kWave);
+
+  // The four wavefronts' parts meet in LDS; lane (i, h) holds dimensions
+  // 16 d + 4 h .. + 3 of row i.
+#pragma unroll
+  for (int d = 0; d < kDt; ++d) *reinterpret_cast<f32x4*>(&so[wave][i][16 * d + 4 * h]) = o[d];
+  if (h == 0) {
+    sm[wave][i] = m;
+    sl[wave][i] = l;
+  }
+  __syncthreads();
+  const size_t all_rows = static_cast<size_t>(c.tokens) * heads;
+  for (int at = threadIdx.x; at < 16 * (D / 4); at += 256) {
+    const int rr = at / (D / 4), d = 4 * (at % (D / 4));
+    const int row = 16 * rt + rr;
+    if (row >= rows) continue;
+    const float mx = fmaxf(fmaxf(sm[0][rr], sm[1][rr]), fmaxf(sm[2][rr], sm[3][rr]));
+    const float base = mx == kNegInf ? 0.f : mx;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    float total = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = __builtin_amdgcn_exp2f(sm[w][rr] - base);
+      total = fmaf(sl[w][rr], f, total);
+      const f32x4 part = *reinterpret_cast<const f32x4*>(&so[w][rr][d]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = fmaf(part[e], f, v[e]);
+    }
+    const int t = row / group, gg = row - t * group;
+    const size_t to = static_cast<size_t>(seq.row0 + t) * heads + head * group + gg;
+    if (splits == 1) {
+      const float inv = total > 0.f ? 1.f / total : 0.f;
+      const uint32_t lo = half_bits<kBf16>(v[0] * inv) | (static_cast<uint32_t>(half_bits<kBf16>(v[1] * inv)) << 16);
+      const uint32_t hi = half_bits<kBf16>(v[2] * inv) | (static_cast<uint32_t>(half_bits<kBf16>(v[3] * inv)) << 16);
+      *reinterpret_cast<u32x2*>(out + to * D + d) = u32x2{lo, hi};
+    } else {
+      float* const p = parts.o + (static_cast<size_t>(split) * all_rows + to) * D + d;
+      *reinterpret_cast<f32x4*>(p) = v;
+      if (d == 0) *reinterpret_cast<f32x2*>(parts.ml + 2 * (static_cast<size_t>(split) * all_rows + to)) = f32x2{mx, total};
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joins the splits of every row: weights 2^(m_z - m), in split order. Rows of
+// no sequence are left alone. One wavefront takes one row.
+// ---------------------------------------------------------------------------
+
+template <int D, bool kBf16>
+__global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __restrict__ out, Parts parts, int heads,
+                                                       int splits) {
+  const size_t rows = static_cast<size_t>(c.tokens) * heads;
+  const size_t row = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (row >= rows) return;
+  const int token = static_cast<int>(row / heads);
+  if (token < c.cu[0] || token >= c.cu[c.batch]) return;
+  const int lane = threadIdx.x & 63;
+  constexpr int kE = D / 64;
+  float m = kNegInf;
+  for (int z = lane; z < splits; z += 64) m = fmaxf(m, parts.ml[2 * (z * rows + row)]);
+  m = wave_max(m);
+  const float base = m == kNegInf ? 0.f : m;
+  float total = 0.f, v[kE] = {};
+  for (int z = 0; z < splits; ++z) {
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(parts.ml + 2 * (z * rows + row));
+    if (!(ml[1] > 0.f)) continue;  // a split without keys for this row (its output is not read)
+    const float f = __builtin_amdgcn_exp2f(ml[0] - base);
+    total = fmaf(ml[1], f, total);
+    const float* const p = parts.o + (z * rows + row) * D + kE * lane;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) v[e] = fmaf(p[e], f, v[e]);
+  }
+  const float inv = total > 0.f ? 1.f / total : 0.f;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) out[row * D + kE * lane + e] = half_bits<kBf16>(v[e] * inv);
+}
+
+// ---------------------------------------------------------------------------
+// Prompts: a workgroup of eight wavefronts takes 256 rows of one kv head (the
+// query heads of the group side by side, so that one K/V tile serves all of
+// them) and walks the keys in tiles of 64. The tile's codes are widened once
+// per workgroup on their way into LDS (double-buffered; the next tile's codes
+// are already in registers), each wavefront then reads it for its 32 rows.
+// v_mfma_32x32x16: lane (i = lane % 32, h = lane / 32). Row i of a K tile is
+// the token with bits 2 and 3 of i exchanged: lane (i, h) then holds, for row
+// i of Q, in registers 8 u .. 8 u + 7 the scores of the consecutive tokens
+// 16 u + 8 h .. + 7, the B operand of the second product.
+// ---------------------------------------------------------------------------
+
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+template <int D, bool kBf16>
+__global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint16_t* __restrict__ q, int64_t q_stride,
+                                                         uint16_t* __restrict__ out, Parts parts, int group,
+                                                         int row_tiles, int splits, float scale_log2) {
+  constexpr int kRows = 256, kKs = D / 16, kDt = D / 32;
+  constexpr int kKRow = 2 * D;                // bytes of a widened K row
+  constexpr int kKBytes = 64 * kKRow, kVBytes = D * 128;
+  constexpr int kBuf = kKBytes + kVBytes;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kBuf];
+  __shared__ f32x4 sscale[2][4];  // per part of 16 keys: k scale, log2 and reciprocal of the v scale (< 0: no page)
+  lds_u8* const lds = (lds_u8*)(smem);
+
+  // the last rows of a sequence see the most keys: they go first
+  const int rt = row_tiles - 1 - static_cast<int>(blockIdx.x) / splits, split = static_cast<int>(blockIdx.x) % splits;
+  const int head = static_cast<int>(blockIdx.y), b = static_cast<int>(blockIdx.z);
+  const Seq seq = sequence(c, b);
+  const int rows = seq.n * group;
+  if (kRows * rt >= rows) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 31, h = lane >> 5;
+  const int heads = c.kv_heads * group;
+
+  const int r = kRows * rt + 32 * wave + i;
+  const bool live = r < rows;
+  const int tq = live ? r / group : 0, g = live ? r - tq * group : 0;
+  const int limit = live ? min(seq.len - seq.n + tq, seq.seen - 1) : -1;
+  const uint16_t* const qrow = q + static_cast<int64_t>(seq.row0 + tq) * q_stride + (head * group + g) * D;
+  f16x8 qf[kKs];
+#pragma unroll
+  for (int ks = 0; ks < kKs; ++ks) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (live) v = *reinterpret_cast<const u32x4*>(qrow + 16 * ks + 8 * h);
+    qf[ks] = __builtin_bit_cast(f16x8, v);
+  }
+
+  const int last_t = min(kRows * rt + kRows - 1, rows - 1) / group;
+  const int top = min(seq.len - seq.n + last_t, seq.seen - 1);
+  const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, 8);
+  const int32_t* const table = c.table + static_cast<size_t>(b) * c.table_width;
+
+  // Staging: 16-byte pieces of codes; piece p of K is row p / (D / 16), of V
+  // dimension p / 4, tokens 16 (p % 4) .. + 15.
+  constexpr int kPieces = 64 * D / 16;  // of K, and of V
+  static_assert(kPieces <= 512, "one piece of each per thread");
+  const bool stager = threadIdx.x < kPieces;
+  const int krow = threadIdx.x / (D / 16), kch = threadIdx.x % (D / 16);
+  const int vdim = threadIdx.x / 4, vpart = threadIdx.x % 4;
+  // Page of the 16 keys `part` of a tile; -1: none, or not one of the pool's.
+  auto page_id = [&](int tile, int part) {
+    const int t = 64 * tile + 16 * part;
+    return tile < span.end && t <= top ? table[t >> c.page_shift] : -1;
+  };
+  auto known = [&](int id) { return id >= 0 && id < c.num_pages; };
+  // Codes and scales of a tile into registers; the page numbers were requested
+  // one call earlier.
+  int kid = -1, vid = -1, sid = -1;
+  auto request_pages = [&](int tile) {
+    kid = page_id(tile, krow / 16);
+    vid = page_id(tile, vpart);
+    sid = page_id(tile, threadIdx.x & 3);
+  };
+  u32x4 kreg, vreg;
+  float kscale = 0.f, vscale = -1.f;
+  auto fetch = [&](int tile) {
+    kreg = vreg = u32x4{0u, 0u, 0u, 0u};
+    vscale = -1.f;
+    if (tile < span.end) {
+      if (stager && known(kid)) {
+        const int at = (64 * tile + krow) & (c.page - 1);
+        kreg = *reinterpret_cast<const u32x4*>(
+            c.k + ((static_cast<size_t>(kid) * c.kv_heads + head) * c.page + at) * D + 16 * kch);
+      }
+      if (stager && known(vid)) {
+        const int at = (64 * tile + 16 * vpart) & (c.page - 1);
+        vreg = *reinterpret_cast<const u32x4*>(
+            c.v + ((static_cast<size_t>(vid) * c.kv_heads + head) * D + vdim) * c.page + at);
+      }
+      if (threadIdx.x < 4 && known(sid)) {
+        const size_t unit = static_cast<size_t>(sid) * c.kv_heads + head;
+        kscale = c.k_scales[unit];
+        vscale = held_scale(c.v_scales[unit]);
+      }
+    }
+    request_pages(tile + 1);
+  };
+  // 16-byte chunk positions are XOR-ed by the row, so that a fragment read of
+  // 32 rows meets no bank twice: K rows of 256 bytes by 16 rows, of 128 bytes
+  // (and V rows) by pairs of rows.
+  auto k_chunk = [&](int row, int ch) {
+    return row * kKRow + 16 * (D == 128 ? ch ^ (row & 15) : ch ^ ((row >> 1) & 7));
+  };
+  auto v_chunk = [&](int row, int ch) { return kKBytes + row * 128 + 16 * (ch ^ ((row >> 1) & 7)); };
+  auto stage = [&](int tile, int buf) {
+    if (threadIdx.x < 4)
+      sscale[buf][threadIdx.x] =
+          f32x4{kscale * scale_log2, __builtin_amdgcn_logf(fmaxf(vscale, kMinScale)), vscale > 0.f ? 1.f / vscale : -1.f, 0.f};
+    if (!stager) return;
+    if (64 * tile + 63 > top) vreg = first_bytes(vreg, top - (64 * tile + 16 * vpart) + 1);
+    lds_u8* const to = lds + buf * kBuf;
+    *(lds_u32x4*)(to + k_chunk(krow, 2 * kch)) = __builtin_bit_cast(u32x4, widen<kBf16>(kreg[0], kreg[1]));
+    *(lds_u32x4*)(to + k_chunk(krow, 2 * kch + 1)) = __builtin_bit_cast(u32x4, widen<kBf16>(kreg[2], kreg[3]));
+    *(lds_u32x4*)(to + v_chunk(vdim, 2 * vpart)) = __builtin_bit_cast(u32x4, widen<false>(vreg[0], vreg[1]));
+    *(lds_u32x4*)(to + v_chunk(vdim, 2 * vpart + 1)) = __builtin_bit_cast(u32x4, widen<false>(vreg[2], vreg[3]));
+  };
+
+  f32x16 o[kDt];
+#pragma unroll
+  for (int d = 0; d < kDt; ++d) o[d] = f32x16{};
+  float m = kNegInf, l = 0.f;
+  const int wave_low = __builtin_amdgcn_readfirstlane(
+      min(seq.len - seq.n + min(kRows * rt + 32 * wave, rows - 1) / group, seq.seen - 1));  // first row's last key
+  const bool wave_full = kRows * rt + 32 * wave + 31 < rows;  // every lane holds a row
+  const int ktok = (i & 19) | ((i & 4) << 1) | ((i & 8) >> 1);  // bits 2 and 3 exchanged
+
+  request_pages(span.first);
+  fetch(span.first);
+  stage(span.first, 0);
+  fetch(span.first + 1);
+  __syncthreads();
+  for (int tile = span.first; tile < span.end; ++tile) {
+    const int buf = (tile - span.first) & 1;
+    if (tile + 1 < span.end) stage(tile + 1, buf ^ 1);  // every wavefront is past its reads of that buffer
+    fetch(tile + 2);
+    const lds_u8* const src = lds + buf * kBuf;
+
+    float f[4], lv[4], iv[4];
+    bool whole = wave_full && 64 * tile + 63 <= wave_low;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const f32x4 sc = sscale[buf][p];
+      f[p] = sc[0];
+      lv[p] = sc[1];
+      iv[p] = sc[2];
+      whole = whole && iv[p] > 0.f;
+    }
+    whole = __builtin_amdgcn_readfirstlane(whole);
+
+    f32x16 s[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      s[a] = f32x16{};
+#pragma unroll
+      for (int ks = 0; ks < kKs; ++ks) {
+        const u32x4 kf = *(const lds_u32x4*)(src + k_chunk(32 * a + ktok, 2 * ks + h));
+        s[a] = mfma_32x32x16<kBf16>(__builtin_bit_cast(f16x8, kf), qf[ks], s[a]);
+      }
+    }
+    float mt = kNegInf;
+    if (whole) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int p = 2 * a + e / 8;
+          s[a][e] = fmaf(s[a][e], f[p], lv[p]);
+          mt = fmaxf(mt, s[a][e]);
+        }
+    } else {
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int p = 2 * a + e / 8;
+          const int t = 64 * tile + 16 * p + 8 * h + e % 8;
+          s[a][e] = t <= limit && iv[p] > 0.f ? fmaf(s[a][e], f[p], lv[p]) : kNegInf;
+          mt = fmaxf(mt, s[a][e]);
+        }
+    }
+    mt = fmaxf(mt, __shfl_xor(mt, 32, kWave));
+    const float mn = fmaxf(m, mt);
+    const float base = mn == kNegInf ? 0.f : mn;
+    const float shrink = __builtin_amdgcn_exp2f(m - base);
+    m = mn;
+    f16x8 w[4];
+    l *= shrink;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      f32x8 x;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = __builtin_amdgcn_exp2f(s[p / 2][8 * (p % 2) + e] - base);
+        sum += x[e];
+      }
+      l = fmaf(sum, fmaxf(iv[p], 0.f), l);
+      w[p] = to_f16(x);
+    }
+#pragma unroll
+    for (int d = 0; d < kDt; ++d) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] *= shrink;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const u32x4 vf = *(const lds_u32x4*)(src + v_chunk(32 * d + i, 2 * p + h));
+        o[d] = mfma_32x32x16<false>(__builtin_bit_cast(f16x8, vf), w[p], o[d]);
+      }
+    }
+    __syncthreads();
+  }
+  l += __shfl_xor(l, 32, kWave);
+  if (!live) return;
+  const size_t to = static_cast<size_t>(seq.row0 + tq) * heads + head * group + g;
+  if (splits == 1) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int d = 0; d < kDt; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t b4[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) b4[x] = half_bits<kBf16>(o[d][4 * e + x] * inv);
+        *reinterpret_cast<u32x2*>(out + to * D + 32 * d + 8 * e + 4 * h) = u32x2{b4[0] | (b4[1] << 16), b4[2] | (b4[3] << 16)};
+      }
+  } else {
+    const size_t at = static_cast<size_t>(split) * c.tokens * heads + to;
+#pragma unroll
+    for (int d = 0; d < kDt; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f32x4*>(parts.o + at * D + 32 * d + 8 * e + 4 * h) =
+            f32x4{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+    if (h == 0) *reinterpret_cast<f32x2*>(parts.ml + 2 * at) = f32x2{m, l};
+  }
+}
+
+constexpr int kDecodeRows = 64;  // rows of one kv head that the decode form takes (four tiles of 16)
+constexpr int kMaxSplits = 64;
+
+template <int D, bool kBf16>
+hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, uint16_t* out, int q_heads, float scale,
+                      const Kv8Plan& plan, void* workspace, hipStream_t stream) {
+  const int group = q_heads / c.kv_heads;
+  const int most = c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
+  const int64_t rows = static_cast<int64_t>(most) * group, all = static_cast<int64_t>(c.tokens) * q_heads;
+  const float scale_log2 = scale * kLog2e;
+  Parts parts = {nullptr, nullptr};
+  if (plan.splits > 1) {
+    parts.o = static_cast<float*>(workspace);
+    parts.ml = parts.o + plan.splits * all * D;
+  }
+  hipError_t e;
+  if (plan.decode) {
+    const int row_tiles = static_cast<int>((rows + 15) / 16);
+    const dim3 grid(static_cast<uint32_t>(plan.splits), static_cast<uint32_t>(c.kv_heads * row_tiles),
+                    static_cast<uint32_t>(c.batch));
+    e = launch_kernel(kv8_decode_kernel<D, kBf16>, grid, dim3(256), 0, stream, c, q, q_stride, out, parts, group,
+                      row_tiles, plan.splits, scale_log2);
+  } else {
+    const int row_tiles = static_cast<int>((rows + 255) / 256);
+    const dim3 grid(static_cast<uint32_t>(row_tiles * plan.splits), static_cast<uint32_t>(c.kv_heads),
+                    static_cast<uint32_t>(c.batch));
+    e = launch_kernel(kv8_prompt_kernel<D, kBf16>, grid, dim3(512), 0, stream, c, q, q_stride, out, parts, group,
+                      row_tiles, plan.splits, scale_log2);
+  }
+  if (e != hipSuccess || plan.splits == 1) return e;
+  return launch_kernel(kv8_join_kernel<D, kBf16>, dim3(static_cast<uint32_t>((all + 3) / 4)), dim3(256), 0, stream, c,
+                       out, parts, q_heads, plan.splits);
+}
+
+}  // namespace
+
+// The keys of a sequence are split over workgroups until the launch holds
+// about kTarget of them; a split keeps at least four tiles of 64 keys (eight
+// for prompts), of the longest sequence that the tables can hold. How long
+// the sequences are is known on the GPU only: there each is cut evenly.
+Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
+  Kv8Plan p;
+  const int group = q_heads / c.kv_heads;
+  const int most = c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
+  const int64_t rows = static_cast<int64_t>(most) * group;
+  p.decode = rows <= kDecodeRows;
+  const int64_t tiles = (static_cast<int64_t>(c.table_width) * c.page + 63) / 64;
+  const int64_t groups = static_cast<int64_t>(c.batch) * c.kv_heads * (p.decode ? (rows + 15) / 16 : (rows + 255) / 256);
+  const int64_t target = p.decode ? 2048 : 256, least = p.decode ? 4 : 8;
+  int64_t splits = groups > 0 ? target / groups : 1;
+  const int64_t fit = (tiles + least - 1) / least;
+  if (splits > fit) splits = fit;
+  if (splits > kMaxSplits) splits = kMaxSplits;
+  // the joining kernel takes four rows per workgroup of 256: under 2^32 work-items
+  if (static_cast<int64_t>(c.tokens) * q_heads >= (int64_t{1} << 26)) splits = 1;
+  p.splits = splits < 1 ? 1 : static_cast<int>(splits);
+  p.workspace_bytes =
+      p.splits > 1 ? static_cast<size_t>(p.splits) * c.tokens * q_heads * (c.head_dim + 2) * sizeof(float) : 0;
+  return p;
+}
+
+hipError_t launch_kv8_attention(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, uint16_t* out, int q_heads,
+                                float softmax_scale, const Kv8Plan& plan, void* workspace, bool bf16,
+                                hipStream_t stream) {
+  if (c.head_dim == 128)
+    return bf16 ? launch_dim<128, true>(c, q, q_stride, out, q_heads, softmax_scale, plan, workspace, stream)
+                : launch_dim<128, false>(c, q, q_stride, out, q_heads, softmax_scale, plan, workspace, stream);
+  if (c.head_dim == 64)
+    return bf16 ? launch_dim<64, true>(c, q, q_stride, out, q_heads, softmax_scale, plan, workspace, stream)
+                : launch_dim<64, false>(c, q, q_stride, out, q_heads, softmax_scale, plan, workspace, stream);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace mq

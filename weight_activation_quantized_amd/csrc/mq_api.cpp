@@ -745,4 +745,186 @@ mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* 
   return fp8_linear_impl(x, wq, s_w, y, M, N, K, workspace, workspace_bytes, true, stream);
 }
 
+// ---- paged e4m3 KV cache ---------------------------------------------------
+
+// Everything but the rows of q, k and v. T == 0 or B == 0 is an empty call.
+static mq_status kv8_cache(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scales, const float* v_scales,
+                           const int32_t* block_table, const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int64_t B,
+                           int64_t Hkv, int64_t D, int64_t page, int64_t num_pages, int64_t table_width,
+                           int64_t max_q_len, mq::Kv8Cache& c) {
+  if (D != 64 && D != 128) return fail(MQ_ERR_UNSUPPORTED, "head_dim=%lld (64 and 128 are provided)", (long long)D);
+  if (page != 16 && page != 32 && page != 64 && page != 128)
+    return fail(MQ_ERR_UNSUPPORTED, "page=%lld (16, 32, 64 and 128 tokens are provided)", (long long)page);
+  if (T < 0 || T > (int64_t{1} << 26)) return fail(MQ_ERR_SHAPE, "T=%lld out of range", (long long)T);
+  if (B < 0 || B > 65535) return fail(MQ_ERR_SHAPE, "B=%lld must lie in [0, 65535]", (long long)B);
+  if (Hkv < 1 || Hkv > 1024) return fail(MQ_ERR_SHAPE, "Hkv=%lld must lie in [1, 1024]", (long long)Hkv);
+  if (num_pages < 1 || num_pages > kMaxDim) return fail(MQ_ERR_SHAPE, "num_pages=%lld out of range", (long long)num_pages);
+  if (table_width < 1 || table_width > (int64_t{1} << 30) / page)
+    return fail(MQ_ERR_SHAPE, "table_width=%lld: a sequence holds at most 2^30 tokens", (long long)table_width);
+  if (max_q_len < 1 || max_q_len > kMaxDim) return fail(MQ_ERR_SHAPE, "max_q_len=%lld must be positive", (long long)max_q_len);
+  MQ_TRY(need(k_cache, 1, "k_cache"));
+  MQ_TRY(need(v_cache, 1, "v_cache"));
+  MQ_TRY(need(k_scales, 1, "k_scales"));
+  MQ_TRY(need(v_scales, 1, "v_scales"));
+  MQ_TRY(need(block_table, B, "block_table"));
+  MQ_TRY(need(cu_q, B, "cu_q"));
+  MQ_TRY(need(kv_lens, B, "kv_lens"));
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(MQ_ERR_ALIGN, "k_cache and v_cache must be 16-byte aligned");
+  if (!aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(kv_lens, 4))
+    return fail(MQ_ERR_ALIGN, "scales, block_table, cu_q and kv_lens must be 4-byte aligned");
+  c = {};
+  c.k = const_cast<uint8_t*>(k_cache);
+  c.v = const_cast<uint8_t*>(v_cache);
+  c.k_scales = const_cast<float*>(k_scales);
+  c.v_scales = const_cast<float*>(v_scales);
+  c.table = block_table;
+  c.cu = cu_q;
+  c.lens = kv_lens;
+  c.batch = static_cast<int>(B);
+  c.kv_heads = static_cast<int>(Hkv);
+  c.head_dim = static_cast<int>(D);
+  c.page = static_cast<int>(page);
+  for (c.page_shift = 4; (1 << c.page_shift) < c.page;) ++c.page_shift;
+  c.num_pages = static_cast<int>(num_pages);
+  c.table_width = static_cast<int>(table_width);
+  c.tokens = static_cast<int>(T);
+  c.max_q_len = static_cast<int>(max_q_len);
+  return MQ_OK;
+}
+
+// Rows of `width` 16-bit values, `stride` values apart.
+static mq_status kv8_rows(const uint16_t* p, int64_t T, int64_t width, int64_t stride, const char* name, size_t& bytes) {
+  MQ_TRY(need(p, T, name));
+  if (stride < width || stride % 8 || stride > kMaxDim)
+    return fail(MQ_ERR_SHAPE, "%s: a stride of %lld for rows of %lld values (a multiple of 8, no less than the row)", name,
+                (long long)stride, (long long)width);
+  if (!aligned(p, 16)) return fail(MQ_ERR_ALIGN, "%s must be 16-byte aligned", name);
+  bytes = T > 0 ? (static_cast<size_t>(T - 1) * stride + width) * 2 : 0;
+  return MQ_OK;
+}
+
+static mq_status kv8_append_impl(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride,
+                                 uint8_t* k_cache, uint8_t* v_cache, float* k_scales, float* v_scales,
+                                 const int32_t* block_table, const int32_t* cu_q, const int32_t* kv_lens, int64_t T,
+                                 int64_t B, int64_t Hkv, int64_t D, int64_t page, int64_t num_pages,
+                                 int64_t table_width, int64_t max_q_len, bool bf16, void* stream) {
+  mq::Kv8Cache c;
+  MQ_TRY(kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, T, B, Hkv, D, page, num_pages,
+                   table_width, max_q_len, c));
+  size_t kb = 0, vb = 0;
+  MQ_TRY(kv8_rows(k, T, Hkv * D, k_stride, "k", kb));
+  MQ_TRY(kv8_rows(v, T, Hkv * D, v_stride, "v", vb));
+  const size_t cache = static_cast<size_t>(num_pages) * Hkv * page * D, sc = static_cast<size_t>(num_pages) * Hkv * 4;
+  const Range in[] = {{k, kb, "k"},
+                      {v, vb, "v"},
+                      {block_table, static_cast<size_t>(B * table_width) * 4, "block_table"},
+                      {cu_q, static_cast<size_t>(B + 1) * 4, "cu_q"},
+                      {kv_lens, static_cast<size_t>(B) * 4, "kv_lens"}};
+  const Range out[] = {{k_cache, cache, "k_cache"}, {v_cache, cache, "v_cache"}, {k_scales, sc, "k_scales"}, {v_scales, sc, "v_scales"}};
+  MQ_TRY(check_alias(in, out));
+  if (T == 0 || B == 0) return ok();
+  if (mq::kv8_append_blocks(c) >= (int64_t{1} << 24))
+    return fail(MQ_ERR_SHAPE, "B * pages of max_q_len tokens * Hkv = %lld must stay below 2^23",
+                (long long)(mq::kv8_append_blocks(c) / 2));
+  return hip_status(mq::launch_kv8_append(c, k, v, k_stride, v_stride, bf16, as_stream(stream)), "kv8_append launch");
+}
+
+mq_status mq_kv8_append(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, uint8_t* k_cache,
+                        uint8_t* v_cache, float* k_scales, float* v_scales, const int32_t* block_table,
+                        const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int64_t B, int64_t Hkv, int64_t D,
+                        int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len, void* stream) {
+  return kv8_append_impl(k, v, k_stride, v_stride, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, T, B,
+                         Hkv, D, page, num_pages, table_width, max_q_len, false, stream);
+}
+
+mq_status mq_kv8_append_bf16(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, uint8_t* k_cache,
+                             uint8_t* v_cache, float* k_scales, float* v_scales, const int32_t* block_table,
+                             const int32_t* cu_q, const int32_t* kv_lens, int64_t T, int64_t B, int64_t Hkv, int64_t D,
+                             int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len, void* stream) {
+  return kv8_append_impl(k, v, k_stride, v_stride, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, T, B,
+                         Hkv, D, page, num_pages, table_width, max_q_len, true, stream);
+}
+
+static mq_status kv8_heads(int64_t Hq, int64_t Hkv) {
+  if (Hq < 1 || Hq > 1024 || Hkv < 1 || Hq % Hkv)
+    return fail(MQ_ERR_SHAPE, "Hq=%lld must be a multiple of Hkv=%lld, at most 1024", (long long)Hq, (long long)Hkv);
+  return MQ_OK;
+}
+
+size_t mq_kv8_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
+                                        int64_t table_width, int64_t max_q_len) {
+  // any addresses do: only sizes are looked at
+  static const float some[4] = {};
+  const uint8_t* const p = reinterpret_cast<const uint8_t*>(16);
+  const int32_t* const t = reinterpret_cast<const int32_t*>(some);
+  mq::Kv8Cache c;
+  if (kv8_cache(p, p, some, some, t, t, t, T, B, Hkv, D, page, 1, table_width, max_q_len, c) != MQ_OK ||
+      kv8_heads(Hq, Hkv) != MQ_OK || T == 0 || B == 0)
+    return 0;
+  return mq::plan_kv8_attention(c, static_cast<int>(Hq)).workspace_bytes;
+}
+
+static mq_status kv8_attention_impl(const uint16_t* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+                                    const float* k_scales, const float* v_scales, const int32_t* block_table,
+                                    const int32_t* cu_q, const int32_t* kv_lens, uint16_t* out, int64_t T, int64_t B,
+                                    int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t num_pages,
+                                    int64_t table_width, int64_t max_q_len, float softmax_scale, void* workspace,
+                                    size_t workspace_bytes, bool bf16, void* stream) {
+  mq::Kv8Cache c;
+  MQ_TRY(kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, T, B, Hkv, D, page, num_pages,
+                   table_width, max_q_len, c));
+  MQ_TRY(kv8_heads(Hq, Hkv));
+  if (!(softmax_scale >= -1e6f && softmax_scale <= 1e6f))
+    return fail(MQ_ERR_UNSUPPORTED, "softmax_scale=%g", static_cast<double>(softmax_scale));
+  size_t qb = 0;
+  MQ_TRY(kv8_rows(q, T, Hq * D, q_stride, "q", qb));
+  MQ_TRY(need(out, T, "out"));
+  if (!aligned(out, 16)) return fail(MQ_ERR_ALIGN, "out must be 16-byte aligned");
+  const mq::Kv8Plan plan = mq::plan_kv8_attention(c, static_cast<int>(Hq));
+  const bool empty = T == 0 || B == 0;
+  const size_t ws = empty ? 0 : plan.workspace_bytes;
+  if (ws > 0) {
+    if (!workspace || workspace_bytes < ws)
+      return fail(MQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", ws,
+                  workspace ? workspace_bytes : static_cast<size_t>(0));
+    if (!aligned(workspace, 16)) return fail(MQ_ERR_ALIGN, "workspace must be 16-byte aligned");
+  }
+  const size_t cache = static_cast<size_t>(num_pages) * Hkv * page * D, sc = static_cast<size_t>(num_pages) * Hkv * 4;
+  const Range in[] = {{q, qb, "q"},
+                      {k_cache, cache, "k_cache"},
+                      {v_cache, cache, "v_cache"},
+                      {k_scales, sc, "k_scales"},
+                      {v_scales, sc, "v_scales"},
+                      {block_table, static_cast<size_t>(B * table_width) * 4, "block_table"},
+                      {cu_q, static_cast<size_t>(B + 1) * 4, "cu_q"},
+                      {kv_lens, static_cast<size_t>(B) * 4, "kv_lens"}};
+  const Range outs[] = {{out, static_cast<size_t>(T) * Hq * D * 2, "out"}, {ws ? workspace : nullptr, ws, "workspace"}};
+  MQ_TRY(check_alias(in, outs));
+  if (empty) return ok();
+  return hip_status(mq::launch_kv8_attention(c, q, q_stride, out, static_cast<int>(Hq), softmax_scale, plan,
+                                             ws ? workspace : nullptr, bf16, as_stream(stream)),
+                    "kv8_attention launch");
+}
+
+mq_status mq_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+                           const float* k_scales, const float* v_scales, const int32_t* block_table, const int32_t* cu_q,
+                           const int32_t* kv_lens, uint16_t* out, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                           int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len, float softmax_scale,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  return kv8_attention_impl(q, q_stride, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, out, T, B, Hq,
+                            Hkv, D, page, num_pages, table_width, max_q_len, softmax_scale, workspace, workspace_bytes,
+                            false, stream);
+}
+
+mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+                                const float* k_scales, const float* v_scales, const int32_t* block_table,
+                                const int32_t* cu_q, const int32_t* kv_lens, uint16_t* out, int64_t T, int64_t B,
+                                int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t num_pages, int64_t table_width,
+                                int64_t max_q_len, float softmax_scale, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  return kv8_attention_impl(q, q_stride, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, out, T, B, Hq,
+                            Hkv, D, page, num_pages, table_width, max_q_len, softmax_scale, workspace, workspace_bytes,
+                            true, stream);
+}
+
 }  // extern "C"
