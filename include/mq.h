@@ -460,17 +460,19 @@ mq_status mq_rmsnorm_fp8_bf16(const uint16_t* x, const uint16_t* residual, const
  *   products, which drops what lies below 2^-13 of the largest of them. The
  *   blocks are added in order, in a fixed number of contiguous ranges:
  *   deterministic.
- * mq_fp8_linear: mq_quant_fp8_blocks, then mq_fp8_block_mm, bit for bit; codes
- *   and scales in `workspace`.
+ * mq_fp8_linear: mq_quant_fp8_blocks, then mq_fp8_block_mm, bit for bit. One
+ *   kernel that needs no workspace for few values (M * ceil(K/128) <= 128 and
+ *   M <= 16); otherwise codes and scales pass through `workspace`.
  *
  *   x     [M, K] fp16   in
  *   xq    [M, K] e4m3 bytes;  s_x [ceil(K/128), M] fp32
  *   wq    [N, K] e4m3 bytes, in (one row per output channel)
  *   s_w   [ceil(N/128), ceil(K/128)] fp32, in
  *   y     [M, N] fp16   out
- *   workspace  >= mq_fp8_linear_workspace_bytes(M, K) bytes, 16-byte aligned,
- *              not overlapping any operand; contents on entry do not matter;
- *              calls sharing it must be ordered.
+ *   workspace  >= mq_fp8_block_mm_workspace_bytes / mq_fp8_linear_workspace_bytes
+ *              (M, N, K) bytes (0: may be NULL), 16-byte aligned, not
+ *              overlapping any operand; contents on entry do not matter; calls
+ *              sharing it must be ordered.
  * Requires: 0 <= M, N <= 2^26, M * N <= 2^36; 16 <= K <= 2^20, K % 16 == 0;
  * the quantizer M * ceil(K/128) < 2^27; x, xq, wq, y 16-byte aligned; scales
  * 4-byte. N need not be a multiple of anything. Codes must not be NaN. _bf16:
@@ -478,11 +480,14 @@ mq_status mq_rmsnorm_fp8_bf16(const uint16_t* x, const uint16_t* residual, const
  */
 mq_status mq_quant_fp8_blocks(const uint16_t* x, uint8_t* xq, float* s_x, int64_t M, int64_t K, void* stream);
 mq_status mq_quant_fp8_blocks_bf16(const uint16_t* x, uint8_t* xq, float* s_x, int64_t M, int64_t K, void* stream);
+size_t mq_fp8_block_mm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 mq_status mq_fp8_block_mm(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
-                          int64_t M, int64_t N, int64_t K, void* stream);
+                          int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                          void* stream);
 mq_status mq_fp8_block_mm_bf16(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
-                               int64_t M, int64_t N, int64_t K, void* stream);
-size_t mq_fp8_linear_workspace_bytes(int64_t M, int64_t K);
+                               int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                               void* stream);
+size_t mq_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 mq_status mq_fp8_linear(const uint16_t* x, const uint8_t* wq, const float* s_w, uint16_t* y, int64_t M, int64_t N,
                         int64_t K, void* workspace, size_t workspace_bytes, void* stream);
 mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* s_w, uint16_t* y, int64_t M, int64_t N,

@@ -45,8 +45,10 @@ def test_quant_fp8(lib):
 
 
 def test_fp8_block_mm(lib):
-    def f(xq=A, sx=B, wq=C, sw=D, y=E, M=4, N=130, K=272):
-        return lib.mq_fp8_block_mm(xq, sx, wq, sw, y, M, N, K, None)
+    ws = lib.mq_fp8_block_mm_workspace_bytes
+
+    def f(xq=A, sx=B, wq=C, sw=D, y=E, M=4, N=130, K=272, w=F, n=1 << 40):
+        return lib.mq_fp8_block_mm(xq, sx, wq, sw, y, M, N, K, w, n, None)
 
     for k in ("xq", "sx", "wq", "sw", "y"):
         assert f(**{k: None}) == NULL, k
@@ -58,22 +60,32 @@ def test_fp8_block_mm(lib):
     assert f(y=A + 16) == ALIAS and f(y=C) == ALIAS and f(y=D) == ALIAS
     assert f(y=B - 4 * 130 * 2 + 16) == ALIAS  # its end reaches the scales
     assert f(M=0, xq=None, sx=None, y=None) == OK and f(N=0, wq=None, sw=None, y=None) == OK
+    # few tiles and a long K are split, which needs a workspace
+    long = dict(M=40, N=512, K=12288)
+    need = ws(40, 512, 12288)
+    assert need > 0 and need % (40 * 512 * 4) == 0
+    assert f(**long, w=None) == WS and f(**long, n=need - 1) == WS and f(**long, w=F + 8) == ALIGN
+    assert f(**long, w=A) == ALIAS and f(**long, w=E + 16) == ALIAS
+    assert ws(4, 130, 272) == 0 and ws(-1, 512, 12288) == 0 and ws(40, 512, 12280) == 0 and ws(0, 512, 12288) == 0
 
 
 def test_fp8_linear(lib):
     ws = lib.mq_fp8_linear_workspace_bytes
-    assert ws(4, 272) == (4 * 272 + 255) // 256 * 256 + 4 * 3 * 4
-    assert ws(0, 272) == 0 and ws(4, 270) == 0 and ws(-1, 272) == 0
+    assert ws(4, 130, 272) == 0  # one kernel
+    need = ws(100, 130, 272)
+    assert need >= 100 * 272 + 100 * 3 * 4
+    assert ws(0, 130, 272) == 0 and ws(100, 130, 270) == 0 and ws(-1, 130, 272) == 0
 
-    def f(x=A, wq=B, sw=C, y=D, M=4, N=130, K=272, w=E, n=None):
-        return lib.mq_fp8_linear(x, wq, sw, y, M, N, K, w, ws(4, 272) if n is None else n, None)
+    def f(x=A, wq=B, sw=C, y=D, M=100, N=130, K=272, w=E, n=None):
+        return lib.mq_fp8_linear(x, wq, sw, y, M, N, K, w, need if n is None else n, None)
 
     for k in ("x", "wq", "sw", "y"):
         assert f(**{k: None}) == NULL, k
-    assert f(w=None) == WS and f(n=ws(4, 272) - 1) == WS
+    assert f(w=None) == WS and f(n=need - 1) == WS
     assert f(w=E + 8) == ALIGN and f(w=A) == ALIAS and f(w=D + 16) == ALIAS and f(y=B) == ALIAS
     assert f(M=(1 << 26) + 1, K=16, N=1, n=1 << 40) == SHAPE and f(K=24) == SHAPE
     assert f(M=0, x=None, y=None, w=None, n=0) == OK
+    assert f(M=4, y=C, n=0, w=None) == ALIAS
 
 
 def test_wrappers_refuse_before_the_library():

@@ -51,7 +51,7 @@ def _check(xq, sx, wq, sw, half, what, rows=None):
 
 
 # one token to past the largest decode form, then the tiled forms
-SHAPES = [(1, 16, 16), (1, 1, 128), (1, 4096, 4096), (3, 130, 144), (5, 300, 1040), (15, 257, 2064), (16, 512, 4096),
+SHAPES = [(1, 16, 16), (1, 1, 128), (2, 9000, 512), (11, 700, 12288), (16, 8200, 4096), (16, 100, 12288), (20, 17, 16), (1, 4096, 4096), (3, 130, 144), (5, 300, 1040), (15, 257, 2064), (16, 512, 4096),
           (17, 384, 1152), (32, 129, 2048), (33, 640, 4096), (63, 1000, 784), (64, 256, 12288), (65, 131, 272),
           (100, 1024, 1024), (255, 300, 144), (256, 4096, 512), (300, 9000, 640), (517, 6144, 1040),
           (1030, 3000, 400), (1500, 13000, 272), (4100, 4100, 160)]
@@ -145,7 +145,7 @@ def test_graph_replays_and_stream(M):
     t, _ = half_tensor(activations(rng, M, K), "bf16")
     _, _, wq, sw = _inputs(rng, 1, N, K)
     wt, st = codes_tensor(wq), _up(sw)
-    ws = torch.empty(mq.fp8_linear_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(mq.fp8_linear_workspace_bytes(M, N, K), 16), dtype=torch.uint8, device="cuda")
     y = mq.fp8_linear(t, wt, st, workspace=ws)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()

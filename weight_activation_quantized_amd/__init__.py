@@ -63,7 +63,7 @@ __all__ = [
     "w8a8_linear_workspace_bytes", "w4a16_gemm_workspace_bytes", "kv_quant",
     "AWQ_FIELD_ORDER", "int4_reorder", "int4_transpose", "u16_transpose",
     "w8a8_linear_noalloc", "NOALLOC_SCRATCH_BYTES",
-    "rmsnorm_int8", "rmsnorm_fp8", "quant_fp8_blocks", "fp8_block_mm", "fp8_linear", "fp8_linear_workspace_bytes",
+    "rmsnorm_int8", "rmsnorm_fp8", "quant_fp8_blocks", "fp8_block_mm", "fp8_block_mm_workspace_bytes", "fp8_linear", "fp8_linear_workspace_bytes",
     "kv8_append", "kv8_attention", "kv8_attention_workspace_bytes",
 ]
 
@@ -131,9 +131,10 @@ _PROTOTYPES = {
     "mq_rmsnorm_fp8_bf16": (ctypes.c_int, _RMSNORM),
     "mq_quant_fp8_blocks": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _P]),
     "mq_quant_fp8_blocks_bf16": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _P]),
-    "mq_fp8_block_mm": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
-    "mq_fp8_block_mm_bf16": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
-    "mq_fp8_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "mq_fp8_block_mm_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "mq_fp8_block_mm": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
+    "mq_fp8_block_mm_bf16": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
+    "mq_fp8_linear_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "mq_fp8_linear": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
     "mq_kv8_append": (ctypes.c_int, _KV8_APPEND),
     "mq_kv8_append_bf16": (ctypes.c_int, _KV8_APPEND),
@@ -591,7 +592,24 @@ def _fp8_weights(wq, s_w, K):
     return N
 
 
-def fp8_block_mm(xq, s_x, wq, s_w, out=None, stream=None, out_dtype=None):
+def _workspace(workspace, need, like):
+    """(pointer, bytes, tensor) of the caller's workspace, or of a fresh one."""
+    torch = _torch()
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    if workspace is None:
+        return None, 0, None
+    if not isinstance(workspace, torch.Tensor) or workspace.device.type != "cuda" or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def fp8_block_mm_workspace_bytes(M, N, K):
+    """Workspace bytes ``fp8_block_mm`` needs (0 if none)."""
+    return int(library().mq_fp8_block_mm_workspace_bytes(M, N, K))
+
+
+def fp8_block_mm(xq, s_x, wq, s_w, out=None, workspace=None, stream=None, out_dtype=None):
     """y[M, N] = xq[M, K] . wq[N, K]^T, both e4m3 with a scale per block of 128
     (s_x [ceil(K/128), M], s_w [ceil(N/128), ceil(K/128)]), in fp16 (default)
     or bf16 (``out_dtype=torch.bfloat16``, or a bf16 ``out``)."""
@@ -609,27 +627,16 @@ def fp8_block_mm(xq, s_x, wq, s_w, out=None, stream=None, out_dtype=None):
     fn = library().mq_fp8_block_mm_bf16 if out_dtype == torch.bfloat16 else library().mq_fp8_block_mm
     with _scope(xq, stream):
         y = _out(out, (M, N), out_dtype, xq, "out")
-        _same_device(xq, s_x, wq, s_w, y)
-        _check(fn(xq.data_ptr(), s_x.data_ptr(), wq.data_ptr(), s_w.data_ptr(), y.data_ptr(), M, N, K,
+        ws_ptr, ws_bytes, workspace = _workspace(workspace, fp8_block_mm_workspace_bytes(M, N, K), xq)
+        _same_device(xq, s_x, wq, s_w, y, workspace)
+        _check(fn(xq.data_ptr(), s_x.data_ptr(), wq.data_ptr(), s_w.data_ptr(), y.data_ptr(), M, N, K, ws_ptr, ws_bytes,
                   _stream_of(xq, stream)))
     return y
 
 
-def _workspace(workspace, need, like):
-    """(pointer, bytes, tensor) of the caller's workspace, or of a fresh one."""
-    torch = _torch()
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-    if workspace is None:
-        return None, 0, None
-    if not isinstance(workspace, torch.Tensor) or workspace.device.type != "cuda" or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous GPU tensor")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
-def fp8_linear_workspace_bytes(M, K):
-    """Workspace bytes ``fp8_linear`` needs (codes and scales of x)."""
-    return int(library().mq_fp8_linear_workspace_bytes(M, K))
+def fp8_linear_workspace_bytes(M, N, K):
+    """Workspace bytes ``fp8_linear`` needs (0 where one kernel does it all)."""
+    return int(library().mq_fp8_linear_workspace_bytes(M, N, K))
 
 
 def fp8_linear(x, wq, s_w, out=None, workspace=None, stream=None):
@@ -644,7 +651,7 @@ def fp8_linear(x, wq, s_w, out=None, workspace=None, stream=None):
     fn = library().mq_fp8_linear_bf16 if dt == torch.bfloat16 else library().mq_fp8_linear
     with _scope(x, stream):
         y = _out(out, (M, N), dt, x, "out")
-        ws_ptr, ws_bytes, workspace = _workspace(workspace, fp8_linear_workspace_bytes(M, K), x)
+        ws_ptr, ws_bytes, workspace = _workspace(workspace, fp8_linear_workspace_bytes(M, N, K), x)
         _same_device(x, wq, s_w, y, workspace)
         _check(fn(x.data_ptr(), wq.data_ptr(), s_w.data_ptr(), y.data_ptr(), M, N, K, ws_ptr, ws_bytes,
                   _stream_of(x, stream)))

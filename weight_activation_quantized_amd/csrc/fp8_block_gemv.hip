@@ -1,27 +1,33 @@
-// e4m3 matrix product with one scale per block of 128 for up to 64 tokens, on
-// gfx950. Same definition as fp8_block_mm.hip:
+// e4m3 matrix product with one scale per block of 128 for up to 16 tokens, on
+// gfx950. Same definition as fp8_block_mm.hip (and the same alignment of 8
+// products inside the fp8 matrix unit):
 //
 //   y[m,n] = rne16( sum_b (sx[b,m] * sw[n/128,b]) * sum_{k in block b} xq[m,k] * wq[n,k] )
-//
-// (the fp8 matrix unit's alignment of 8 products as described there).
 //
 // With few tokens the product is bound by the weight stream (N*K bytes), so
 // every weight byte is read once, straight into registers, with as many bytes
 // in flight as the registers hold:
-// - A workgroup owns 16 output channels; its wavefronts split K into
-//   contiguous ranges of whole blocks and add their binary32 sums in LDS in
-//   wavefront order (deterministic).
+// - A capped grid of workgroups walks tiles of 16 output channels. Before the
+//   first one it brings the tokens' codes and scales into LDS, once for all of
+//   its tiles, behind its first weight requests: either from xq and s_x, or
+//   (few values) quantized right there from x, which saves a launch and the
+//   codes' way through memory.
+// - The wavefronts of a workgroup split K into contiguous ranges of whole
+//   blocks; their binary32 sums meet in LDS in wavefront order (deterministic).
 // - v_mfma_f32_16x16x128_f8f6f4 covers exactly one scale block: weight rows
 //   are its A operand, 16 tokens its B operand. Lane (i = lane % 16,
 //   h = lane / 16) takes the 16-byte chunks h and 4 + h of row i's 128 bytes
 //   (both operands alike, so which k a lane holds does not matter): the four
-//   lanes of a row read 64 contiguous bytes. The block's result starts from
-//   zero and joins the running sum with four multiply-adds per lane.
-// - Two register sets of blocks alternate: one set's loads are in flight while
-//   the other's MFMAs run. Buffer loads past a descriptor's size return zero
-//   (rows past N, tokens past M, the end of a ragged last block).
+//   lanes of a row read 64 contiguous bytes. Lanes of tokens past M read the
+//   last token's row; their results are not stored. The block's result starts
+//   from zero and joins the running sum with four multiply-adds per lane.
+// - Two register sets of four blocks alternate, across tiles too: one set's
+//   loads are in flight while the other's MFMAs run. Buffer loads past a
+//   descriptor's size return zero (rows past N, the end of a ragged last
+//   block, blocks past the wavefront's range).
 #include "device_common.h"
 #include "launch.h"
+#include "quant_codes.h"
 
 namespace mq {
 namespace {
@@ -30,138 +36,223 @@ typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kOob = 0x80000000u;    // a buffer offset past every operand: the load returns 0
 constexpr int kBufferFlags = 0x00020000;  // gfx9 buffer descriptor word 3 (raw 32-bit data)
+constexpr int kU = 4;                     // blocks per register set
+constexpr int kMaxM = 16;
+constexpr int kFusedUnits = 128;          // blocks of 128 values that a workgroup quantizes from its registers
+constexpr int64_t kCuLds = 160 * 1024;
+constexpr int64_t kGemvLds = 140 * 1024;  // codes and scales, beside the sums of eight wavefronts
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* base, int64_t bytes) {
   const int64_t n = bytes < 0 ? 0 : (bytes > 0x7fffffff ? 0x7fffffff : bytes);
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(n), kBufferFlags);
 }
 
-__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
-
-// One register set: kU blocks of one 16-channel weight tile and kT 16-token
-// tiles, with the token scales of each.
-template <int kU, int kT>
 struct Set {
-  i32x4 w[kU][2], x[kU][kT][2];
-  float sx[kU][kT], sw[kU];
+  i32x4 w[kU][2];
+  float sw[kU];
 };
 
-template <int kU, int kT>
-__device__ __forceinline__ void issue(Set<kU, kT>& f, __amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rx,
-                                      __amdgpu_buffer_rsrc_t rsx, const float* __restrict__ s_w, int i, int h, int M,
-                                      int K, int b0, int b_end) {
-#pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    const int b = b0 + u;
-    const bool in = b < b_end;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int k = 128 * b + 64 * c + 16 * h;
-      const bool ok = in && k < K;
-      f.w[u][c] = load16(rw, ok ? static_cast<uint32_t>(i * K + k) : kOob);
-#pragma unroll
-      for (int t = 0; t < kT; ++t) f.x[u][t][c] = load16(rx, ok ? static_cast<uint32_t>((16 * t + i) * K + k) : kOob);
-    }
-#pragma unroll
-    for (int t = 0; t < kT; ++t) {
-      const bool ok = in && 16 * t + i < M;
-      f.sx[u][t] = __builtin_bit_cast(
-          float, __builtin_amdgcn_raw_buffer_load_b32(rsx, ok ? static_cast<uint32_t>(b * M + 16 * t + i) * 4u : kOob,
-                                                      0, 0));
-    }
-    f.sw[u] = s_w[in ? b : b_end - 1];
-  }
-}
+// LDS: M rows of codes (whole blocks, 16 bytes of padding so that the rows
+// start on different banks), then the scales [blocks][16].
+__host__ __device__ constexpr int64_t code_pitch(int64_t K) { return (K + 127) / 128 * 128 + 16; }
+int64_t lds_bytes(int64_t M, int64_t K) { return M * code_pitch(K) + (K + 127) / 128 * kMaxM * 4; }
 
-template <int kU, int kT>
-__device__ __forceinline__ void use(const Set<kU, kT>& f, f32x4 (&acc)[kT]) {
-#pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    const i32x8 w = __builtin_shufflevector(f.w[u][0], f.w[u][1], 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-    for (int t = 0; t < kT; ++t) {
-      const i32x8 x = __builtin_shufflevector(f.x[u][t][0], f.x[u][t][1], 0, 1, 2, 3, 4, 5, 6, 7);
-      f32x4 p = {0.f, 0.f, 0.f, 0.f};
-      p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, p, 0, 0, 0, 0, 0, 0);
-      const float sc = f.sx[u][t] * f.sw[u];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(p[e], sc, acc[t][e]);
-    }
-  }
-}
-
-template <int kW, int kU, int kT, bool kBf16>
-__global__ __launch_bounds__(64 * kW) void fp8_block_gemv_kernel(const uint8_t* __restrict__ xq,
+template <int kW, bool kFused, bool kBf16>
+__global__ __launch_bounds__(64 * kW) void fp8_block_gemv_kernel(const uint16_t* __restrict__ x,
+                                                                 const uint8_t* __restrict__ xq,
                                                                  const float* __restrict__ s_x,
                                                                  const uint8_t* __restrict__ wq,
                                                                  const float* __restrict__ s_w,
                                                                  uint16_t* __restrict__ y, int M, int N, int K) {
-  __shared__ float part[kW][16 * kT][17];
-  const int n0 = static_cast<int>(blockIdx.x) * 16;
+  constexpr int kTh = 64 * kW;
+  __shared__ float part[2][kW][kMaxM][17];
+  extern __shared__ __attribute__((aligned(16))) uint8_t codes[];
+  const int blocks = (K + 127) / 128;
+  const int pitch = static_cast<int>(code_pitch(K));
+  float* const scales = reinterpret_cast<float*>(codes + static_cast<size_t>(M) * pitch);
+
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, h = lane >> 4;
-  const int blocks = (K + 127) / 128;
+  const int tiles = (N + 15) / 16, step = static_cast<int>(gridDim.x);
   const int share = (blocks + kW - 1) / kW;
   const int b_begin = min(blocks, wave * share), b_end = min(blocks, b_begin + share);
+  const int sets = (share + kU - 1) / kU;  // the same for every wavefront: all meet the tiles' barriers
 
-  const __amdgpu_buffer_rsrc_t rw = rsrc(wq + static_cast<size_t>(n0) * K, static_cast<int64_t>(min(16, N - n0)) * K);
-  const __amdgpu_buffer_rsrc_t rx = rsrc(xq, static_cast<int64_t>(M) * K);
-  const __amdgpu_buffer_rsrc_t rsx = rsrc(s_x, static_cast<int64_t>(blocks) * M * 4);
-  const float* const sw = s_w + static_cast<size_t>(n0 / 128) * blocks;
-
-  f32x4 acc[kT];
+  auto issue = [&](Set& f, int tile, int set) {
+    const int n0 = 16 * min(tile, tiles - 1);
+    const __amdgpu_buffer_rsrc_t rw =
+        rsrc(wq + static_cast<size_t>(n0) * K, tile < tiles ? static_cast<int64_t>(min(16, N - n0)) * K : 0);
+    const float* const sw = s_w + static_cast<size_t>(n0 / 128) * blocks;
 #pragma unroll
-  for (int t = 0; t < kT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (b_begin < b_end) {
-    Set<kU, kT> fa, fb;
-    issue(fa, rw, rx, rsx, sw, i, h, M, K, b_begin, b_end);
-    for (int b = b_begin; b < b_end; b += 2 * kU) {
-      issue(fb, rw, rx, rsx, sw, i, h, M, K, b + kU, b_end);
-      __builtin_amdgcn_sched_barrier(0);
-      use(fa, acc);
-      __builtin_amdgcn_sched_barrier(0);
-      issue(fa, rw, rx, rsx, sw, i, h, M, K, b + 2 * kU, b_end);
-      __builtin_amdgcn_sched_barrier(0);
-      use(fb, acc);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int u = 0; u < kU; ++u) {
+      const int b = b_begin + set * kU + u;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int k = 128 * b + 64 * c + 16 * h;
+        f.w[u][c] = __builtin_bit_cast(
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                       rw, b < b_end && k < K ? static_cast<uint32_t>(i * K + k) : kOob, 0, 0));
+      }
+      f.sw[u] = sw[min(b, blocks - 1)];
+    }
+  };
+  const uint8_t* const row = codes + static_cast<size_t>(min(i, M - 1)) * pitch + 16 * h;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  auto use = [&](const Set& f, int set) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int b = min(b_begin + set * kU + u, blocks - 1);  // past the range the weights are zero
+      const i32x4 x0 = *reinterpret_cast<const i32x4*>(row + 128 * b);
+      const i32x4 x1 = *reinterpret_cast<const i32x4*>(row + 128 * b + 64);
+      f32x4 p = {0.f, 0.f, 0.f, 0.f};
+      p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          __builtin_shufflevector(f.w[u][0], f.w[u][1], 0, 1, 2, 3, 4, 5, 6, 7),
+          __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7), p, 0, 0, 0, 0, 0, 0);
+      const float sc = scales[b * kMaxM + i] * f.sw[u];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(p[e], sc, acc[e]);
+    }
+  };
+
+  Set fa, fb;
+  int tile = static_cast<int>(blockIdx.x);  // < tiles: the grid is at most the tile count
+  if constexpr (kFused) {
+    // 16 lanes take one block of one row, kTh / 16 of them at a time.
+    const int nchunk = K / 8, units = M * blocks;
+    constexpr int kUnits = kTh / 16, kMost = kFusedUnits / kUnits;
+    u32x4 v[kMost];
+#pragma unroll
+    for (int r = 0; r < kMost; ++r) {
+      const int g = static_cast<int>(threadIdx.x >> 4) + kUnits * r;
+      const int m = g / blocks, c = (g - m * blocks) * 16 + static_cast<int>(threadIdx.x & 15);
+      v[r] = u32x4{0u, 0u, 0u, 0u};
+      if (g < units && c < nchunk) v[r] = *reinterpret_cast<const u32x4*>(x + static_cast<size_t>(m) * K + 8 * c);
+    }
+    issue(fa, tile, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int r = 0; r < kMost; ++r) {
+      const int g = static_cast<int>(threadIdx.x >> 4) + kUnits * r;
+      if (g >= units) break;  // uniform within the 16 lanes of a block
+      const int m = g / blocks, b = g - m * blocks;
+      float f[8], a = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        word_to_floats<kBf16>(v[r][w], f[2 * w], f[2 * w + 1]);
+        a = fmaxf(a, fmaxf(fabsf(f[2 * w]), fabsf(f[2 * w + 1])));
+      }
+      const float s = row16_max(a) / kE4m3Max;
+      *reinterpret_cast<u32x2*>(codes + static_cast<size_t>(m) * pitch + 128 * b + 8 * (threadIdx.x & 15)) =
+          e4m3_codes(f, s, __builtin_amdgcn_rcpf(s));
+      if ((threadIdx.x & 15) == 0) scales[b * kMaxM + m] = s;
+    }
+  } else {
+    issue(fa, tile, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    const int per = blocks * 8;  // 16-byte pieces of a row, whole blocks
+    for (int q = threadIdx.x; q < M * per; q += kTh) {
+      const int m = q / per, c = q - m * per;
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (16 * c < K) v = *reinterpret_cast<const u32x4*>(xq + static_cast<size_t>(m) * K + 16 * c);
+      *reinterpret_cast<u32x4*>(codes + static_cast<size_t>(m) * pitch + 16 * c) = v;
+    }
+    for (int q = threadIdx.x; q < M * blocks; q += kTh) {
+      const int b = q / M, m = q - b * M;
+      scales[b * kMaxM + m] = s_x[q];
     }
   }
-  // Lane (j, h) register e of a tile holds channel 4 h + e of token j.
+  // scales of lanes past M: any finite value (their results are not stored)
+  for (int q = threadIdx.x; q < (kMaxM - M) * blocks; q += kTh) {
+    const int b = q / (kMaxM - M);
+    scales[b * kMaxM + M + (q - b * (kMaxM - M))] = 0.f;
+  }
+  wait_counts<63, 0>();  // LDS only: the first weight set stays in flight
+  bare_barrier();
+
+  // Ends a tile: the wavefronts' sums meet, every thread finishes its outputs.
+  // One barrier per tile: the sums alternate between two buffers.
+  int turn = 0;
+  auto finish = [&](int n0) {
 #pragma unroll
-  for (int t = 0; t < kT; ++t)
+    for (int e = 0; e < 4; ++e) part[turn][wave][i][4 * h + e] = acc[e];
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    wait_counts<63, 0>();
+    bare_barrier();
+    for (int o = threadIdx.x; o < 16 * M; o += kTh) {
+      const int m = o >> 4, n = o & 15;
+      float v = part[turn][0][m][n];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) part[wave][16 * t + i][4 * h + e] = acc[t][e];
-  __syncthreads();
-  for (int o = threadIdx.x; o < 256 * kT; o += 64 * kW) {
-    const int m = o >> 4, n = o & 15;
-    float v = part[0][m][n];
-#pragma unroll
-    for (int w = 1; w < kW; ++w) v += part[w][m][n];
-    if (m < M && n0 + n < N) y[static_cast<size_t>(m) * N + n0 + n] = half_bits<kBf16>(v);
+      for (int w = 1; w < kW; ++w) v += part[turn][w][m][n];
+      if (n0 + n < N) y[static_cast<size_t>(m) * N + n0 + n] = half_bits<kBf16>(v);
+    }
+    turn ^= 1;
+  };
+
+  // Sets of all tiles in one sequence, two at a time.
+  int set = 0;
+  auto advance = [&](int& t, int& s) {
+    if (++s == sets) {
+      s = 0;
+      t += step;
+    }
+  };
+  while (tile < tiles) {
+    int t1 = tile, s1 = set;
+    advance(t1, s1);
+    issue(fb, t1, s1);
+    __builtin_amdgcn_sched_barrier(0);
+    use(fa, set);
+    __builtin_amdgcn_sched_barrier(0);
+    if (s1 == 0) finish(16 * tile);
+    if (t1 >= tiles) break;
+    int t2 = t1, s2 = s1;
+    advance(t2, s2);
+    issue(fa, t2, s2);
+    __builtin_amdgcn_sched_barrier(0);
+    use(fb, s1);
+    __builtin_amdgcn_sched_barrier(0);
+    if (s2 == 0) finish(16 * t1);
+    tile = t2;
+    set = s2;
   }
 }
 
-template <int kW, int kU, int kT>
-hipError_t launch_tiles(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y, int M,
-                        int N, int K, bool bf16, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>((N + 15) / 16)), block(64 * kW);
-  if (bf16)
-    return launch_kernel(fp8_block_gemv_kernel<kW, kU, kT, true>, grid, block, 0, stream, xq, s_x, wq, s_w, y, M, N, K);
-  return launch_kernel(fp8_block_gemv_kernel<kW, kU, kT, false>, grid, block, 0, stream, xq, s_x, wq, s_w, y, M, N, K);
+// Workgroups of four wavefronts while two of them fit a CU's LDS, of eight
+// where the codes take more (one workgroup per CU) or where there are too few
+// tiles for two workgroups per CU. The grid is what the GPU holds at once.
+template <bool kFused, bool kBf16>
+hipError_t launch_gemv(const uint16_t* x, const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
+                       uint16_t* y, int M, int N, int K, hipStream_t stream) {
+  const int64_t lds = lds_bytes(M, K);
+  const int tiles = (N + 15) / 16;
+  const bool wide = lds > 64 * 1024 || tiles < 512;
+  const int64_t held = kCuLds / (lds + sizeof(float) * 2 * (wide ? 8 : 4) * kMaxM * 17);
+  const int64_t per_cu = held < 1 ? 1 : held > (wide ? 2 : 4) ? (wide ? 2 : 4) : held;
+  const int64_t cap = 256 * per_cu;
+  const dim3 grid(static_cast<uint32_t>(tiles < cap ? tiles : cap)), block(wide ? 512 : 256);
+  if (wide)
+    return launch_kernel(fp8_block_gemv_kernel<8, kFused, kBf16>, grid, block, static_cast<size_t>(lds), stream, x, xq,
+                         s_x, wq, s_w, y, M, N, K);
+  return launch_kernel(fp8_block_gemv_kernel<4, kFused, kBf16>, grid, block, static_cast<size_t>(lds), stream, x, xq,
+                       s_x, wq, s_w, y, M, N, K);
 }
 
 }  // namespace
 
-hipError_t launch_fp8_block_gemv(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
-                                 int64_t M, int64_t N, int64_t K, bool bf16, hipStream_t stream) {
-  if (M > kFp8GemvMaxM) return hipErrorInvalidValue;
+bool fp8_use_gemv(int64_t M, int64_t K) { return M <= kMaxM && lds_bytes(M, K) <= kGemvLds; }
+bool fp8_use_fused(int64_t M, int64_t K) { return fp8_use_gemv(M, K) && M * ((K + 127) / 128) <= kFusedUnits; }
+
+hipError_t launch_fp8_block_gemv(const uint16_t* x, const uint8_t* xq, const float* s_x, const uint8_t* wq,
+                                 const float* s_w, uint16_t* y, int64_t M, int64_t N, int64_t K, bool bf16,
+                                 hipStream_t stream) {
+  if (!fp8_use_gemv(M, K) || (x != nullptr && !fp8_use_fused(M, K))) return hipErrorInvalidValue;
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
-  if (M <= 16) return launch_tiles<8, 2, 1>(xq, s_x, wq, s_w, y, m, n, k, bf16, stream);
-  if (M <= 32) return launch_tiles<8, 2, 2>(xq, s_x, wq, s_w, y, m, n, k, bf16, stream);
-  return launch_tiles<8, 1, 4>(xq, s_x, wq, s_w, y, m, n, k, bf16, stream);
+  if (x != nullptr)
+    return bf16 ? launch_gemv<true, true>(x, xq, s_x, wq, s_w, y, m, n, k, stream)
+                : launch_gemv<true, false>(x, xq, s_x, wq, s_w, y, m, n, k, stream);
+  return bf16 ? launch_gemv<false, true>(x, xq, s_x, wq, s_w, y, m, n, k, stream)
+              : launch_gemv<false, false>(x, xq, s_x, wq, s_w, y, m, n, k, stream);
 }
 
 }  // namespace mq

@@ -1,5 +1,5 @@
-// e4m3 matrix product with one scale per block of 128, for gfx950 (more than
-// 64 tokens; fp8_block_gemv.hip takes the rest).
+// e4m3 matrix product with one scale per block of 128, for gfx950
+// (fp8_block_gemv.hip takes up to 16 tokens that fit LDS).
 //
 //   y[m,n] = rne16( sum_b (sx[b,m] * sw[n/128,b]) * sum_{k in block b} xq[m,k] * wq[n,k] )
 //
@@ -17,22 +17,32 @@
 //   multiply-add per value by the block's scale. That is 16 VALU operations
 //   (64 cycles) for 128 cycles of matrix unit, so a wavefront takes whole
 //   blocks (a split of a block's K over wavefronts would double the VALU work
-//   to parity with the MFMAs), and each SIMD has two wavefronts so that one's
-//   multiply-adds run under the other's MFMAs.
+//   to parity with the MFMAs), and each SIMD has two wavefronts or more so
+//   that one's multiply-adds run under another's MFMAs.
 // - Weight rows are the MFMA's A operand and token rows its B operand: a lane
 //   of the 32x32 result holds one token, so the scale sx * sw is one value
 //   per lane and tile (sw is uniform: a tile of 32 channels lies within one
 //   block of 128).
-// - Tiles move HBM -> LDS by buffer_load ... lds, one stage of 128 bytes of K
-//   ahead of the compute. LDS rows are 128 bytes, their 16-byte chunks
-//   XOR-swizzled by the row, so a fragment read of 32 rows meets no bank
-//   conflict. Loads past the buffer's end return zero (ragged M, N, K).
+// - Tiles move HBM -> LDS by buffer_load ... lds, one or more stages of 128
+//   bytes of K ahead of the compute. LDS rows are 128 bytes, their 16-byte
+//   chunks XOR-swizzled by the row, so a fragment read of 32 rows meets no
+//   bank conflict. Loads past the buffer's end return zero (ragged M, N, K).
 // - A lane's 32 bytes of a k-step are the chunks 4 t + h and 4 t + 2 + h of
 //   its row; which k a lane holds does not matter as long as both operands
-//   agree.
+//   agree (and 8 consecutive k stay together: the groups above).
+// - Four tile sizes, and for few tiles ranges of K whose binary32 sums a
+//   second kernel adds in order (plan_fp8_block_mm says when).
 // - Workgroups go round-robin over the 8 XCDs; each XCD gets a contiguous run
 //   of tiles in groups of kGroupM token tiles, so that what a run shares stays
 //   in its L2.
+//
+// What bounds it, at 4096 tokens x 4096 x 24576 (256 x 256 tiles, 415 us, 1.99
+// PFLOP/s): the matrix unit is busy 45% of the time. Without the multiply-adds
+// the call takes 380 us, without the fills 343; the rest is the start of every
+// stage, when all wavefronts meet at the barrier and wait for their first
+// fragments. Reading the next stage's fragments before the barrier (possible
+// for the smaller tiles, which have the registers) changed nothing there: they
+// are bound by the fills, about 60 GB/s per CU.
 #include "device_common.h"
 #include "launch.h"
 
@@ -45,9 +55,7 @@ typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
 typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
-constexpr int kBK = 128;  // bytes of K per stage: one scale block
-constexpr int kWaves = 8;
-constexpr int kThreads = kWaves * 64;
+constexpr int kBK = 128;                  // bytes of K per stage: one scale block
 constexpr int kGroupM = 4;                // token tiles per group in the tile order
 constexpr uint32_t kOob = 0x80000000u;    // a buffer offset past every tile: the load returns 0
 constexpr int kBufferFlags = 0x00020000;  // gfx9 buffer descriptor word 3 (raw 32-bit data)
@@ -58,33 +66,43 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const uint8_t* bas
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, bytes, kBufferFlags);
 }
 
-// A workgroup computes BM tokens x BN channels; its eight wavefronts stand WM
-// x WN over it, each with a tile of 32 TB tokens x 32 TA channels.
-template <int BM, int BN, int WM>
+// A workgroup computes BM tokens x BN channels over a range of stages; its
+// WM x WN wavefronts stand over the tile, each with 32 TB tokens x 32 TA
+// channels. SLOTS stages of LDS: SLOTS - 1 are in flight or waiting while one
+// is computed.
+template <int BM_, int BN_, int WM_, int WN_, int SLOTS_>
 struct Shape {
-  static constexpr int WN = kWaves / WM;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kSlots = SLOTS_;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int TB = BM / WM / 32, TA = BN / WN / 32;
   static constexpr int kStage = (BM + BN) * kBK;
-  static constexpr int kSlots = 3 * kStage <= 150 * 1024 ? 3 : 2;
   static constexpr int kPitch = BN * 2 + 16;  // staged output rows
   static constexpr int kLds = kSlots * kStage > BM * kPitch ? kSlots * kStage : BM * kPitch;
-  static constexpr int kLoads = (BM + BN) / 8 / kWaves;  // fills per wavefront and stage (8 rows of 128 bytes each)
+  static constexpr int kLoadsX = BM / 8 / kWaves;              // fills per wavefront and stage (8 rows of 128 bytes each)
+  static constexpr int kLoads = kLoadsX + BN / 8 / kWaves;
+  static constexpr int kAhead = (kSlots - 2) * kLoads;         // fills that may be in flight at a round's end
   static_assert(kLds <= 160 * 1024, "LDS capacity");
-  static_assert(TA >= 1 && TB >= 1 && (BM + BN) % (8 * kWaves) == 0 && BN % 128 == 0, "tile shape");
-  static_assert(BM % (8 * kWaves) == 0, "a wavefront's fills do not straddle the operands");
+  static_assert(TA >= 1 && TB >= 1 && BM == 32 * TB * WM && BN == 32 * TA * WN, "wavefront tiles");
+  static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "a wavefront's fills do not straddle the operands");
+  static_assert(128 % BN == 0 || BN % 128 == 0, "a tile of 32 channels lies in one scale block");
+  static_assert(kAhead < 63, "vmcnt range");
 };
 
-template <int BM, int BN, int WM, bool kBf16>
-__global__ __launch_bounds__(kThreads) void fp8_block_mm_kernel(
+// kSplit: the stages of a tile are cut into `splits` contiguous ranges of
+// `share`, one workgroup each, whose binary32 sums go to part[split][M][N].
+template <typename S, bool kSplit, bool kBf16>
+__global__ __launch_bounds__(S::kThreads) void fp8_block_mm_kernel(
     const uint8_t* __restrict__ xq, const float* __restrict__ s_x, const uint8_t* __restrict__ wq,
-    const float* __restrict__ s_w, uint16_t* __restrict__ y, int M, int N, int K, int tiles_m, int tiles_n,
-    int per_xcd) {
-  typedef Shape<BM, BN, WM> S;
+    const float* __restrict__ s_w, uint16_t* __restrict__ y, float* __restrict__ part, int M, int N, int K,
+    int tiles_m, int tiles_n, int per_xcd, int splits, int share) {
+  constexpr int BM = S::BM, BN = S::BN, kWaves = S::kWaves, kLoadsX = S::kLoadsX;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S::kLds];
   lds_u8* const sm = (lds_u8*)(smem);
 
-  const int t_id = static_cast<int>(blockIdx.x & 7) * per_xcd + static_cast<int>(blockIdx.x >> 3);
-  if (t_id >= tiles_m * tiles_n) return;
+  int t_id = static_cast<int>(blockIdx.x & 7) * per_xcd + static_cast<int>(blockIdx.x >> 3);
+  if (t_id >= tiles_m * tiles_n * splits) return;
+  const int split = kSplit ? t_id % splits : 0;
+  if (kSplit) t_id /= splits;
   const int group_tiles = kGroupM * tiles_n;
   const int tgroup = t_id / group_tiles;
   const int first_m = tgroup * kGroupM;
@@ -101,31 +119,34 @@ __global__ __launch_bounds__(kThreads) void fp8_block_mm_kernel(
   const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(xq + static_cast<size_t>(m0) * K, min(BM, M - m0) * K);
   const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(wq + static_cast<size_t>(n0) * K, min(BN, N - n0) * K);
 
-  // Fill l covers tile rows 8 (wave + 8 l) .. + 7 (token rows first, then
-  // channel rows); lane L writes physical chunk L % 8 of row L / 8, so it
-  // fetches the logical chunk that the swizzle places there.
-  constexpr int kLoadsX = BM / 8 / kWaves;
-  uint32_t loff[S::kLoads];
-  int lk[S::kLoads];
+  // Scales: this lane's token of each 32-token tile (tokens past M take the
+  // last one's; their results are not stored), this wavefront's channel block.
+  const int blocks = (K + kBK - 1) / kBK;
+  const int first = kSplit ? split * share : 0, nst = kSplit ? min(share, blocks - first) : blocks;
+  int tok[S::TB];
 #pragma unroll
-  for (int l = 0; l < S::kLoads; ++l) {
-    const int row = 8 * (wave + kWaves * (l < kLoadsX ? l : l - kLoadsX)) + (lane >> 3);
-    lk[l] = 16 * ((lane & 7) ^ chunk_swizzle(row));
-    loff[l] = static_cast<uint32_t>(row * K + lk[l]);
-  }
+  for (int b = 0; b < S::TB; ++b) tok[b] = min(m0 + wm * 32 * S::TB + 32 * b + fi, M - 1);
+  int nblk[S::TA];
+#pragma unroll
+  for (int a = 0; a < S::TA; ++a) nblk[a] = min(n0 + wn * 32 * S::TA + 32 * a, N - 1) / 128;
+
+  // Fill l covers rows 8 (wave + kWaves l) .. + 7 of its operand's tile; lane L
+  // writes physical chunk L % 8 of row L / 8, so it fetches the logical chunk
+  // that the swizzle places there. The swizzle repeats every 16 rows, so the
+  // fills of a lane differ by whole rows only.
+  const int frow = 8 * wave + (lane >> 3);
+  const int fk = 16 * ((lane & 7) ^ chunk_swizzle(frow));
+  const uint32_t foff = static_cast<uint32_t>(frow * K + fk);
   auto fill = [&](int s) {
-    const int k0 = s * kBK;
-    const int krem = K - k0;
-    lds_u8* const dst = sm + (s % S::kSlots) * S::kStage;
+    const int k0 = (first + s) * kBK;
+    const uint32_t base = fk < K - k0 ? foff : kOob;
+    lds_u8* const dst = sm + (s % S::kSlots) * S::kStage + wave * 1024;
 #pragma unroll
     for (int l = 0; l < S::kLoads; ++l) {
-      const uint32_t off = lk[l] < krem ? loff[l] + k0 : kOob;
-      if (l < kLoadsX) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(dst + (wave + kWaves * l) * 1024), 16, off, 0, 0, 0);
-      } else {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rw, (lds_void*)(dst + BM * kBK + (wave + kWaves * (l - kLoadsX)) * 1024), 16, off, 0, 0, 0);
-      }
+      const int u = l < kLoadsX ? l : l - kLoadsX;
+      const uint32_t off = base + static_cast<uint32_t>(8 * kWaves * u * K + k0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          l < kLoadsX ? rx : rw, (lds_void*)(dst + (l < kLoadsX ? 0 : BM * kBK) + kWaves * u * 1024), 16, off, 0, 0, 0);
     }
   };
 
@@ -136,16 +157,6 @@ __global__ __launch_bounds__(kThreads) void fp8_block_mm_kernel(
   const int xrow = (wm * 32 * S::TB + fi) * kBK;
   const int wrow = BM * kBK + (wn * 32 * S::TA + fi) * kBK;
 
-  // Scales: this lane's token of each 32-token tile (tokens past M take the
-  // last one's; their results are not stored), this wavefront's channel block.
-  const int nst = (K + kBK - 1) / kBK;
-  int tok[S::TB];
-#pragma unroll
-  for (int b = 0; b < S::TB; ++b) tok[b] = min(m0 + wm * 32 * S::TB + 32 * b + fi, M - 1);
-  int nblk[S::TA];
-#pragma unroll
-  for (int a = 0; a < S::TA; ++a) nblk[a] = min(n0 + wn * 32 * S::TA + 32 * a, N - 1) / 128;
-
   f32x16 acc[S::TA][S::TB];
 #pragma unroll
   for (int a = 0; a < S::TA; ++a)
@@ -154,75 +165,143 @@ __global__ __launch_bounds__(kThreads) void fp8_block_mm_kernel(
 
   float sx[S::TB], sw[S::TA], sxn[S::TB], swn[S::TA];
 #pragma unroll
-  for (int b = 0; b < S::TB; ++b) sx[b] = s_x[tok[b]];
+  for (int b = 0; b < S::TB; ++b) sx[b] = s_x[static_cast<size_t>(first) * M + tok[b]];
 #pragma unroll
-  for (int a = 0; a < S::TA; ++a) sw[a] = s_w[static_cast<size_t>(nblk[a]) * nst];
+  for (int a = 0; a < S::TA; ++a) sw[a] = s_w[static_cast<size_t>(nblk[a]) * blocks + first];
 
-  fill(0);
-  if (S::kSlots > 2 && nst > 1) fill(1);
-  if (S::kSlots > 2 && nst > 1) {
-    wait_counts<S::kLoads, 0>();
+#pragma unroll
+  for (int s = 0; s < S::kSlots - 1; ++s)
+    if (s < nst) fill(s);
+  if (S::kSlots - 1 <= nst) {
+    wait_counts<S::kAhead, 0>();
   } else {
     wait_counts<0, 0>();
   }
   bare_barrier();
 
-  // Round s: the scales of stage s + 1 and the fill of the stage kSlots - 1
-  // ahead go out (into the slot that every wavefront finished reading before
-  // the barrier that ended round s - 1), stage s is computed, and the
-  // wavefront waits for its own share of stage s + 1 before the barrier.
-  for (int s = 0; s < nst; ++s) {
+  auto fragment = [&](int slot, int at, int t) {
+    const lds_u8* const src = sm + slot * S::kStage + at;
+    const i32x4 lo = *(const lds_i32x4*)(src + coff[2 * t]);
+    const i32x4 hi = *(const lds_i32x4*)(src + coff[2 * t + 1]);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto product = [&](const i32x8 (&w)[2], const i32x8 (&x)[2]) {
+    f32x16 v = f32x16{};
+    v = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[0], x[0], v, 0, 0, 0, 0, 0, 0);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[1], x[1], v, 0, 0, 0, 0, 0, 0);
+  };
+  auto add = [&](int a, int b, const f32x16& v) {
+    const float sc = sx[b] * sw[a];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[a][b][i] = fmaf(v[i], sc, acc[a][b][i]);
+  };
+  // What every round s begins with: the scales of stage s + 1 and the fill of
+  // the stage kSlots - 1 ahead, into the slot that every wavefront finished
+  // reading before the barrier that ended round s - 1.
+  auto begin = [&](int s) {
     const int s1 = min(s + 1, nst - 1);
 #pragma unroll
-    for (int b = 0; b < S::TB; ++b) sxn[b] = s_x[static_cast<size_t>(s1) * M + tok[b]];
+    for (int b = 0; b < S::TB; ++b) sxn[b] = s_x[static_cast<size_t>(first + s1) * M + tok[b]];
 #pragma unroll
-    for (int a = 0; a < S::TA; ++a) swn[a] = s_w[static_cast<size_t>(nblk[a]) * nst + s1];
-    const bool more = s + S::kSlots - 1 < nst;
-    if (more) fill(s + S::kSlots - 1);
-
-    const lds_u8* const src = sm + (s % S::kSlots) * S::kStage;
-    i32x8 fw[S::TA][2];
-#pragma unroll
-    for (int a = 0; a < S::TA; ++a)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const i32x4 lo = *(const lds_i32x4*)(src + wrow + a * 32 * kBK + coff[2 * t]);
-        const i32x4 hi = *(const lds_i32x4*)(src + wrow + a * 32 * kBK + coff[2 * t + 1]);
-        fw[a][t] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      }
-#pragma unroll
-    for (int b = 0; b < S::TB; ++b) {
-      i32x8 fx[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const i32x4 lo = *(const lds_i32x4*)(src + xrow + b * 32 * kBK + coff[2 * t]);
-        const i32x4 hi = *(const lds_i32x4*)(src + xrow + b * 32 * kBK + coff[2 * t + 1]);
-        fx[t] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      }
-#pragma unroll
-      for (int a = 0; a < S::TA; ++a) {
-        f32x16 p = f32x16{};
-        p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[a][0], fx[0], p, 0, 0, 0, 0, 0, 0);
-        p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[a][1], fx[1], p, 0, 0, 0, 0, 0, 0);
-        const float sc = sx[b] * sw[a];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[a][b][i] = fmaf(p[i], sc, acc[a][b][i]);
-      }
-    }
+    for (int a = 0; a < S::TA; ++a) swn[a] = s_w[static_cast<size_t>(nblk[a]) * blocks + first + s1];
+    if (s + S::kSlots - 1 < nst) fill(s + S::kSlots - 1);
+  };
+  // And ends with: this wavefront's share of the next stage needed is there.
+  auto end = [&](int s) {
 #pragma unroll
     for (int b = 0; b < S::TB; ++b) sx[b] = sxn[b];
 #pragma unroll
     for (int a = 0; a < S::TA; ++a) sw[a] = swn[a];
-    if (S::kSlots > 2 && more) {
-      wait_counts<S::kLoads, 0>();
+    if (s + S::kSlots - 1 < nst) {
+      wait_counts<S::kAhead, 0>();
     } else {
       wait_counts<0, 0>();
     }
     bare_barrier();
+  };
+
+  if constexpr (S::TA * S::TB <= 4) {
+    for (int s = 0; s < nst; ++s) {
+      begin(s);
+      const int slot = s % S::kSlots;
+      i32x8 fw[S::TA][2], fx[S::TB][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int a = 0; a < S::TA; ++a) fw[a][t] = fragment(slot, wrow + a * 32 * kBK, t);
+#pragma unroll
+        for (int b = 0; b < S::TB; ++b) fx[b][t] = fragment(slot, xrow + b * 32 * kBK, t);
+      }
+#pragma unroll
+      for (int a = 0; a < S::TA; ++a)
+#pragma unroll
+        for (int b = 0; b < S::TB; ++b) add(a, b, product(fw[a], fx[b]));
+      end(s);
+    }
+  } else {
+    // Large wavefront tiles: the next token tile's fragments are read under
+    // this one's MFMAs, a tile's multiply-adds follow the next tile's MFMAs.
+    // The fences and the empty statement hold that order: left alone the
+    // compiler moves every multiply-add behind the round, where the products
+    // no longer fit the registers.
+    for (int s = 0; s < nst; ++s) {
+      begin(s);
+      const int slot = s % S::kSlots;
+      i32x8 fw[S::TA][2], fx[2][2];
+      f32x16 p[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int a = 0; a < S::TA; ++a) fw[a][t] = fragment(slot, wrow + a * 32 * kBK, t);
+        fx[0][t] = fragment(slot, xrow, t);
+      }
+#pragma unroll
+      for (int at = 0; at < S::TA * S::TB; ++at) {
+        const int b = at / S::TA, a = at % S::TA;
+        if (a == 0 && b + 1 < S::TB) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) fx[(b + 1) & 1][t] = fragment(slot, xrow + (b + 1) * 32 * kBK, t);
+        }
+        p[at & 1] = product(fw[a], fx[b & 1]);
+        if (at > 0) {
+          const int b1 = (at - 1) / S::TA, a1 = (at - 1) % S::TA;
+          add(a1, b1, p[(at - 1) & 1]);
+          asm volatile("" : "+v"(acc[a1][b1]));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      add(S::TA - 1, S::TB - 1, p[(S::TA * S::TB - 1) & 1]);
+      end(s);
+    }
   }
 
   // Lane (j, h) register r of a tile holds channel 8 (r / 4) + 4 h + r % 4 of
-  // token j: staged in LDS as rows of 16-bit outputs, written out whole.
+  // token j.
+  if constexpr (kSplit) {
+#pragma unroll
+    for (int b = 0; b < S::TB; ++b) {
+      const int m = m0 + wm * 32 * S::TB + 32 * b + fi;
+      if (m >= M) continue;
+      float* const row = part + (static_cast<size_t>(split) * M + m) * N;
+#pragma unroll
+      for (int a = 0; a < S::TA; ++a)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = n0 + wn * 32 * S::TA + 32 * a + 8 * q + 4 * fh;
+          if ((N & 3) == 0) {
+            if (n < N)
+              *reinterpret_cast<f32x4*>(row + n) =
+                  f32x4{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (n + i < N) row[n + i] = acc[a][b][4 * q + i];
+          }
+        }
+    }
+    return;
+  }
+  // Staged in LDS as rows of 16-bit outputs, written out whole.
 #pragma unroll
   for (int a = 0; a < S::TA; ++a)
 #pragma unroll
@@ -241,7 +320,7 @@ __global__ __launch_bounds__(kThreads) void fp8_block_mm_kernel(
   const int c = threadIdx.x % kPieces;
   const int n = n0 + 8 * c;
   const bool whole = (N & 7) == 0;  // rows start 16-byte aligned; a piece is all in or all out
-  for (int rr = threadIdx.x / kPieces; rr < BM; rr += kThreads / kPieces) {
+  for (int rr = threadIdx.x / kPieces; rr < BM; rr += S::kThreads / kPieces) {
     const int m = m0 + rr;
     if (m >= M || n >= N) continue;
     const u32x4 v = *(const lds_u32x4*)(sm + rr * S::kPitch + c * 16);
@@ -258,32 +337,118 @@ __global__ __launch_bounds__(kThreads) void fp8_block_mm_kernel(
   }
 }
 
-template <int BM, int BN, int WM>
-hipError_t launch_shape(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y, int M,
-                        int N, int K, bool bf16, hipStream_t stream) {
-  const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
-  const int64_t tiles = static_cast<int64_t>(tiles_m) * tiles_n;
-  if (tiles > (1 << 22)) return hipErrorInvalidValue;
-  const int per_xcd = static_cast<int>((tiles + 7) / 8);
-  const dim3 grid(static_cast<uint32_t>(8 * per_xcd)), block(kThreads);
-  if (bf16)
-    return launch_kernel(fp8_block_mm_kernel<BM, BN, WM, true>, grid, block, 0, stream, xq, s_x, wq, s_w, y, M, N, K,
-                         tiles_m, tiles_n, per_xcd);
-  return launch_kernel(fp8_block_mm_kernel<BM, BN, WM, false>, grid, block, 0, stream, xq, s_x, wq, s_w, y, M, N, K,
-                       tiles_m, tiles_n, per_xcd);
+// Adds the splits of every output in split order.
+template <bool kBf16>
+__global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__ part, uint16_t* __restrict__ y,
+                                                       int64_t outputs, int splits) {
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (at + 4 <= outputs && (outputs & 3) == 0) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(part + at);
+    for (int z = 1; z < splits; ++z) {
+      const f32x4 p = *reinterpret_cast<const f32x4*>(part + z * outputs + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += p[i];
+    }
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = half_bits<kBf16>(v[i]);
+    *reinterpret_cast<u32x2*>(y + at) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+    return;
+  }
+  for (int64_t o = at; o < at + 4 && o < outputs; ++o) {
+    float v = part[o];
+    for (int z = 1; z < splits; ++z) v += part[z * outputs + o];
+    y[o] = half_bits<kBf16>(v);
+  }
 }
+
+template <typename S>
+hipError_t launch_shape(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y, int M,
+                        int N, int K, int splits, float* part, bool bf16, hipStream_t stream) {
+  const int tiles_m = (M + S::BM - 1) / S::BM, tiles_n = (N + S::BN - 1) / S::BN;
+  const int blocks = (K + kBK - 1) / kBK, share = (blocks + splits - 1) / splits;
+  const int64_t units = static_cast<int64_t>(tiles_m) * tiles_n * splits;
+  if (units > (1 << 22) || share * (splits - 1) >= blocks) return hipErrorInvalidValue;
+  const int per_xcd = static_cast<int>((units + 7) / 8);
+  const dim3 grid(static_cast<uint32_t>(8 * per_xcd)), block(S::kThreads);
+  if (splits == 1) {
+    if (bf16)
+      return launch_kernel(fp8_block_mm_kernel<S, false, true>, grid, block, 0, stream, xq, s_x, wq, s_w, y, part, M, N,
+                           K, tiles_m, tiles_n, per_xcd, 1, blocks);
+    return launch_kernel(fp8_block_mm_kernel<S, false, false>, grid, block, 0, stream, xq, s_x, wq, s_w, y, part, M, N,
+                         K, tiles_m, tiles_n, per_xcd, 1, blocks);
+  }
+  const hipError_t e = launch_kernel(fp8_block_mm_kernel<S, true, false>, grid, block, 0, stream, xq, s_x, wq, s_w, y,
+                                     part, M, N, K, tiles_m, tiles_n, per_xcd, splits, share);
+  if (e != hipSuccess) return e;
+  const int64_t outputs = static_cast<int64_t>(M) * N;
+  const dim3 jgrid(static_cast<uint32_t>((outputs + 1023) / 1024));
+  if (bf16) return launch_kernel(fp8_join_kernel<true>, jgrid, dim3(256), 0, stream, part, y, outputs, splits);
+  return launch_kernel(fp8_join_kernel<false>, jgrid, dim3(256), 0, stream, part, y, outputs, splits);
+}
+
+typedef Shape<256, 256, 2, 4, 2> Big;
+typedef Shape<128, 128, 2, 4, 2> Mid;   // two workgroups per CU
+typedef Shape<64, 128, 2, 4, 3> Low;    // two
+typedef Shape<64, 64, 2, 2, 4> Small;   // two
 
 }  // namespace
 
+// Which tile, and how many ranges of K. A tile's stages cost the more the
+// larger it is, a launch takes as many of them as its fullest CU holds, and
+// splitting K adds a second kernel and the sums' way through memory. The
+// figures (microseconds) are fitted to timed launches of every form over 17 to
+// 4096 tokens: per stage with one workgroup on a CU, with two of them, and the
+// fixed part. For example 48 tokens at K = 12288, N = 4096: 64 x 64 tiles in 8
+// ranges 19 us, 64 x 128 in 8 20 us, unsplit over 45; 1000 tokens at 4096 x
+// 4096: 64 x 128 26.6, 128 x 128 30, 64 x 64 36, 256 x 256 over 100; 4096 tokens
+// at 4096 x 24576: 256 x 256 415, 128 x 128 490, 64 x 128 620, 64 x 64 900.
+Fp8Plan plan_fp8_block_mm(int64_t M, int64_t N, int64_t K) {
+  Fp8Plan p = {Fp8Form::kGemv, 1, 0};
+  if (fp8_use_gemv(M, K)) return p;
+  struct Cost {
+    Fp8Form form;
+    int bm, bn;
+    double one, two;
+  };
+  constexpr Cost kCosts[] = {{Fp8Form::kBig, 256, 256, 2.1, 4.2},
+                             {Fp8Form::kMid, 128, 128, 0.80, 1.07},
+                             {Fp8Form::kLow, 64, 128, 0.47, 0.70},
+                             {Fp8Form::kSmall, 64, 64, 0.36, 0.47}};
+  const int64_t blocks = (K + kBK - 1) / kBK;
+  double best = 1e300;
+  for (const Cost& c : kCosts) {
+    const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+    for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      const int64_t share = (blocks + splits - 1) / splits;
+      if (splits > 1 && (share * (splits - 1) >= blocks || tiles * splits > 1024)) break;
+      const int64_t on = (tiles * splits + 255) / 256;  // workgroups of the fullest CU
+      double t = static_cast<double>(share) * (static_cast<double>(on / 2) * c.two + static_cast<double>(on % 2) * c.one);
+      if (splits > 1) t += 3.0 + static_cast<double>(splits) * static_cast<double>(M * N) * 2e-6;
+      if (t < best) {
+        best = t;
+        p.form = c.form;
+        p.splits = splits;
+      }
+    }
+  }
+  if (p.splits > 1) p.workspace_bytes = static_cast<size_t>(p.splits) * static_cast<size_t>(M * N) * sizeof(float);
+  return p;
+}
+
 hipError_t launch_fp8_block_mm(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
-                               int64_t M, int64_t N, int64_t K, bool bf16, hipStream_t stream) {
-  if (M <= kFp8GemvMaxM) return launch_fp8_block_gemv(xq, s_x, wq, s_w, y, M, N, K, bf16, stream);
+                               int64_t M, int64_t N, int64_t K, const Fp8Plan& plan, void* workspace, bool bf16,
+                               hipStream_t stream) {
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
-  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
-  if (big >= 200) return launch_shape<256, 256, 2>(xq, s_x, wq, s_w, y, m, n, k, bf16, stream);
-  const int64_t mid = ((M + 255) / 256) * ((N + 127) / 128);
-  if (mid >= 200) return launch_shape<256, 128, 4>(xq, s_x, wq, s_w, y, m, n, k, bf16, stream);
-  return launch_shape<64, 128, 2>(xq, s_x, wq, s_w, y, m, n, k, bf16, stream);
+  float* const part = static_cast<float*>(workspace);
+  switch (plan.form) {
+    case Fp8Form::kGemv: return launch_fp8_block_gemv(nullptr, xq, s_x, wq, s_w, y, M, N, K, bf16, stream);
+    case Fp8Form::kBig: return launch_shape<Big>(xq, s_x, wq, s_w, y, m, n, k, plan.splits, part, bf16, stream);
+    case Fp8Form::kMid: return launch_shape<Mid>(xq, s_x, wq, s_w, y, m, n, k, plan.splits, part, bf16, stream);
+    case Fp8Form::kLow: return launch_shape<Low>(xq, s_x, wq, s_w, y, m, n, k, plan.splits, part, bf16, stream);
+    case Fp8Form::kSmall: return launch_shape<Small>(xq, s_x, wq, s_w, y, m, n, k, plan.splits, part, bf16, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace mq

@@ -60,11 +60,24 @@ hipError_t launch_quant_fp8_blocks(const uint16_t* x, uint8_t* codes, float* sca
 // y[M, N] = xq[M, K] . wq[N, K]^T, both e4m3 with scales per block of 128
 // (s_x [ceil(K / 128), M], s_w [ceil(N / 128), ceil(K / 128)]); the decode
 // form for M <= kFp8GemvMaxM.
-constexpr int64_t kFp8GemvMaxM = 64;
+enum class Fp8Form { kGemv, kSmall, kLow, kMid, kBig };
+struct Fp8Plan {
+  Fp8Form form;
+  int splits;              // ranges of K, each a workgroup's; their sums meet in the workspace
+  size_t workspace_bytes;  // 0 without splits
+};
+Fp8Plan plan_fp8_block_mm(int64_t M, int64_t N, int64_t K);
 hipError_t launch_fp8_block_mm(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
-                               int64_t M, int64_t N, int64_t K, bool bf16, hipStream_t stream);
-hipError_t launch_fp8_block_gemv(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
-                                 int64_t M, int64_t N, int64_t K, bool bf16, hipStream_t stream);
+                               int64_t M, int64_t N, int64_t K, const Fp8Plan& plan, void* workspace, bool bf16,
+                               hipStream_t stream);
+
+// The form for few tokens whose codes fit LDS; with x (and without xq, s_x) it
+// quantizes the rows itself, to the same bits, where fp8_use_fused says.
+bool fp8_use_gemv(int64_t M, int64_t K);
+bool fp8_use_fused(int64_t M, int64_t K);
+hipError_t launch_fp8_block_gemv(const uint16_t* x, const uint8_t* xq, const float* s_x, const uint8_t* wq,
+                                 const float* s_w, uint16_t* y, int64_t M, int64_t N, int64_t K, bool bf16,
+                                 hipStream_t stream);
 
 // The paged e4m3 KV cache: K pages [page, head_dim] and V pages
 // [head_dim, page] for every (page, kv head), one binary32 scale each; the

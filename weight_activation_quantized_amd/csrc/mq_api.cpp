@@ -660,16 +660,30 @@ mq_status mq_quant_fp8_blocks_bf16(const uint16_t* x, uint8_t* xq, float* s_x, i
 constexpr int64_t kMaxFp8Dim = int64_t{1} << 26;    // M, N of the e4m3 product (launch size)
 constexpr int64_t kMaxFp8Out = int64_t{1} << 36;    // M * N of it
 
+static bool fp8_mm_sizes(int64_t M, int64_t N, int64_t K) {
+  return M >= 0 && M <= kMaxFp8Dim && N >= 0 && N <= kMaxFp8Dim && K >= 16 && K <= kMaxK && K % 16 == 0 &&
+         M * N <= kMaxFp8Out && M * K <= kMaxElems && K * N <= kMaxElems;
+}
+
 static mq_status check_fp8_mm(int64_t M, int64_t N, int64_t K) {
   MQ_TRY(check_mk(M, K, 16, kMaxK, 16));
   if (M > kMaxFp8Dim) return fail(MQ_ERR_SHAPE, "M=%lld out of range", (long long)M);
   if (N < 0 || N > kMaxFp8Dim) return fail(MQ_ERR_SHAPE, "N=%lld out of range", (long long)N);
-  if (M * N > kMaxFp8Out || K * N > kMaxElems) return fail(MQ_ERR_SHAPE, "problem too large");
+  if (!fp8_mm_sizes(M, N, K)) return fail(MQ_ERR_SHAPE, "problem too large");
+  return MQ_OK;
+}
+
+static mq_status check_workspace(const void* workspace, size_t given, size_t needed) {
+  if (needed == 0) return MQ_OK;
+  if (!workspace || given < needed)
+    return fail(MQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", needed, workspace ? given : static_cast<size_t>(0));
+  if (!aligned(workspace, 16)) return fail(MQ_ERR_ALIGN, "workspace must be 16-byte aligned");
   return MQ_OK;
 }
 
 static mq_status fp8_mm_impl(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
-                             int64_t M, int64_t N, int64_t K, bool bf16, void* stream) {
+                             int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, bool bf16,
+                             void* stream) {
   MQ_TRY(check_fp8_mm(M, N, K));
   MQ_TRY(need(xq, M * K, "xq"));
   MQ_TRY(need(s_x, M, "s_x"));
@@ -679,30 +693,56 @@ static mq_status fp8_mm_impl(const uint8_t* xq, const float* s_x, const uint8_t*
   if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(y, 16))
     return fail(MQ_ERR_ALIGN, "xq, wq and y must be 16-byte aligned");
   if (!aligned(s_x, 4) || !aligned(s_w, 4)) return fail(MQ_ERR_ALIGN, "s_x and s_w must be 4-byte aligned");
+  const bool empty = M == 0 || N == 0;
+  const mq::Fp8Plan plan = empty ? mq::Fp8Plan{} : mq::plan_fp8_block_mm(M, N, K);
+  MQ_TRY(check_workspace(workspace, workspace_bytes, plan.workspace_bytes));
   const Range in[] = {{xq, static_cast<size_t>(M * K), "xq"},
                       {s_x, static_cast<size_t>(M) * blocks_of(K) * 4, "s_x"},
                       {wq, static_cast<size_t>(N * K), "wq"},
                       {s_w, blocks_of(N) * blocks_of(K) * 4, "s_w"}};
-  const Range out[] = {{y, static_cast<size_t>(M * N) * 2, "y"}};
+  const Range out[] = {{y, static_cast<size_t>(M * N) * 2, "y"}, {workspace, plan.workspace_bytes, "workspace"}};
   MQ_TRY(check_alias(in, out));
-  if (M == 0 || N == 0) return ok();
-  return hip_status(mq::launch_fp8_block_mm(xq, s_x, wq, s_w, y, M, N, K, bf16, as_stream(stream)),
+  if (empty) return ok();
+  return hip_status(mq::launch_fp8_block_mm(xq, s_x, wq, s_w, y, M, N, K, plan, workspace, bf16, as_stream(stream)),
                     "fp8_block_mm launch");
 }
 
+size_t mq_fp8_block_mm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (!fp8_mm_sizes(M, N, K) || M == 0 || N == 0) return 0;
+  return mq::plan_fp8_block_mm(M, N, K).workspace_bytes;
+}
+
 mq_status mq_fp8_block_mm(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
-                          int64_t M, int64_t N, int64_t K, void* stream) {
-  return fp8_mm_impl(xq, s_x, wq, s_w, y, M, N, K, false, stream);
+                          int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  return fp8_mm_impl(xq, s_x, wq, s_w, y, M, N, K, workspace, workspace_bytes, false, stream);
 }
 
 mq_status mq_fp8_block_mm_bf16(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w, uint16_t* y,
-                               int64_t M, int64_t N, int64_t K, void* stream) {
-  return fp8_mm_impl(xq, s_x, wq, s_w, y, M, N, K, true, stream);
+                               int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  return fp8_mm_impl(xq, s_x, wq, s_w, y, M, N, K, workspace, workspace_bytes, true, stream);
 }
 
-size_t mq_fp8_linear_workspace_bytes(int64_t M, int64_t K) {
-  if (M < 1 || M > kMaxFp8Dim || K < 16 || K > kMaxK || K % 16 || M * K > kMaxElems) return 0;
-  return (static_cast<size_t>(M * K) + 255) / 256 * 256 + static_cast<size_t>(M) * blocks_of(K) * 4;
+// fp8_linear's workspace: the codes, the scales, the product's own part. None
+// where one kernel does it all.
+struct Fp8LinearPlan {
+  mq::Fp8Plan mm;
+  bool fused;
+  size_t scales_at, mm_at, bytes;
+};
+static Fp8LinearPlan fp8_linear_plan(int64_t M, int64_t N, int64_t K) {
+  Fp8LinearPlan p = {};
+  if (M == 0 || N == 0) return p;
+  p.mm = mq::plan_fp8_block_mm(M, N, K);
+  p.fused = mq::fp8_use_fused(M, K);
+  if (p.fused) return p;
+  p.scales_at = (static_cast<size_t>(M * K) + 255) / 256 * 256;
+  p.mm_at = (p.scales_at + static_cast<size_t>(M) * blocks_of(K) * 4 + 255) / 256 * 256;
+  p.bytes = p.mm_at + p.mm.workspace_bytes;
+  return p;
+}
+
+size_t mq_fp8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return fp8_mm_sizes(M, N, K) ? fp8_linear_plan(M, N, K).bytes : 0;
 }
 
 static mq_status fp8_linear_impl(const uint16_t* x, const uint8_t* wq, const float* s_w, uint16_t* y, int64_t M,
@@ -717,21 +757,22 @@ static mq_status fp8_linear_impl(const uint16_t* x, const uint8_t* wq, const flo
   if (!aligned(x, 16) || !aligned(wq, 16) || !aligned(y, 16))
     return fail(MQ_ERR_ALIGN, "x, wq and y must be 16-byte aligned");
   if (!aligned(s_w, 4)) return fail(MQ_ERR_ALIGN, "s_w must be 4-byte aligned");
-  const size_t ws = mq_fp8_linear_workspace_bytes(M, K);
-  if (ws > 0 && (!workspace || workspace_bytes < ws))
-    return fail(MQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", ws,
-                workspace ? workspace_bytes : static_cast<size_t>(0));
-  if (!aligned(workspace, 16)) return fail(MQ_ERR_ALIGN, "workspace must be 16-byte aligned");
+  const Fp8LinearPlan plan = fp8_linear_plan(M, N, K);
+  MQ_TRY(check_workspace(workspace, workspace_bytes, plan.bytes));
   const Range in[] = {{x, static_cast<size_t>(M * K) * 2, "x"},
                       {wq, static_cast<size_t>(N * K), "wq"},
                       {s_w, blocks_of(N) * blocks_of(K) * 4, "s_w"}};
-  const Range out[] = {{y, static_cast<size_t>(M * N) * 2, "y"}, {workspace, ws, "workspace"}};
+  const Range out[] = {{y, static_cast<size_t>(M * N) * 2, "y"}, {workspace, plan.bytes, "workspace"}};
   MQ_TRY(check_alias(in, out));
   if (M == 0 || N == 0) return ok();
-  uint8_t* xq = static_cast<uint8_t*>(workspace);
-  float* s_x = reinterpret_cast<float*>(xq + (static_cast<size_t>(M * K) + 255) / 256 * 256);
+  if (plan.fused)
+    return hip_status(mq::launch_fp8_block_gemv(x, nullptr, nullptr, wq, s_w, y, M, N, K, bf16, as_stream(stream)),
+                      "fp8_linear launch");
+  uint8_t* const xq = static_cast<uint8_t*>(workspace);
+  float* const s_x = reinterpret_cast<float*>(xq + plan.scales_at);
   MQ_TRY(hip_status(mq::launch_quant_fp8_blocks(x, xq, s_x, M, K, bf16, as_stream(stream)), "fp8_linear quant launch"));
-  return hip_status(mq::launch_fp8_block_mm(xq, s_x, wq, s_w, y, M, N, K, bf16, as_stream(stream)),
+  return hip_status(mq::launch_fp8_block_mm(xq, s_x, wq, s_w, y, M, N, K, plan.mm, xq + plan.mm_at, bf16,
+                                            as_stream(stream)),
                     "fp8_linear mm launch");
 }
 
@@ -883,12 +924,7 @@ static mq_status kv8_attention_impl(const uint16_t* q, int64_t q_stride, const u
   const mq::Kv8Plan plan = mq::plan_kv8_attention(c, static_cast<int>(Hq));
   const bool empty = T == 0 || B == 0;
   const size_t ws = empty ? 0 : plan.workspace_bytes;
-  if (ws > 0) {
-    if (!workspace || workspace_bytes < ws)
-      return fail(MQ_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", ws,
-                  workspace ? workspace_bytes : static_cast<size_t>(0));
-    if (!aligned(workspace, 16)) return fail(MQ_ERR_ALIGN, "workspace must be 16-byte aligned");
-  }
+  MQ_TRY(check_workspace(workspace, workspace_bytes, ws));
   const size_t cache = static_cast<size_t>(num_pages) * Hkv * page * D, sc = static_cast<size_t>(num_pages) * Hkv * 4;
   const Range in[] = {{q, qb, "q"},
                       {k_cache, cache, "k_cache"},
