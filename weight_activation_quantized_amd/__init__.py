@@ -50,8 +50,8 @@ and the compositions used by a model's linear layer:
     fp8_linear(x, wq, s_w)                           e4m3 codes of x per 128 values, then the block-scaled product
 """
 
-import contextlib
 import ctypes
+import importlib.util
 import os
 
 __all__ = [
@@ -189,12 +189,6 @@ def _dev_tensor(t, name, dtype, ndim):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
-
-
-def _same_device(first, *rest):
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}: one call takes one GPU's")
 
 
 def _stream_of(t, stream):
@@ -501,54 +495,38 @@ def kv_quant(x, bits=8, codes=None, params=None, stream=None):
     return codes, params
 
 
-def _scope(t, stream):
-    """Where a call's outputs and workspace are allocated and its kernels are
-    launched: the given stream (memory from its own pool), else the current
-    stream of t's GPU."""
-    torch = _torch()
-    if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"stream on {stream.device}, tensors on {t.device}")
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() == t.device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+# The wrappers below have a native half (csrc/torch_binding.cpp): the checks of
+# the tensors, the outputs' allocation and the call itself, which in Python
+# would cost several times what the smaller kernels take.
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_mq_torch.so")
+_BOUND = ("mq_rmsnorm_int8", "mq_rmsnorm_int8_bf16", "mq_rmsnorm_fp8", "mq_rmsnorm_fp8_bf16", "mq_quant_fp8_blocks",
+          "mq_quant_fp8_blocks_bf16", "mq_fp8_block_mm_workspace_bytes", "mq_fp8_block_mm", "mq_fp8_block_mm_bf16",
+          "mq_fp8_linear_workspace_bytes", "mq_fp8_linear", "mq_fp8_linear_bf16", "mq_kv8_append",
+          "mq_kv8_append_bf16", "mq_kv8_attention_workspace_bytes", "mq_kv8_attention", "mq_kv8_attention_bf16")
+_native_module = None
 
 
-def _blocks(n):
-    return (n + 127) // 128
+def _native():
+    """The native half, bound to the loaded library. Raises if it is not built."""
+    global _native_module
+    if _native_module is None:
+        lib = library()
+        _torch()  # its libraries first
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(
+                f"{BINDING_PATH} is not built; run `python -m weight_activation_quantized_amd._build`")
+        spec = importlib.util.spec_from_file_location("_mq_torch", BINDING_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.bind(tuple(ctypes.cast(getattr(lib, n), _P).value for n in _BOUND), _check)
+        _native_module = mod
+    return _native_module
 
 
-def _rmsnorm(x, weight, eps, residual, out, s_out, h_out, stream, fp8):
-    torch = _torch()
-    dt = _half_dtype(x, "x")
-    _dev_tensor(x, "x", dt, 2)
-    _dev_tensor(weight, "weight", dt, 1)
-    M, K = x.shape
-    if weight.shape[0] != K:
-        raise ValueError("weight must be [K]")
-    if residual is not None:
-        _dev_tensor(residual, "residual", dt, 2)
-        if residual.shape != x.shape:
-            raise ValueError("residual must have x's shape")
-    elif h_out is not None:
-        raise ValueError("h_out needs a residual")
-    lib, bf = library(), dt == torch.bfloat16
-    if fp8:
-        fn = lib.mq_rmsnorm_fp8_bf16 if bf else lib.mq_rmsnorm_fp8
-    else:
-        fn = lib.mq_rmsnorm_int8_bf16 if bf else lib.mq_rmsnorm_int8
-    with _scope(x, stream):
-        xq = _out(out, (M, K), torch.float8_e4m3fn if fp8 else torch.int8, x, "out")
-        s = _out(s_out, (_blocks(K), M) if fp8 else (M,), torch.float32, x, "s_out")
-        h, rp, hp = None, None, None
-        if residual is not None:
-            h = _out(h_out, (M, K), dt, x, "h_out")
-            rp, hp = residual.data_ptr(), h.data_ptr()
-        _same_device(x, weight, residual, xq, s, h)
-        _check(fn(x.data_ptr(), rp, weight.data_ptr(), eps, hp, xq.data_ptr(), s.data_ptr(), M, K,
-                  _stream_of(x, stream)))
-    return (xq, s) if residual is None else (xq, s, h)
+def _on(stream):
+    """The given stream as the current one: outputs and workspace come from its
+    own pool and the kernels run on it."""
+    return _torch().cuda.stream(stream)
 
 
 def rmsnorm_int8(x, weight, eps=1e-6, residual=None, out=None, s_out=None, h_out=None, stream=None):
@@ -556,52 +534,32 @@ def rmsnorm_int8(x, weight, eps=1e-6, residual=None, out=None, s_out=None, h_out
     of ``w8a8_scaled_mm``: (xq int8 [M, K], s_tok fp32 [M]) and, with a
     residual, h = x + residual in x's dtype (``h_out=residual`` updates the
     residual stream in place)."""
-    return _rmsnorm(x, weight, eps, residual, out, s_out, h_out, stream, False)
+    fn = (_native_module or _native()).rmsnorm
+    if stream is None:
+        return fn(x, weight, eps, residual, out, s_out, h_out, False)
+    with _on(stream):
+        return fn(x, weight, eps, residual, out, s_out, h_out, False)
 
 
 def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, out=None, s_out=None, h_out=None, stream=None):
     """RMS norm of x (+ residual) [M, K] with e4m3 codes and a scale per 128
     values, the input of ``fp8_block_mm``: (xq float8_e4m3fn [M, K], s_x fp32
     [ceil(K/128), M]) and, with a residual, h as in ``rmsnorm_int8``."""
-    return _rmsnorm(x, weight, eps, residual, out, s_out, h_out, stream, True)
+    fn = (_native_module or _native()).rmsnorm
+    if stream is None:
+        return fn(x, weight, eps, residual, out, s_out, h_out, True)
+    with _on(stream):
+        return fn(x, weight, eps, residual, out, s_out, h_out, True)
 
 
 def quant_fp8_blocks(x, out=None, s_out=None, stream=None):
     """e4m3 codes of fp16 or bf16 x [M, K] with a scale per token and 128
     values: (xq float8_e4m3fn [M, K], s_x fp32 [ceil(K/128), M])."""
-    torch = _torch()
-    dt = _half_dtype(x, "x")
-    _dev_tensor(x, "x", dt, 2)
-    M, K = x.shape
-    fn = library().mq_quant_fp8_blocks_bf16 if dt == torch.bfloat16 else library().mq_quant_fp8_blocks
-    with _scope(x, stream):
-        xq = _out(out, (M, K), torch.float8_e4m3fn, x, "out")
-        s = _out(s_out, (_blocks(K), M), torch.float32, x, "s_out")
-        _same_device(x, xq, s)
-        _check(fn(x.data_ptr(), xq.data_ptr(), s.data_ptr(), M, K, _stream_of(x, stream)))
-    return xq, s
-
-
-def _fp8_weights(wq, s_w, K):
-    torch = _torch()
-    _dev_tensor(wq, "wq", torch.float8_e4m3fn, 2)
-    _dev_tensor(s_w, "s_w", torch.float32, 2)
-    N = wq.shape[0]
-    if wq.shape[1] != K or tuple(s_w.shape) != (_blocks(N), _blocks(K)):
-        raise ValueError("wq must be [N, K] and s_w [ceil(N/128), ceil(K/128)]")
-    return N
-
-
-def _workspace(workspace, need, like):
-    """(pointer, bytes, tensor) of the caller's workspace, or of a fresh one."""
-    torch = _torch()
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-    if workspace is None:
-        return None, 0, None
-    if not isinstance(workspace, torch.Tensor) or workspace.device.type != "cuda" or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous GPU tensor")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    fn = (_native_module or _native()).quant_fp8_blocks
+    if stream is None:
+        return fn(x, out, s_out)
+    with _on(stream):
+        return fn(x, out, s_out)
 
 
 def fp8_block_mm_workspace_bytes(M, N, K):
@@ -614,24 +572,15 @@ def fp8_block_mm(xq, s_x, wq, s_w, out=None, workspace=None, stream=None, out_dt
     (s_x [ceil(K/128), M], s_w [ceil(N/128), ceil(K/128)]), in fp16 (default)
     or bf16 (``out_dtype=torch.bfloat16``, or a bf16 ``out``)."""
     torch = _torch()
-    _dev_tensor(xq, "xq", torch.float8_e4m3fn, 2)
-    _dev_tensor(s_x, "s_x", torch.float32, 2)
-    M, K = xq.shape
-    if tuple(s_x.shape) != (_blocks(K), M):
-        raise ValueError("s_x must be [ceil(K/128), M]")
-    N = _fp8_weights(wq, s_w, K)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.float16
     if out_dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("out_dtype must be float16 or bfloat16")
-    fn = library().mq_fp8_block_mm_bf16 if out_dtype == torch.bfloat16 else library().mq_fp8_block_mm
-    with _scope(xq, stream):
-        y = _out(out, (M, N), out_dtype, xq, "out")
-        ws_ptr, ws_bytes, workspace = _workspace(workspace, fp8_block_mm_workspace_bytes(M, N, K), xq)
-        _same_device(xq, s_x, wq, s_w, y, workspace)
-        _check(fn(xq.data_ptr(), s_x.data_ptr(), wq.data_ptr(), s_w.data_ptr(), y.data_ptr(), M, N, K, ws_ptr, ws_bytes,
-                  _stream_of(xq, stream)))
-    return y
+    fn, bf = (_native_module or _native()).fp8_block_mm, out_dtype == torch.bfloat16
+    if stream is None:
+        return fn(xq, s_x, wq, s_w, out, workspace, bf)
+    with _on(stream):
+        return fn(xq, s_x, wq, s_w, out, workspace, bf)
 
 
 def fp8_linear_workspace_bytes(M, N, K):
@@ -643,59 +592,11 @@ def fp8_linear(x, wq, s_w, out=None, workspace=None, stream=None):
     """FP8 linear layer from fp16 or bf16 x (y in x's dtype): e4m3 codes of x
     per 128 values, then the block-scaled product. Bit-identical to
     ``fp8_block_mm(*quant_fp8_blocks(x), wq, s_w, out_dtype=x.dtype)``."""
-    torch = _torch()
-    dt = _half_dtype(x, "x")
-    _dev_tensor(x, "x", dt, 2)
-    M, K = x.shape
-    N = _fp8_weights(wq, s_w, K)
-    fn = library().mq_fp8_linear_bf16 if dt == torch.bfloat16 else library().mq_fp8_linear
-    with _scope(x, stream):
-        y = _out(out, (M, N), dt, x, "out")
-        ws_ptr, ws_bytes, workspace = _workspace(workspace, fp8_linear_workspace_bytes(M, N, K), x)
-        _same_device(x, wq, s_w, y, workspace)
-        _check(fn(x.data_ptr(), wq.data_ptr(), s_w.data_ptr(), y.data_ptr(), M, N, K, ws_ptr, ws_bytes,
-                  _stream_of(x, stream)))
-    return y
-
-
-def _kv8_rows(t, name, dtype, D):
-    """Rows [T, heads, D] of a 16-bit tensor, dense within a row: their stride in values."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
-        raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be on a GPU (got {t.device})")
-    if t.dim() != 3 or t.shape[2] != D:
-        raise ValueError(f"{name} must be [T, heads, {D}] (got shape {tuple(t.shape)})")
-    T, H, _ = t.shape
-    if T == 0:
-        return H * D
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
-        raise ValueError(f"{name}: a token's heads must lie side by side (strides {t.stride()})")
-    return t.stride(0) if T > 1 else H * D
-
-
-def _kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens):
-    torch = _torch()
-    _dev_tensor(k_cache, "k_cache", torch.float8_e4m3fn, 4)
-    _dev_tensor(v_cache, "v_cache", torch.float8_e4m3fn, 4)
-    _dev_tensor(k_scales, "k_scales", torch.float32, 2)
-    _dev_tensor(v_scales, "v_scales", torch.float32, 2)
-    _dev_tensor(block_table, "block_table", torch.int32, 2)
-    _dev_tensor(cu_q, "cu_q", torch.int32, 1)
-    _dev_tensor(kv_lens, "kv_lens", torch.int32, 1)
-    P, H, page, D = k_cache.shape
-    if tuple(v_cache.shape) != (P, H, D, page):
-        raise ValueError("k_cache must be [P, Hkv, page, D] and v_cache [P, Hkv, D, page]")
-    if tuple(k_scales.shape) != (P, H) or tuple(v_scales.shape) != (P, H):
-        raise ValueError("k_scales and v_scales must be [P, Hkv]")
-    B, width = block_table.shape
-    if cu_q.shape[0] != B + 1 or kv_lens.shape[0] != B:
-        raise ValueError("cu_q must be [B + 1] and kv_lens [B] for block_table [B, width]")
-    _same_device(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens)
-    pointers = (k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-                block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr())
-    return P, H, page, D, B, width, pointers
+    fn = (_native_module or _native()).fp8_linear
+    if stream is None:
+        return fn(x, wq, s_w, out, workspace)
+    with _on(stream):
+        return fn(x, wq, s_w, out, workspace)
 
 
 def kv8_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, stream=None):
@@ -704,17 +605,11 @@ def kv8_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv
     v_cache [P, Hkv, D, page], scales [P, Hkv], all updated in place. Sequence
     b's rows are cu_q[b] .. cu_q[b + 1]; kv_lens[b] counts its tokens with
     them; block_table[b] names its pages."""
-    dt = _half_dtype(k, "k")
-    P, H, page, D, B, width, pointers = _kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens)
-    ks, vs = _kv8_rows(k, "k", dt, D), _kv8_rows(v, "v", dt, D)
-    if k.shape != v.shape or k.shape[1] != H:
-        raise ValueError("k and v must be [T, Hkv, D]")
-    _same_device(k_cache, k, v)
-    bf = dt == _torch().bfloat16
-    fn = library().mq_kv8_append_bf16 if bf else library().mq_kv8_append
-    with _scope(k_cache, stream):
-        _check(fn(k.data_ptr(), v.data_ptr(), ks, vs, *pointers, k.shape[0], B, H, D, page, P, width, max_q_len,
-                  _stream_of(k_cache, stream)))
+    fn = (_native_module or _native()).kv8_append
+    if stream is None:
+        return fn(k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len)
+    with _on(stream):
+        return fn(k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len)
 
 
 def kv8_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len):
@@ -729,23 +624,13 @@ def kv8_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv
     dtype: a sequence's rows are its last tokens, each sees the keys up to its
     own. ``softmax_scale`` defaults to D ** -0.5. Rows of no sequence are left
     as they are (unset in a fresh ``out``)."""
-    torch = _torch()
-    dt = _half_dtype(q, "q")
-    P, H, page, D, B, width, pointers = _kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens)
-    qs = _kv8_rows(q, "q", dt, D)
-    T, Hq = q.shape[0], q.shape[1]
-    if softmax_scale is None:
-        softmax_scale = D ** -0.5
-    lib = library()
-    fn = lib.mq_kv8_attention_bf16 if dt == torch.bfloat16 else lib.mq_kv8_attention
-    with _scope(q, stream):
-        o = _out(out, (T, Hq, D), dt, q, "out")
-        need = kv8_attention_workspace_bytes(T, B, Hq, H, D, page, width, max_q_len)
-        ws_ptr, ws_bytes, workspace = _workspace(workspace, need, q)
-        _same_device(q, k_cache, o, workspace)
-        _check(fn(q.data_ptr(), qs, *pointers, o.data_ptr(), T, B, Hq, H, D, page, P, width, max_q_len, softmax_scale,
-                  ws_ptr, ws_bytes, _stream_of(q, stream)))
-    return o
+    fn = (_native_module or _native()).kv8_attention
+    if stream is None:
+        return fn(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, softmax_scale, out,
+                  workspace)
+    with _on(stream):
+        return fn(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, softmax_scale, out,
+                  workspace)
 
 
 # Field order of AWQ-style checkpoint words: field j holds element

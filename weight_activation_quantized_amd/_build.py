@@ -1,4 +1,4 @@
-"""Build libmq.so (gfx950) in-tree with hipcc.
+"""Build libmq.so (gfx950) in-tree with hipcc, and the torch wrappers' native half.
 
     python -m weight_activation_quantized_amd._build [-D NAME=VALUE ...] [--out PATH]
 
@@ -8,9 +8,11 @@ without a GPU.
 """
 
 import argparse
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmq.so")
+BINDING_PATH = os.path.join(HERE, "_mq_torch.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["mq_api.cpp", "quant_int8.hip", "w8a8_gemm.hip", "w8a8_gemv.hip", "w4a16_gemv.hip",
@@ -65,6 +68,23 @@ def _run(cmd):
     return out
 
 
+def build_binding(out=BINDING_PATH, build_dir=BUILD_DIR):
+    """The native half of the torch wrappers (host code only): a CPython
+    extension against the installed torch's headers."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    tmp = out + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+          "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-D_GLIBCXX_USE_CXX11_ABI=1", f"-I{INCLUDE}",
+          "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+          "-isystem", os.path.join(rocm, "include"), "-isystem", sysconfig.get_paths()["include"],
+          os.path.join(CSRC, "torch_binding.cpp"), "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+          "-lc10_hip"])
+    os.replace(tmp, out)
+    return out
+
+
 def build(out=LIB_PATH, defines=(), build_dir=BUILD_DIR, jobs=None, verbose=False):
     """Compile and link; returns the path of the shared library."""
     os.makedirs(build_dir, exist_ok=True)
@@ -76,6 +96,7 @@ def build(out=LIB_PATH, defines=(), build_dir=BUILD_DIR, jobs=None, verbose=Fals
         return obj
 
     jobs = jobs or min(len(SOURCES), max(1, (os.cpu_count() or 2) // 2))
+    binding = ThreadPoolExecutor(max_workers=1).submit(build_binding) if out == LIB_PATH else None
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         objs = list(ex.map(compile_one, SOURCES))
     tmp = out + ".tmp"
@@ -83,6 +104,10 @@ def build(out=LIB_PATH, defines=(), build_dir=BUILD_DIR, jobs=None, verbose=Fals
     os.replace(tmp, out)
     if verbose:
         print(f"built {out}")
+    if out == LIB_PATH:  # one binding serves every build of the library
+        binding.result()
+        if verbose:
+            print(f"built {BINDING_PATH}")
     return out
 
 
