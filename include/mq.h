@@ -550,7 +550,7 @@ mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* 
  * Requires: D in {64, 128}, page in {16, 32, 64, 128} (else
  * MQ_ERR_UNSUPPORTED); 0 <= T <= 2^26; 0 <= B <= 65535; 1 <= Hkv <= Hq <=
  * 1024, Hq % Hkv == 0; num_pages >= 1; 1 <= table_width * page <= 2^30;
- * max_q_len >= 1; for the append B * Hkv * (max_q_len / page + 2) below about
+ * max_q_len >= 1; 0 <= softmax_scale <= 1e6; for the append B * Hkv * (max_q_len / page + 2) below about
  * 2^23; q, k, v, caches, out 16-byte aligned, the rest 4-byte. _bf16: k, v, q
  * and out are bf16.
  */

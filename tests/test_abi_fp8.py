@@ -158,6 +158,7 @@ def test_kv8_attention_arguments(lib):
     assert _attention(lib, Hq=7) == SHAPE and _attention(lib, Hq=0) == SHAPE and _attention(lib, Hq=2048) == SHAPE
     assert _attention(lib, sq=1000) == SHAPE and _attention(lib, q=Cache.at["q"] + 4) == ALIGN
     assert _attention(lib, scale=float("nan")) == UNSUP and _attention(lib, scale=float("inf")) == UNSUP
+    assert _attention(lib, scale=-0.1) == UNSUP and _attention(lib, T=0, q=None, out=None, scale=0.0) == OK
     assert _attention(lib, out=Cache.at["q"] + 512) == ALIAS and _attention(lib, out=Cache.at["kc"]) == ALIAS
     assert _attention(lib, out=Cache.at["out"] + 8) == ALIGN
     # a long sequence needs a workspace

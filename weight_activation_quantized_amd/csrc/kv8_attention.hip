@@ -357,24 +357,43 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
 // ---------------------------------------------------------------------------
 // Prompts: a workgroup of eight wavefronts takes 256 rows of one kv head (the
 // query heads of the group side by side, so that one K/V tile serves all of
-// them) and walks the keys in tiles of 64. The tile's codes are widened once
-// per workgroup on their way into LDS (double-buffered; the next tile's codes
-// are already in registers), each wavefront then reads it for its 32 rows.
+// them) and walks the keys in tiles of 64; each wavefront has 32 rows.
+//
 // v_mfma_32x32x16: lane (i = lane % 32, h = lane / 32). Row i of a K tile is
 // the token with bits 2 and 3 of i exchanged: lane (i, h) then holds, for row
 // i of Q, in registers 8 u .. 8 u + 7 the scores of the consecutive tokens
 // 16 u + 8 h .. + 7, the B operand of the second product.
+//
+// A tile is 1024 cycles of matrix unit per wavefront and about as many of
+// vector unit (exponentials first of all), so the two wavefronts of a SIMD
+// take turns: wavefronts 0-3 and 4-7 (one of each per SIMD) walk the same
+// tiles half a step apart, one half in its product phase (second product of
+// tile t - 1, scores of tile t) while the other is in its softmax phase of the
+// tile before. Every phase ends at a barrier.
+//
+// The codes of a tile are widened once per workgroup on their way into LDS.
+// What a product phase t reads, K of tile t and V of tile t - 1, is one of two
+// buffers: phase t of the first half falls on step 2 t, of the second on
+// 2 t + 1, so the other buffer is free on both, and each half fills its share
+// of it in its softmax phase. The codes come into registers a phase pair
+// earlier, the page numbers that lead to them another one earlier.
+//
+// The reference of the exponentials follows the maximum lazily: it moves (and
+// the sums are rescaled) only when a score passes it by more than 2^8, so
+// weights stay at most 2^8 and nearly every tile goes without rescaling.
 // ---------------------------------------------------------------------------
 
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+constexpr float kLazy = 8.f;
 
 template <int D, bool kBf16>
 __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint16_t* __restrict__ q, int64_t q_stride,
                                                          uint16_t* __restrict__ out, Parts parts, int group,
                                                          int row_tiles, int splits, float scale_log2) {
   constexpr int kRows = 256, kKs = D / 16, kDt = D / 32;
-  constexpr int kKRow = 2 * D;                // bytes of a widened K row
+  constexpr int kKRow = 2 * D;  // bytes of a widened K row
   constexpr int kKBytes = 64 * kKRow, kVBytes = D * 128;
   constexpr int kBuf = kKBytes + kVBytes;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kBuf];
@@ -388,6 +407,7 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
   const int rows = seq.n * group;
   if (kRows * rt >= rows) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = wave >> 2;
   const int i = lane & 31, h = lane >> 5;
   const int heads = c.kv_heads * group;
 
@@ -407,52 +427,54 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
   const int last_t = min(kRows * rt + kRows - 1, rows - 1) / group;
   const int top = min(seq.len - seq.n + last_t, seq.seen - 1);
   const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, 8);
+  const int tiles = span.end - span.first;
   const int32_t* const table = c.table + static_cast<size_t>(b) * c.table_width;
 
   // Staging: 16-byte pieces of codes; piece p of K is row p / (D / 16), of V
-  // dimension p / 4, tokens 16 (p % 4) .. + 15.
-  constexpr int kPieces = 64 * D / 16;  // of K, and of V
-  static_assert(kPieces <= 512, "one piece of each per thread");
-  const bool stager = threadIdx.x < kPieces;
-  const int krow = threadIdx.x / (D / 16), kch = threadIdx.x % (D / 16);
-  const int vdim = threadIdx.x / 4, vpart = threadIdx.x % 4;
+  // dimension p / 4, tokens 16 (p % 4) .. + 15. 4 D pieces of each: one of both
+  // per thread for D = 128, one of either for D = 64.
+  constexpr bool kBoth = D == 128;
+  static_assert(4 * D == (kBoth ? 512 : 256), "pieces per thread");
+  const bool does_k = kBoth || threadIdx.x < 256, does_v = kBoth || threadIdx.x >= 256;
+  const int kp = threadIdx.x & (4 * D - 1);
+  const int krow = kp / (D / 16), kch = kp % (D / 16);
+  const int vdim = kp / 4, vpart = kp % 4;
   // Page of the 16 keys `part` of a tile; -1: none, or not one of the pool's.
   auto page_id = [&](int tile, int part) {
     const int t = 64 * tile + 16 * part;
-    return tile < span.end && t <= top ? table[t >> c.page_shift] : -1;
+    return tile >= span.first && tile < span.end && t <= top ? table[t >> c.page_shift] : -1;
   };
   auto known = [&](int id) { return id >= 0 && id < c.num_pages; };
-  // Codes and scales of a tile into registers; the page numbers were requested
-  // one call earlier.
-  int kid = -1, vid = -1, sid = -1;
-  auto request_pages = [&](int tile) {
-    kid = page_id(tile, krow / 16);
-    vid = page_id(tile, vpart);
-    sid = page_id(tile, threadIdx.x & 3);
+  // Pair j: K (and the scales) of tile first + j, V of the tile before it.
+  int kid, vid, sid;
+  auto request_pages = [&](int j) {
+    kid = page_id(span.first + j, krow / 16);
+    vid = page_id(span.first + j - 1, vpart);
+    sid = page_id(span.first + j, threadIdx.x & 3);
   };
   u32x4 kreg, vreg;
-  float kscale = 0.f, vscale = -1.f;
-  auto fetch = [&](int tile) {
+  float kscale, vscale;
+  auto fetch = [&](int j) {
+    const int tile = span.first + j;
     kreg = vreg = u32x4{0u, 0u, 0u, 0u};
+    kscale = 0.f;
     vscale = -1.f;
-    if (tile < span.end) {
-      if (stager && known(kid)) {
-        const int at = (64 * tile + krow) & (c.page - 1);
-        kreg = *reinterpret_cast<const u32x4*>(
-            c.k + ((static_cast<size_t>(kid) * c.kv_heads + head) * c.page + at) * D + 16 * kch);
-      }
-      if (stager && known(vid)) {
-        const int at = (64 * tile + 16 * vpart) & (c.page - 1);
-        vreg = *reinterpret_cast<const u32x4*>(
-            c.v + ((static_cast<size_t>(vid) * c.kv_heads + head) * D + vdim) * c.page + at);
-      }
-      if (threadIdx.x < 4 && known(sid)) {
-        const size_t unit = static_cast<size_t>(sid) * c.kv_heads + head;
-        kscale = c.k_scales[unit];
-        vscale = held_scale(c.v_scales[unit]);
-      }
+    if (does_k && known(kid)) {
+      const int at = (64 * tile + krow) & (c.page - 1);
+      kreg = *reinterpret_cast<const u32x4*>(
+          c.k + ((static_cast<size_t>(kid) * c.kv_heads + head) * c.page + at) * D + 16 * kch);
     }
-    request_pages(tile + 1);
+    if (does_v && known(vid)) {
+      const int at = (64 * (tile - 1) + 16 * vpart) & (c.page - 1);
+      vreg = *reinterpret_cast<const u32x4*>(
+          c.v + ((static_cast<size_t>(vid) * c.kv_heads + head) * D + vdim) * c.page + at);
+    }
+    if (threadIdx.x < 4 && known(sid)) {
+      const size_t unit = static_cast<size_t>(sid) * c.kv_heads + head;
+      kscale = c.k_scales[unit];
+      vscale = held_scale(c.v_scales[unit]);
+    }
+    request_pages(j + 1);
   };
   // 16-byte chunk positions are XOR-ed by the row, so that a fragment read of
   // 32 rows meets no bank twice: K rows of 256 bytes by 16 rows, of 128 bytes
@@ -461,113 +483,147 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
     return row * kKRow + 16 * (D == 128 ? ch ^ (row & 15) : ch ^ ((row >> 1) & 7));
   };
   auto v_chunk = [&](int row, int ch) { return kKBytes + row * 128 + 16 * (ch ^ ((row >> 1) & 7)); };
-  auto stage = [&](int tile, int buf) {
+  const int kto0 = k_chunk(krow, 2 * kch), kto1 = k_chunk(krow, 2 * kch + 1);
+  const int vto0 = v_chunk(vdim, 2 * vpart), vto1 = v_chunk(vdim, 2 * vpart + 1);
+  auto stage = [&](int j) {
+    if (j > tiles) return;
+    const int buf = j & 1;
     if (threadIdx.x < 4)
-      sscale[buf][threadIdx.x] =
-          f32x4{kscale * scale_log2, __builtin_amdgcn_logf(fmaxf(vscale, kMinScale)), vscale > 0.f ? 1.f / vscale : -1.f, 0.f};
-    if (!stager) return;
-    if (64 * tile + 63 > top) vreg = first_bytes(vreg, top - (64 * tile + 16 * vpart) + 1);
+      // (a score scale of 0 would turn a masked score's infinity into NaN)
+      sscale[buf][threadIdx.x] = f32x4{fmaxf(kscale * scale_log2, 0x1p-126f), __builtin_amdgcn_logf(fmaxf(vscale, kMinScale)),
+                                       vscale > 0.f ? 1.f / vscale : -1.f, 0.f};
+    const int behind = 64 * (span.first + j - 1) + 63 - top;  // keys of the V tile past the last one
+    if (behind > 0) vreg = first_bytes(vreg, 64 - behind - 16 * vpart);
     lds_u8* const to = lds + buf * kBuf;
-    *(lds_u32x4*)(to + k_chunk(krow, 2 * kch)) = __builtin_bit_cast(u32x4, widen<kBf16>(kreg[0], kreg[1]));
-    *(lds_u32x4*)(to + k_chunk(krow, 2 * kch + 1)) = __builtin_bit_cast(u32x4, widen<kBf16>(kreg[2], kreg[3]));
-    *(lds_u32x4*)(to + v_chunk(vdim, 2 * vpart)) = __builtin_bit_cast(u32x4, widen<false>(vreg[0], vreg[1]));
-    *(lds_u32x4*)(to + v_chunk(vdim, 2 * vpart + 1)) = __builtin_bit_cast(u32x4, widen<false>(vreg[2], vreg[3]));
+    if (does_k) {
+      *(lds_u32x4*)(to + kto0) = __builtin_bit_cast(u32x4, widen<kBf16>(kreg[0], kreg[1]));
+      *(lds_u32x4*)(to + kto1) = __builtin_bit_cast(u32x4, widen<kBf16>(kreg[2], kreg[3]));
+    }
+    if (does_v) {
+      *(lds_u32x4*)(to + vto0) = __builtin_bit_cast(u32x4, widen<false>(vreg[0], vreg[1]));
+      *(lds_u32x4*)(to + vto1) = __builtin_bit_cast(u32x4, widen<false>(vreg[2], vreg[3]));
+    }
+  };
+  auto phase_end = [&]() {
+    wait_counts<63, 0>();  // LDS only: the codes on their way stay in flight
+    bare_barrier();
   };
 
-  f32x16 o[kDt];
+  f32x16 o[kDt], s[2];
+  f16x8 w[4];
 #pragma unroll
   for (int d = 0; d < kDt; ++d) o[d] = f32x16{};
-  float m = kNegInf, l = 0.f;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) w[p] = f16x8{};  // tile -1: no weights, and zeros for its V
+  float base = kNegInf, l = 0.f;
   const int wave_low = __builtin_amdgcn_readfirstlane(
       min(seq.len - seq.n + min(kRows * rt + 32 * wave, rows - 1) / group, seq.seen - 1));  // first row's last key
   const bool wave_full = kRows * rt + 32 * wave + 31 < rows;  // every lane holds a row
   const int ktok = (i & 19) | ((i & 4) << 1) | ((i & 8) >> 1);  // bits 2 and 3 exchanged
+  int kat[kKs], vat[4];
+#pragma unroll
+  for (int ks = 0; ks < kKs; ++ks) kat[ks] = k_chunk(ktok, 2 * ks + h);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) vat[p] = v_chunk(i, 2 * p + h);
 
-  request_pages(span.first);
-  fetch(span.first);
-  stage(span.first, 0);
-  fetch(span.first + 1);
-  __syncthreads();
-  for (int tile = span.first; tile < span.end; ++tile) {
-    const int buf = (tile - span.first) & 1;
-    if (tile + 1 < span.end) stage(tile + 1, buf ^ 1);  // every wavefront is past its reads of that buffer
-    fetch(tile + 2);
-    const lds_u8* const src = lds + buf * kBuf;
-
+  auto second_product = [&](int j) {
+    const lds_u8* const src = lds + (j & 1) * kBuf;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int d = 0; d < kDt; ++d)
+        o[d] = mfma_32x32x16<false>(__builtin_bit_cast(f16x8, *(const lds_u32x4*)(src + vat[p] + d * 32 * 128)), w[p],
+                                    o[d]);
+  };
+  auto scores = [&](int j) {
+    const lds_u8* const src = lds + (j & 1) * kBuf;
+    s[0] = f32x16{};
+    s[1] = f32x16{};
+#pragma unroll
+    for (int ks = 0; ks < kKs; ++ks)
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+        s[a] = mfma_32x32x16<kBf16>(__builtin_bit_cast(f16x8, *(const lds_u32x4*)(src + kat[ks] + a * 32 * kKRow)),
+                                    qf[ks], s[a]);
+  };
+  auto softmax = [&](int j) {
+    const int t0 = 64 * (span.first + j);
     float f[4], lv[4], iv[4];
-    bool whole = wave_full && 64 * tile + 63 <= wave_low;
+    bool whole = wave_full && t0 + 63 <= wave_low;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const f32x4 sc = sscale[buf][p];
+      const f32x4 sc = sscale[j & 1][p];
       f[p] = sc[0];
       lv[p] = sc[1];
       iv[p] = sc[2];
       whole = whole && iv[p] > 0.f;
     }
-    whole = __builtin_amdgcn_readfirstlane(whole);
-
-    f32x16 s[2];
+    if (!__builtin_amdgcn_readfirstlane(whole)) {
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      s[a] = f32x16{};
+      for (int a = 0; a < 2; ++a)
 #pragma unroll
-      for (int ks = 0; ks < kKs; ++ks) {
-        const u32x4 kf = *(const lds_u32x4*)(src + k_chunk(32 * a + ktok, 2 * ks + h));
-        s[a] = mfma_32x32x16<kBf16>(__builtin_bit_cast(f16x8, kf), qf[ks], s[a]);
-      }
+        for (int e = 0; e < 16; ++e) {
+          const int p = 2 * a + e / 8, t = t0 + 16 * p + 8 * h + e % 8;
+          s[a][e] = t <= limit && iv[p] > 0.f ? s[a][e] : kNegInf;
+        }
     }
     float mt = kNegInf;
-    if (whole) {
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int p = 2 * a + e / 8;
-          s[a][e] = fmaf(s[a][e], f[p], lv[p]);
-          mt = fmaxf(mt, s[a][e]);
-        }
-    } else {
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int p = 2 * a + e / 8;
-          const int t = 64 * tile + 16 * p + 8 * h + e % 8;
-          s[a][e] = t <= limit && iv[p] > 0.f ? fmaf(s[a][e], f[p], lv[p]) : kNegInf;
-          mt = fmaxf(mt, s[a][e]);
-        }
-    }
-    mt = fmaxf(mt, __shfl_xor(mt, 32, kWave));
-    const float mn = fmaxf(m, mt);
-    const float base = mn == kNegInf ? 0.f : mn;
-    const float shrink = __builtin_amdgcn_exp2f(m - base);
-    m = mn;
-    f16x8 w[4];
-    l *= shrink;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
+      float mp = s[p / 2][8 * (p % 2)];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) mp = fmaxf(mp, s[p / 2][8 * (p % 2) + e]);
+      mt = fmaxf(mt, fmaf(mp, f[p], lv[p]));
+    }
+    mt = fmaxf(mt, __shfl_xor(mt, 32, kWave));
+    if (__any(mt > base + kLazy)) {
+      const float moved = mt > base + kLazy ? mt : base;
+      const float shrink = moved == kNegInf ? 1.f : __builtin_amdgcn_exp2f(base - moved);  // 0 for the first keys
+      base = moved;
+      l *= shrink;
+#pragma unroll
+      for (int d = 0; d < kDt; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][e] *= shrink;
+    }
+    const float ref = base == kNegInf ? 0.f : base;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float off = lv[p] - ref;
       f32x8 x;
       float sum = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] = __builtin_amdgcn_exp2f(s[p / 2][8 * (p % 2) + e] - base);
+        x[e] = __builtin_amdgcn_exp2f(fmaf(s[p / 2][8 * (p % 2) + e], f[p], off));
         sum += x[e];
       }
       l = fmaf(sum, fmaxf(iv[p], 0.f), l);
       w[p] = to_f16(x);
     }
-#pragma unroll
-    for (int d = 0; d < kDt; ++d) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[d][e] *= shrink;
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const u32x4 vf = *(const lds_u32x4*)(src + v_chunk(32 * d + i, 2 * p + h));
-        o[d] = mfma_32x32x16<false>(__builtin_bit_cast(f16x8, vf), w[p], o[d]);
-      }
-    }
-    __syncthreads();
+  };
+
+  request_pages(0);
+  fetch(0);
+  stage(0);
+  fetch(1);
+  phase_end();
+  if (half == 1) {  // the second half's first step: it has no product to form yet
+    stage(1);
+    fetch(2);
+    phase_end();
   }
+  for (int j = 0; j < tiles; ++j) {
+    second_product(j);
+    scores(j);
+    phase_end();
+    softmax(j);
+    stage(j + 1 + half);
+    fetch(j + 2 + half);
+    phase_end();
+  }
+  second_product(tiles);
+  if (half == 0) phase_end();  // the second half's last softmax phase
+
   l += __shfl_xor(l, 32, kWave);
   if (!live) return;
   const size_t to = static_cast<size_t>(seq.row0 + tq) * heads + head * group + g;
@@ -590,7 +646,7 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<f32x4*>(parts.o + at * D + 32 * d + 8 * e + 4 * h) =
             f32x4{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
-    if (h == 0) *reinterpret_cast<f32x2*>(parts.ml + 2 * at) = f32x2{m, l};
+    if (h == 0) *reinterpret_cast<f32x2*>(parts.ml + 2 * at) = f32x2{base, l};
   }
 }
 

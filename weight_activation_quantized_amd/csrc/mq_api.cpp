@@ -915,8 +915,8 @@ static mq_status kv8_attention_impl(const uint16_t* q, int64_t q_stride, const u
   MQ_TRY(kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, T, B, Hkv, D, page, num_pages,
                    table_width, max_q_len, c));
   MQ_TRY(kv8_heads(Hq, Hkv));
-  if (!(softmax_scale >= -1e6f && softmax_scale <= 1e6f))
-    return fail(MQ_ERR_UNSUPPORTED, "softmax_scale=%g", static_cast<double>(softmax_scale));
+  if (!(softmax_scale >= 0.f && softmax_scale <= 1e6f))
+    return fail(MQ_ERR_UNSUPPORTED, "softmax_scale=%g must lie in [0, 1e6]", static_cast<double>(softmax_scale));
   size_t qb = 0;
   MQ_TRY(kv8_rows(q, T, Hq * D, q_stride, "q", qb));
   MQ_TRY(need(out, T, "out"));
