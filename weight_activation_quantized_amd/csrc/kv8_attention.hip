@@ -25,6 +25,8 @@
 // behind the last token are cleared, so whatever a page holds there (NaN codes
 // too) counts for nothing; so do pages whose number is not one of the pool's.
 // A row that sees no key is 0.
+#include <type_traits>
+
 #include "device_common.h"
 #include "launch.h"
 
@@ -359,24 +361,31 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
 // query heads of the group side by side, so that one K/V tile serves all of
 // them) and walks the keys in tiles of 64; each wavefront has 32 rows.
 //
-// v_mfma_32x32x16: lane (i = lane % 32, h = lane / 32). Row i of a K tile is
-// the token with bits 2 and 3 of i exchanged: lane (i, h) then holds, for row
-// i of Q, in registers 8 u .. 8 u + 7 the scores of the consecutive tokens
-// 16 u + 8 h .. + 7, the B operand of the second product.
+// v_mfma_32x32x16: lane (i = lane % 32, h = lane / 32). Row i of half a of a K
+// tile (32 keys) is the key with the bits (4 3 2) of i turned to (3 2 4): lane
+// (i, h) then holds, for row i of Q, in registers 0 .. 15 the scores of the 16
+// consecutive keys 32 a + 16 h + 0 .. 15. They lie in one page, so the scales
+// are lane values, and the first and second eight are, widened to fp16, the B
+// operands of two steps of the second product, whose A operands are the two
+// halves of one 16-byte piece of a V row.
 //
-// A tile is 1024 cycles of matrix unit per wavefront and about as many of
-// vector unit (exponentials first of all), so the two wavefronts of a SIMD
-// take turns: wavefronts 0-3 and 4-7 (one of each per SIMD) walk the same
-// tiles half a step apart, one half in its product phase (second product of
-// tile t - 1, scores of tile t) while the other is in its softmax phase of the
-// tile before. Every phase ends at a barrier.
+// A tile is 1024 cycles of matrix unit per wavefront (D = 128) and as many of
+// vector unit (exponentials first of all), so the two wavefronts of a SIMD take
+// turns: wavefronts 0-3 and 4-7 (one of each per SIMD) walk the same tiles half
+// a step apart, one half in its product phase (second product of tile t - 1,
+// scores of tile t) while the other is in its softmax phase. Every phase ends
+// at a barrier.
 //
-// The codes of a tile are widened once per workgroup on their way into LDS.
-// What a product phase t reads, K of tile t and V of tile t - 1, is one of two
-// buffers: phase t of the first half falls on step 2 t, of the second on
-// 2 t + 1, so the other buffer is free on both, and each half fills its share
-// of it in its softmax phase. The codes come into registers a phase pair
-// earlier, the page numbers that lead to them another one earlier.
+// Codes move from memory into LDS untouched (DMA, no registers) and are
+// widened as a wavefront reads them, under its MFMAs: widening them once per
+// workgroup on the way into LDS cost the softmax phase, the longer one, more
+// than it saved, and twice the LDS traffic. What product phase t reads, K of
+// tile t and V of tile t - 1 ("pair t"), is one of three buffers. Phase t of
+// the first half falls on step 2 t, of the second on 2 t + 1; the first half
+// requests pair t + 2 in its softmax phase on step 2 t + 1, the second pair
+// t + 3 on 2 t + 2, when the buffer's last readers (pair t - 1, pair t) are past
+// it, and both wait at the next softmax phase, two steps later, before a
+// barrier that precedes the pair's first use.
 //
 // The reference of the exponentials follows the maximum lazily: it moves (and
 // the sums are rescaled) only when a score passes it by more than 2^8, so
@@ -385,19 +394,27 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
 
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef const __attribute__((address_space(1))) void gbl_void;
 
 constexpr float kLazy = 8.f;
+
+// The larger of x in lanes l and l ^ 32, in both: the swap leaves the lower
+// half's values in one register and the upper half's in the other. (Written
+// out: the compiler drops the second result of the builtin.)
+__device__ __forceinline__ float halves_max(float x) {
+  float lower = x, upper = x;
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\ts_nop 1" : "+v"(lower), "+v"(upper));
+  return fmaxf(lower, upper);
+}
 
 template <int D, bool kBf16>
 __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint16_t* __restrict__ q, int64_t q_stride,
                                                          uint16_t* __restrict__ out, Parts parts, int group,
                                                          int row_tiles, int splits, float scale_log2) {
-  constexpr int kRows = 256, kKs = D / 16, kDt = D / 32;
-  constexpr int kKRow = 2 * D;  // bytes of a widened K row
-  constexpr int kKBytes = 64 * kKRow, kVBytes = D * 128;
-  constexpr int kBuf = kKBytes + kVBytes;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kBuf];
-  __shared__ f32x4 sscale[2][4];  // per part of 16 keys: k scale, log2 and reciprocal of the v scale (< 0: no page)
+  constexpr int kRows = 256, kKk = D / 32, kDt = D / 32;  // 16-byte steps of a K row per lane; 32-row tiles of V
+  constexpr int kBytes = 64 * D;                          // of K, and of V, in a tile
+  constexpr int kSlots = 3;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * 2 * kBytes];
   lds_u8* const lds = (lds_u8*)(smem);
 
   // the last rows of a sequence see the most keys: they go first
@@ -414,215 +431,247 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
   const int r = kRows * rt + 32 * wave + i;
   const bool live = r < rows;
   const int tq = live ? r / group : 0, g = live ? r - tq * group : 0;
-  const int limit = live ? min(seq.len - seq.n + tq, seq.seen - 1) : -1;
+  const int limit = live ? min(seq.len - seq.n + tq, seq.seen - 1) : -1;  // last key the row sees
   const uint16_t* const qrow = q + static_cast<int64_t>(seq.row0 + tq) * q_stride + (head * group + g) * D;
-  f16x8 qf[kKs];
+  // k-steps 2 kk and 2 kk + 1 are the halves of the 16-byte pieces 2 kk + h of the K rows
+  f16x8 qf[2 * kKk];
 #pragma unroll
-  for (int ks = 0; ks < kKs; ++ks) {
+  for (int ks = 0; ks < 2 * kKk; ++ks) {
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (live) v = *reinterpret_cast<const u32x4*>(qrow + 16 * ks + 8 * h);
+    if (live) v = *reinterpret_cast<const u32x4*>(qrow + 32 * (ks / 2) + 16 * h + 8 * (ks % 2));
     qf[ks] = __builtin_bit_cast(f16x8, v);
   }
 
   const int last_t = min(kRows * rt + kRows - 1, rows - 1) / group;
-  const int top = min(seq.len - seq.n + last_t, seq.seen - 1);
+  const int top = min(seq.len - seq.n + last_t, seq.seen - 1);  // the workgroup's last key
   const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, 8);
   const int tiles = span.end - span.first;
-  const int32_t* const table = c.table + static_cast<size_t>(b) * c.table_width;
-
-  // Staging: 16-byte pieces of codes; piece p of K is row p / (D / 16), of V
-  // dimension p / 4, tokens 16 (p % 4) .. + 15. 4 D pieces of each: one of both
-  // per thread for D = 128, one of either for D = 64.
-  constexpr bool kBoth = D == 128;
-  static_assert(4 * D == (kBoth ? 512 : 256), "pieces per thread");
-  const bool does_k = kBoth || threadIdx.x < 256, does_v = kBoth || threadIdx.x >= 256;
-  const int kp = threadIdx.x & (4 * D - 1);
-  const int krow = kp / (D / 16), kch = kp % (D / 16);
-  const int vdim = kp / 4, vpart = kp % 4;
-  // Page of the 16 keys `part` of a tile; -1: none, or not one of the pool's.
-  auto page_id = [&](int tile, int part) {
-    const int t = 64 * tile + 16 * part;
-    return tile >= span.first && tile < span.end && t <= top ? table[t >> c.page_shift] : -1;
-  };
-  auto known = [&](int id) { return id >= 0 && id < c.num_pages; };
-  // Pair j: K (and the scales) of tile first + j, V of the tile before it.
-  int kid, vid, sid;
-  auto request_pages = [&](int j) {
-    kid = page_id(span.first + j, krow / 16);
-    vid = page_id(span.first + j - 1, vpart);
-    sid = page_id(span.first + j, threadIdx.x & 3);
-  };
-  u32x4 kreg, vreg;
-  float kscale, vscale;
-  auto fetch = [&](int j) {
-    const int tile = span.first + j;
-    kreg = vreg = u32x4{0u, 0u, 0u, 0u};
-    kscale = 0.f;
-    vscale = -1.f;
-    if (does_k && known(kid)) {
-      const int at = (64 * tile + krow) & (c.page - 1);
-      kreg = *reinterpret_cast<const u32x4*>(
-          c.k + ((static_cast<size_t>(kid) * c.kv_heads + head) * c.page + at) * D + 16 * kch);
-    }
-    if (does_v && known(vid)) {
-      const int at = (64 * (tile - 1) + 16 * vpart) & (c.page - 1);
-      vreg = *reinterpret_cast<const u32x4*>(
-          c.v + ((static_cast<size_t>(vid) * c.kv_heads + head) * D + vdim) * c.page + at);
-    }
-    if (threadIdx.x < 4 && known(sid)) {
-      const size_t unit = static_cast<size_t>(sid) * c.kv_heads + head;
-      kscale = c.k_scales[unit];
-      vscale = held_scale(c.v_scales[unit]);
-    }
-    request_pages(j + 1);
-  };
-  // 16-byte chunk positions are XOR-ed by the row, so that a fragment read of
-  // 32 rows meets no bank twice: K rows of 256 bytes by 16 rows, of 128 bytes
-  // (and V rows) by pairs of rows.
-  auto k_chunk = [&](int row, int ch) {
-    return row * kKRow + 16 * (D == 128 ? ch ^ (row & 15) : ch ^ ((row >> 1) & 7));
-  };
-  auto v_chunk = [&](int row, int ch) { return kKBytes + row * 128 + 16 * (ch ^ ((row >> 1) & 7)); };
-  const int kto0 = k_chunk(krow, 2 * kch), kto1 = k_chunk(krow, 2 * kch + 1);
-  const int vto0 = v_chunk(vdim, 2 * vpart), vto1 = v_chunk(vdim, 2 * vpart + 1);
-  auto stage = [&](int j) {
-    if (j > tiles) return;
-    const int buf = j & 1;
-    if (threadIdx.x < 4)
-      // (a score scale of 0 would turn a masked score's infinity into NaN)
-      sscale[buf][threadIdx.x] = f32x4{fmaxf(kscale * scale_log2, 0x1p-126f), __builtin_amdgcn_logf(fmaxf(vscale, kMinScale)),
-                                       vscale > 0.f ? 1.f / vscale : -1.f, 0.f};
-    const int behind = 64 * (span.first + j - 1) + 63 - top;  // keys of the V tile past the last one
-    if (behind > 0) vreg = first_bytes(vreg, 64 - behind - 16 * vpart);
-    lds_u8* const to = lds + buf * kBuf;
-    if (does_k) {
-      *(lds_u32x4*)(to + kto0) = __builtin_bit_cast(u32x4, widen<kBf16>(kreg[0], kreg[1]));
-      *(lds_u32x4*)(to + kto1) = __builtin_bit_cast(u32x4, widen<kBf16>(kreg[2], kreg[3]));
-    }
-    if (does_v) {
-      *(lds_u32x4*)(to + vto0) = __builtin_bit_cast(u32x4, widen<false>(vreg[0], vreg[1]));
-      *(lds_u32x4*)(to + vto1) = __builtin_bit_cast(u32x4, widen<false>(vreg[2], vreg[3]));
-    }
-  };
-  auto phase_end = [&]() {
-    wait_counts<63, 0>();  // LDS only: the codes on their way stay in flight
-    bare_barrier();
-  };
 
   f32x16 o[kDt], s[2];
   f16x8 w[4];
 #pragma unroll
   for (int d = 0; d < kDt; ++d) o[d] = f32x16{};
 #pragma unroll
-  for (int p = 0; p < 4; ++p) w[p] = f16x8{};  // tile -1: no weights, and zeros for its V
+  for (int p = 0; p < 4; ++p) w[p] = f16x8{};
   float base = kNegInf, l = 0.f;
-  const int wave_low = __builtin_amdgcn_readfirstlane(
-      min(seq.len - seq.n + min(kRows * rt + 32 * wave, rows - 1) / group, seq.seen - 1));  // first row's last key
-  const bool wave_full = kRows * rt + 32 * wave + 31 < rows;  // every lane holds a row
-  const int ktok = (i & 19) | ((i & 4) << 1) | ((i & 8) >> 1);  // bits 2 and 3 exchanged
-  int kat[kKs], vat[4];
-#pragma unroll
-  for (int ks = 0; ks < kKs; ++ks) kat[ks] = k_chunk(ktok, 2 * ks + h);
-#pragma unroll
-  for (int p = 0; p < 4; ++p) vat[p] = v_chunk(i, 2 * p + h);
 
-  auto second_product = [&](int j) {
-    const lds_u8* const src = lds + (j & 1) * kBuf;
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-#pragma unroll
-      for (int d = 0; d < kDt; ++d)
-        o[d] = mfma_32x32x16<false>(__builtin_bit_cast(f16x8, *(const lds_u32x4*)(src + vat[p] + d * 32 * 128)), w[p],
-                                    o[d]);
-  };
-  auto scores = [&](int j) {
-    const lds_u8* const src = lds + (j & 1) * kBuf;
-    s[0] = f32x16{};
-    s[1] = f32x16{};
-#pragma unroll
-    for (int ks = 0; ks < kKs; ++ks)
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-        s[a] = mfma_32x32x16<kBf16>(__builtin_bit_cast(f16x8, *(const lds_u32x4*)(src + kat[ks] + a * 32 * kKRow)),
-                                    qf[ks], s[a]);
-  };
-  auto softmax = [&](int j) {
-    const int t0 = 64 * (span.first + j);
-    float f[4], lv[4], iv[4];
-    bool whole = wave_full && t0 + 63 <= wave_low;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const f32x4 sc = sscale[j & 1][p];
-      f[p] = sc[0];
-      lv[p] = sc[1];
-      iv[p] = sc[2];
-      whole = whole && iv[p] > 0.f;
-    }
-    if (!__builtin_amdgcn_readfirstlane(whole)) {
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int p = 2 * a + e / 8, t = t0 + 16 * p + 8 * h + e % 8;
-          s[a][e] = t <= limit && iv[p] > 0.f ? s[a][e] : kNegInf;
-        }
-    }
-    float mt = kNegInf;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      float mp = s[p / 2][8 * (p % 2)];
-#pragma unroll
-      for (int e = 1; e < 8; ++e) mp = fmaxf(mp, s[p / 2][8 * (p % 2) + e]);
-      mt = fmaxf(mt, fmaf(mp, f[p], lv[p]));
-    }
-    mt = fmaxf(mt, __shfl_xor(mt, 32, kWave));
-    if (__any(mt > base + kLazy)) {
-      const float moved = mt > base + kLazy ? mt : base;
-      const float shrink = moved == kNegInf ? 1.f : __builtin_amdgcn_exp2f(base - moved);  // 0 for the first keys
-      base = moved;
-      l *= shrink;
-#pragma unroll
-      for (int d = 0; d < kDt; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[d][e] *= shrink;
-    }
-    const float ref = base == kNegInf ? 0.f : base;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const float off = lv[p] - ref;
-      f32x8 x;
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = __builtin_amdgcn_exp2f(fmaf(s[p / 2][8 * (p % 2) + e], f[p], off));
-        sum += x[e];
+  if (tiles > 0) {
+    const int32_t* const table = c.table + static_cast<size_t>(b) * c.table_width;
+    // Every lane's page numbers and addresses are those of some key of the
+    // sequence, so that all loads go out without branches; what lies outside
+    // the split or behind the last key is never used or counts for nothing.
+    auto page_at = [&](int t) { return table[min(max(t, 0), top) >> c.page_shift]; };
+    auto known = [&](int id) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages); };
+    const uint32_t page_bytes = static_cast<uint32_t>(c.kv_heads) * c.page * D;  // <= 2^24
+
+    // DMA: a wavefront's load fills 1 KB of LDS, lane L the piece at 16 L. K
+    // rows are D bytes, V rows 64 (keys); the 16-byte pieces of a row are
+    // XOR-ed so that 16 lanes of a fragment read fall on different banks
+    // (rows of K in the order above, rows of V consecutive).
+    constexpr int kPer = D / 16;  // pieces of a K row
+    constexpr int kLoads = kBytes / 1024;  // of K, and of V
+    static_assert(kLoads == 8 || kLoads == 4, "one load of both, or of either, per wavefront");
+    auto k_piece = [](int row, int piece) {
+      return D == 128 ? piece ^ (((row >> 1) & 3) | ((row >> 2) & 4)) : piece ^ (((row >> 2) & 1) | ((row >> 3) & 2));
+    };
+    auto v_piece = [](int row, int piece) { return piece ^ ((row >> 2) & 3); };
+    const bool does_k = kLoads == 8 || half == 0, does_v = kLoads == 8 || half == 1;
+    const int wl = wave & (kLoads - 1);
+    const int krow = wl * (1024 / D) + lane / kPer, kfrom = 16 * k_piece(krow, lane % kPer);
+    const int vrow = wl * 16 + lane / 4, vpart = v_piece(vrow, lane % 4);
+    const uint8_t* const kbase = c.k + static_cast<size_t>(head) * c.page * D + kfrom;
+    const uint8_t* const vbase = c.v + static_cast<size_t>(head) * c.page * D + vrow * c.page;
+    int kid, vid;
+    auto request_pages = [&](int j) {
+      kid = page_at(64 * (span.first + j) + krow);
+      vid = page_at(64 * (span.first + j - 1) + 16 * vpart);
+    };
+    auto request_pair = [&](int j) {
+      const int t = 64 * (span.first + j);
+      lds_u8* const to = lds + (j % kSlots) * 2 * kBytes + wl * 1024;
+      if (does_k) {
+        const uint8_t* const p = kbase + static_cast<uint64_t>(known(kid) ? static_cast<uint32_t>(kid) : 0u) * page_bytes +
+                                 ((t + krow) & (c.page - 1)) * D;
+        __builtin_amdgcn_global_load_lds((gbl_void*)p, (lds_void*)to, 16, 0, 0);
       }
-      l = fmaf(sum, fmaxf(iv[p], 0.f), l);
-      w[p] = to_f16(x);
-    }
-  };
+      if (does_v) {
+        const uint8_t* const p = vbase + static_cast<uint64_t>(known(vid) ? static_cast<uint32_t>(vid) : 0u) * page_bytes +
+                                 ((t - 64 + 16 * vpart) & (c.page - 1));
+        __builtin_amdgcn_global_load_lds((gbl_void*)p, (lds_void*)(to + kBytes), 16, 0, 0);
+      }
+    };
+    // Scales of this lane's 16 keys in each half of a tile, requested a tile
+    // ahead, their pages two.
+    int sid[2], okid[2];
+    float ks[2], vs[2];
+    auto request_scale_pages = [&](int j) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) sid[a] = page_at(64 * (span.first + j) + 32 * a + 16 * h);
+    };
+    auto request_scales = [&]() {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        okid[a] = known(sid[a]);
+        const size_t unit = static_cast<size_t>(okid[a] ? sid[a] : 0) * c.kv_heads + head;
+        ks[a] = c.k_scales[unit];
+        vs[a] = c.v_scales[unit];
+      }
+    };
+    auto phase_end = [&]() {
+      wait_counts<63, 0>();  // LDS only: what was requested stays in flight
+      bare_barrier();
+    };
 
-  request_pages(0);
-  fetch(0);
-  stage(0);
-  fetch(1);
-  phase_end();
-  if (half == 1) {  // the second half's first step: it has no product to form yet
-    stage(1);
-    fetch(2);
-    phase_end();
+    // Fragment reads: this lane's K row and its piece 2 kk + h, V row and piece 2 p + h.
+    const int ktok = ((i & 4) << 2) | ((i >> 1) & 12) | (i & 3);
+    int kat[kKk], vat[2];
+#pragma unroll
+    for (int kk = 0; kk < kKk; ++kk) kat[kk] = ktok * D + 16 * k_piece(ktok, 2 * kk + h);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) vat[p] = kBytes + i * 64 + 16 * v_piece(i, 2 * p + h);
+
+    int count[2] = {0, 0};  // keys of this lane's V pieces that exist; before the first tile none
+    bool ragged = true;     // some lane's are fewer than 16
+
+    // A product phase. Reads go out ahead of the MFMAs that use them; the
+    // fences keep them there (one at a time would leave the matrix unit waiting
+    // for each).
+    auto products = [&](int j, auto with_scores) {
+      const lds_u8* const src = lds + (j % kSlots) * 2 * kBytes;
+      u32x4 rv[2][kDt], rk[2][kKk];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int d = 0; d < kDt; ++d) rv[p][d] = *(const lds_u32x4*)(src + vat[p] + d * 32 * 64);
+      auto read_k = [&](int a) {
+        if constexpr (with_scores) {
+#pragma unroll
+          for (int kk = 0; kk < kKk; ++kk) rk[a][kk] = *(const lds_u32x4*)(src + kat[kk] + a * 32 * D);
+        }
+      };
+      if (ragged) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int d = 0; d < kDt; ++d) rv[p][d] = first_bytes(rv[p][d], count[p]);
+      }
+      read_k(0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int d = 0; d < kDt; ++d) {
+          o[d] = mfma_32x32x16<false>(widen<false>(rv[p][d][0], rv[p][d][1]), w[2 * p], o[d]);
+          o[d] = mfma_32x32x16<false>(widen<false>(rv[p][d][2], rv[p][d][3]), w[2 * p + 1], o[d]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (p == 0) read_k(1);
+      }
+      if constexpr (with_scores) {
+        s[0] = f32x16{};
+        s[1] = f32x16{};
+#pragma unroll
+        for (int kk = 0; kk < kKk; ++kk)
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            s[a] = mfma_32x32x16<kBf16>(widen<kBf16>(rk[a][kk][0], rk[a][kk][1]), qf[2 * kk], s[a]);
+            s[a] = mfma_32x32x16<kBf16>(widen<kBf16>(rk[a][kk][2], rk[a][kk][3]), qf[2 * kk + 1], s[a]);
+          }
+      }
+    };
+
+    auto softmax = [&](int j) {
+      const int t0 = 64 * (span.first + j) + 16 * h;
+      float f[2], lv[2], iv[2];
+      int see[2];
+      // Everything that was requested two steps ago has arrived: the pair
+      // that the next phases read, the scales, the page numbers.
+      wait_counts<0, 15>();
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const float v = held_scale(vs[a]);
+        f[a] = fmaxf(ks[a] * scale_log2, 0x1p-126f);  // (0 would turn a masked score's infinity into NaN)
+        lv[a] = __builtin_amdgcn_logf(v);
+        iv[a] = __builtin_amdgcn_rcpf(v);
+        see[a] = okid[a] ? limit - (t0 + 32 * a) : -1;
+        count[a] = okid[a] ? top - (t0 + 32 * a) + 1 : 0;
+      }
+      ragged = __any(min(count[0], count[1]) < 16);
+      request_pair(j + 2 + half);
+      request_pages(j + 3 + half);
+      request_scales();
+      request_scale_pages(j + 2);
+
+      if (__any(min(see[0], see[1]) < 15)) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[a][e] = e <= see[a] ? s[a][e] : kNegInf;
+      }
+      float mt = kNegInf;
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        float ma = s[a][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) ma = fmaxf(ma, s[a][e]);
+        mt = fmaxf(mt, fmaf(ma, f[a], lv[a]));
+      }
+      mt = halves_max(mt);
+      if (__any(mt > base + kLazy)) {
+        const float moved = mt > base + kLazy ? mt : base;
+        const float shrink = moved == kNegInf ? 1.f : __builtin_amdgcn_exp2f(base - moved);  // 0 for the first keys
+        base = moved;
+        l *= shrink;
+#pragma unroll
+        for (int d = 0; d < kDt; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[d][e] *= shrink;
+      }
+      const float ref = base == kNegInf ? 0.f : base;
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const float off = lv[a] - ref;
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          f32x8 x;
+#pragma unroll
+          for (int z = 0; z < 8; ++z) {
+            x[z] = __builtin_amdgcn_exp2f(fmaf(s[a][8 * e + z], f[a], off));
+            sum[e] += x[z];
+          }
+          w[2 * a + e] = to_f16(x);
+          asm volatile("" : "+v"(w[2 * a + e]));  // formed in this phase, not where it is used
+        }
+        l = fmaf(sum[0] + sum[1], iv[a], l);
+      }
+    };
+
+    request_pages(0);
+    request_pair(0);
+    request_pages(1);
+    request_pair(1);
+    request_pages(2);
+    request_scale_pages(0);
+    request_scales();
+    request_scale_pages(1);
+    wait_counts<0, 0>();
+    bare_barrier();
+    if (half == 1) {  // the second half's first step: it has nothing to compute yet
+      request_pair(2);
+      request_pages(3);
+      phase_end();
+    }
+    for (int j = 0; j < tiles; ++j) {
+      products(j, std::true_type{});
+      phase_end();
+      softmax(j);
+      phase_end();
+    }
+    products(tiles, std::false_type{});
+    if (half == 0) phase_end();  // the second half's last softmax phase
+    wait_counts<0, 0>();         // nothing may arrive in LDS after the workgroup has ended
   }
-  for (int j = 0; j < tiles; ++j) {
-    second_product(j);
-    scores(j);
-    phase_end();
-    softmax(j);
-    stage(j + 1 + half);
-    fetch(j + 2 + half);
-    phase_end();
-  }
-  second_product(tiles);
-  if (half == 0) phase_end();  // the second half's last softmax phase
 
   l += __shfl_xor(l, 32, kWave);
   if (!live) return;
