@@ -247,6 +247,29 @@ def test_prompt_long(G):
     _check_attention(rng, [513, 200], [1100, 200], 1, G, 128, 64, "bf16", "long prompts")
 
 
+def test_prompts_of_many_sequences():
+    """More sequences than a wavefront has lanes, some without new tokens, some
+    of several row tiles."""
+    rng = np.random.default_rng(18)
+    news = [int(n) for n in rng.integers(0, 30, 150)]
+    news[0], news[70], news[149] = 0, 300, 200
+    totals = [n + int(t) for n, t in zip(news, rng.integers(0, 60, 150))]
+    _check_attention(rng, news, totals, 1, 4, 64, 16, "bf16", "many sequences", pad=2)
+
+
+@pytest.mark.parametrize("page", [16, 128])
+def test_prompts_over_many_tiles(page):
+    """Workgroups that walk thousands of keys: 64 row tiles, so the keys are
+    hardly split, over up to 54 tiles of 64 with unknown pages among them."""
+    rng = np.random.default_rng(19)
+    totals = [3400, 2111]
+    table = _table(rng, totals, page, 400)
+    cache = _cache(rng, 400, 8, page, 64)
+    _fill(rng, cache, table, totals)
+    table[0, 1100 // page] = table[1, 2000 // page] = -1
+    _check_attention(rng, [66, 300], totals, 8, 32, 64, page, "fp16", "many tiles", cache=cache, table=table)
+
+
 def test_empty_rows_and_padding():
     """No key at all, more new tokens than cached ones, rows of no sequence."""
     rng = np.random.default_rng(7)

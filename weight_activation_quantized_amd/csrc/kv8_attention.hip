@@ -361,40 +361,40 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
 // query heads of the group side by side, so that one K/V tile serves all of
 // them) and walks the keys in tiles of 64; each wavefront has 32 rows.
 //
-// v_mfma_32x32x16: lane (i = lane % 32, h = lane / 32). Row i of half a of a K
-// tile (32 keys) is the key with the bits (4 3 2) of i turned to (3 2 4): lane
-// (i, h) then holds, for row i of Q, in registers 0 .. 15 the scores of the 16
-// consecutive keys 32 a + 16 h + 0 .. 15. They lie in one page, so the scales
-// are lane values, and the first and second eight are, widened to fp16, the B
-// operands of two steps of the second product, whose A operands are the two
-// halves of one 16-byte piece of a V row.
+// v_mfma_32x32x16: lane (i = lane % 32, h = lane / 32). Row i of a K tile is
+// the key with bits 2 and 3 of i exchanged: lane (i, h) then holds, for row i
+// of Q, in registers 8 u .. 8 u + 7 the scores of the consecutive keys
+// 16 u + 8 h .. + 7, the B operand of the second product, and a register's page
+// is the same in every lane.
 //
-// A tile is 1024 cycles of matrix unit per wavefront (D = 128) and as many of
-// vector unit (exponentials first of all), so the two wavefronts of a SIMD take
-// turns: wavefronts 0-3 and 4-7 (one of each per SIMD) walk the same tiles half
-// a step apart, one half in its product phase (second product of tile t - 1,
-// scores of tile t) while the other is in its softmax phase. Every phase ends
-// at a barrier.
+// Per tile and wavefront 1024 cycles of matrix unit (D = 128) face some 230
+// vector operations, 32 of them exponentials of four times the cost, and 32
+// fragments of 16 bytes per lane from LDS, whose bandwidth is another 1024. So
+// - codes are widened once per workgroup on their way into LDS: 16 conversions
+//   per wavefront and tile,
+// - pages and scales come 16 tiles at a time, one part of 16 keys per lane, and
+//   are handed out by v_readlane (scalar loads in every softmax phase, that
+//   each phase had to wait for: 597 us where this took 536),
+// - the reference of the exponentials follows the maximum lazily: it moves (and
+//   the sums are rescaled) only when a score passes it by more than 2^8, so
+//   weights stay at most 2^8 and nearly every tile goes without rescaling.
 //
-// Codes move from memory into LDS untouched (DMA, no registers) and are
-// widened as a wavefront reads them, under its MFMAs: widening them once per
-// workgroup on the way into LDS cost the softmax phase, the longer one, more
-// than it saved, and twice the LDS traffic. What product phase t reads, K of
-// tile t and V of tile t - 1 ("pair t"), is one of three buffers. Phase t of
-// the first half falls on step 2 t, of the second on 2 t + 1; the first half
-// requests pair t + 2 in its softmax phase on step 2 t + 1, the second pair
-// t + 3 on 2 t + 2, when the buffer's last readers (pair t - 1, pair t) are past
-// it, and both wait at the next softmax phase, two steps later, before a
-// barrier that precedes the pair's first use.
+// The two wavefronts of a SIMD take turns: wavefronts 0-3 and 4-7 (one of each
+// per SIMD) walk the same tiles half a step apart, one half in its product
+// phase (second product of tile t - 1, scores of tile t) while the other is in
+// its softmax phase. Every phase ends at a barrier. What product phase t reads,
+// K of tile t and V of tile t - 1 ("pair t"), is one of two buffers: phase t of
+// the first half falls on step 2 t, of the second on 2 t + 1, so the other
+// buffer is free on both, and each half fills its share of it in its product
+// phase, between the MFMAs, from registers loaded a step earlier.
 //
-// The reference of the exponentials follows the maximum lazily: it moves (and
-// the sums are rescaled) only when a score passes it by more than 2^8, so
-// weights stay at most 2^8 and nearly every tile goes without rescaling.
+// Two sequences of about 4096 and 3000 new tokens over 2048, 32 query heads on
+// 8, D = 128: 447 us, 0.87 PFLOP/s. The products alone take 269 us, the softmax
+// alone 262; with both the clock falls to 2.0 GHz (2.2 with half the CUs idle).
 // ---------------------------------------------------------------------------
 
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
-typedef const __attribute__((address_space(1))) void gbl_void;
 
 constexpr float kLazy = 8.f;
 
@@ -407,19 +407,60 @@ __device__ __forceinline__ float halves_max(float x) {
   return fmaxf(lower, upper);
 }
 
+constexpr int kPromptRows = 256;  // rows of a row tile
+
+// The n-th row tile of the call: its sequence (-1: there are fewer) and its
+// number within it. Every wavefront counts the sequences' tiles, 64 sequences
+// at a time, so that the workgroups that have work are the first of the grid:
+// a grid of equal parts for every sequence left half of the CUs without any
+// while the other half worked (two sequences of 4096 and some 3000 tokens:
+// 536 us, 447 with this). Workgroups go to the shader engines in strict turn,
+// those that end at once took the turns of some.
+struct RowTile {
+  int b, rt;
+};
+__device__ __forceinline__ RowTile row_tile(const Kv8Cache& c, int group, int n) {
+  const int lane = threadIdx.x & 63;
+  for (int b0 = 0; b0 < c.batch; b0 += 64) {
+    const int tiles = b0 + lane < c.batch ? (sequence(c, b0 + lane).n * group + kPromptRows - 1) / kPromptRows : 0;
+    int sum = tiles;  // of this sequence and those before it
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int below = __shfl_up(sum, d, kWave);
+      sum += lane >= d ? below : 0;
+    }
+    const uint64_t behind = __ballot(sum > n);
+    if (behind) {
+      const int at = __builtin_ctzll(behind);
+      return {b0 + at, __builtin_amdgcn_readlane(sum, at) - 1 - n};  // the last tile first
+    }
+    n -= __builtin_amdgcn_readlane(sum, 63);
+  }
+  return {-1, 0};
+}
+
 template <int D, bool kBf16>
 __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint16_t* __restrict__ q, int64_t q_stride,
                                                          uint16_t* __restrict__ out, Parts parts, int group,
-                                                         int row_tiles, int splits, float scale_log2) {
-  constexpr int kRows = 256, kKk = D / 32, kDt = D / 32;  // 16-byte steps of a K row per lane; 32-row tiles of V
-  constexpr int kBytes = 64 * D;                          // of K, and of V, in a tile
-  constexpr int kSlots = 3;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * 2 * kBytes];
+                                                         int splits, float scale_log2) {
+  constexpr int kRows = kPromptRows, kKs = D / 16, kDt = D / 32;
+  constexpr int kKRow = 2 * D;  // bytes of a widened K row
+  constexpr int kKBytes = 64 * kKRow, kVBytes = D * 128;
+  constexpr int kBuf = kKBytes + kVBytes;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kBuf];
   lds_u8* const lds = (lds_u8*)(smem);
 
-  // the last rows of a sequence see the most keys: they go first
-  const int rt = row_tiles - 1 - static_cast<int>(blockIdx.x) / splits, split = static_cast<int>(blockIdx.x) % splits;
-  const int head = static_cast<int>(blockIdx.y), b = static_cast<int>(blockIdx.z);
+  // Heads next to each other (the XCDs take workgroups in turn: one that gets
+  // the same head again finds its codes in L2), then sequence by sequence the
+  // row tiles from the last, whose rows see the most keys, down to the first,
+  // so that short workgroups fill the gaps at the end.
+  unsigned at = blockIdx.y * gridDim.x + blockIdx.x;
+  const int head = static_cast<int>(at % c.kv_heads);
+  at /= c.kv_heads;
+  const int split = static_cast<int>(at % splits);
+  const RowTile tile = row_tile(c, group, static_cast<int>(at / splits));
+  if (tile.b < 0) return;
+  const int b = tile.b, rt = tile.rt;
   const Seq seq = sequence(c, b);
   const int rows = seq.n * group;
   if (kRows * rt >= rows) return;
@@ -433,188 +474,203 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
   const int tq = live ? r / group : 0, g = live ? r - tq * group : 0;
   const int limit = live ? min(seq.len - seq.n + tq, seq.seen - 1) : -1;  // last key the row sees
   const uint16_t* const qrow = q + static_cast<int64_t>(seq.row0 + tq) * q_stride + (head * group + g) * D;
-  // k-steps 2 kk and 2 kk + 1 are the halves of the 16-byte pieces 2 kk + h of the K rows
-  f16x8 qf[2 * kKk];
+  f16x8 qf[kKs];
 #pragma unroll
-  for (int ks = 0; ks < 2 * kKk; ++ks) {
+  for (int ks = 0; ks < kKs; ++ks) {
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (live) v = *reinterpret_cast<const u32x4*>(qrow + 32 * (ks / 2) + 16 * h + 8 * (ks % 2));
+    if (live) v = *reinterpret_cast<const u32x4*>(qrow + 16 * ks + 8 * h);
     qf[ks] = __builtin_bit_cast(f16x8, v);
   }
 
   const int last_t = min(kRows * rt + kRows - 1, rows - 1) / group;
-  const int top = min(seq.len - seq.n + last_t, seq.seen - 1);  // the workgroup's last key
+  const int top = __builtin_amdgcn_readfirstlane(min(seq.len - seq.n + last_t, seq.seen - 1));  // the last key
   const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, 8);
-  const int tiles = span.end - span.first;
+  const int first = __builtin_amdgcn_readfirstlane(span.first);
+  const int tiles = __builtin_amdgcn_readfirstlane(span.end - span.first);
 
   f32x16 o[kDt], s[2];
   f16x8 w[4];
 #pragma unroll
   for (int d = 0; d < kDt; ++d) o[d] = f32x16{};
 #pragma unroll
-  for (int p = 0; p < 4; ++p) w[p] = f16x8{};
+  for (int p = 0; p < 4; ++p) w[p] = f16x8{};  // tile -1: no weights, and zeros for its V
   float base = kNegInf, l = 0.f;
 
   if (tiles > 0) {
+    // Pages and scales, 64 parts of 16 keys (a batch of 16 tiles) at a time:
+    // lane p holds those of part p, v_readlane hands them out. The next
+    // batch's pages are requested as a batch begins, their scales six tiles
+    // later. Every index is that of some key of the sequence; what lies behind
+    // the last key counts for nothing.
     const int32_t* const table = c.table + static_cast<size_t>(b) * c.table_width;
-    // Every lane's page numbers and addresses are those of some key of the
-    // sequence, so that all loads go out without branches; what lies outside
-    // the split or behind the last key is never used or counts for nothing.
-    auto page_at = [&](int t) { return table[min(max(t, 0), top) >> c.page_shift]; };
     auto known = [&](int id) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages); };
     const uint32_t page_bytes = static_cast<uint32_t>(c.kv_heads) * c.page * D;  // <= 2^24
 
-    // DMA: a wavefront's load fills 1 KB of LDS, lane L the piece at 16 L. K
-    // rows are D bytes, V rows 64 (keys); the 16-byte pieces of a row are
-    // XOR-ed so that 16 lanes of a fragment read fall on different banks
-    // (rows of K in the order above, rows of V consecutive).
-    constexpr int kPer = D / 16;  // pieces of a K row
-    constexpr int kLoads = kBytes / 1024;  // of K, and of V
-    static_assert(kLoads == 8 || kLoads == 4, "one load of both, or of either, per wavefront");
-    auto k_piece = [](int row, int piece) {
-      return D == 128 ? piece ^ (((row >> 1) & 3) | ((row >> 2) & 4)) : piece ^ (((row >> 2) & 1) | ((row >> 3) & 2));
+    // A wavefront's share of pair j: for D = 128, 8 rows of K (part wave / 2 of
+    // the tile's four parts of 16 keys) and part wave % 4 of 64 rows of V; for
+    // D = 64 the first half brings K, 16 rows per wavefront, the second V.
+    constexpr bool kBoth = D == 128;
+    const bool does_k = kBoth || half == 0, does_v = kBoth || half == 1;
+    const int kpart = kBoth ? wave >> 1 : wave & 3, vpart = wave & 3;
+    const int krow = kBoth ? 8 * wave + (lane >> 3) : 16 * (wave & 3) + (lane >> 2), kch = lane % (D / 16);
+    const int vrow = (kBoth ? 64 * half : 0) + lane;
+    const uint32_t koff = static_cast<uint32_t>((krow & 15) * D + 16 * kch), voff = static_cast<uint32_t>(vrow * c.page);
+    const uint8_t* const khead = c.k + static_cast<size_t>(head) * c.page * D;
+    const uint8_t* const vhead = c.v + static_cast<size_t>(head) * c.page * D;
+    auto batch_pages = [&](int n) {
+      const uint32_t t = 64u * static_cast<uint32_t>(first + 16 * n) + 16u * static_cast<uint32_t>(lane);
+      return table[min(t, static_cast<uint32_t>(top)) >> c.page_shift];
     };
-    auto v_piece = [](int row, int piece) { return piece ^ ((row >> 2) & 3); };
-    const bool does_k = kLoads == 8 || half == 0, does_v = kLoads == 8 || half == 1;
-    const int wl = wave & (kLoads - 1);
-    const int krow = wl * (1024 / D) + lane / kPer, kfrom = 16 * k_piece(krow, lane % kPer);
-    const int vrow = wl * 16 + lane / 4, vpart = v_piece(vrow, lane % 4);
-    const uint8_t* const kbase = c.k + static_cast<size_t>(head) * c.page * D + kfrom;
-    const uint8_t* const vbase = c.v + static_cast<size_t>(head) * c.page * D + vrow * c.page;
-    int kid, vid;
-    auto request_pages = [&](int j) {
-      kid = page_at(64 * (span.first + j) + krow);
-      vid = page_at(64 * (span.first + j - 1) + 16 * vpart);
+    auto unit = [&](int id) { return static_cast<size_t>(known(id) ? id : 0) * c.kv_heads + head; };
+    int id0, id1;             // pages of this batch and of the next
+    uint64_t ok;              // parts whose page is known
+    float ks1, vs1;           // scales of the next batch
+    float f0, off0, iv0;      // of this one: times scale_log2; V's, as log2 and reciprocal
+    auto enter_batch = [&]() {
+      id0 = id1;
+      ok = __ballot(known(id0));
+      const float v = held_scale(vs1);
+      f0 = fmaxf(ks1 * scale_log2, 0x1p-126f);  // (0 would turn a masked score's infinity into NaN)
+      off0 = __builtin_amdgcn_logf(v);
+      iv0 = __builtin_amdgcn_rcpf(v);
     };
-    auto request_pair = [&](int j) {
-      const int t = 64 * (span.first + j);
-      lds_u8* const to = lds + (j % kSlots) * 2 * kBytes + wl * 1024;
+    auto lane_float = [](float v, int at) {
+      return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), at));
+    };
+
+    int held = 0;  // keys of the V part in the registers
+    u32x4 kreg, vreg;
+    auto fetch = [&](int j, int batch) {
+      auto page_of = [&](int t, int part) {  // t: a tile of this batch or the next
+        const int at = 4 * (t & 15) + part;
+        const int here = __builtin_amdgcn_readlane(id0, at), there = __builtin_amdgcn_readlane(id1, at);
+        return t >> 4 == batch ? here : there;
+      };
+      const int tk = 64 * (first + j) + 16 * kpart, tv = 64 * (first + j - 1) + 16 * vpart;
       if (does_k) {
-        const uint8_t* const p = kbase + static_cast<uint64_t>(known(kid) ? static_cast<uint32_t>(kid) : 0u) * page_bytes +
-                                 ((t + krow) & (c.page - 1)) * D;
-        __builtin_amdgcn_global_load_lds((gbl_void*)p, (lds_void*)to, 16, 0, 0);
+        const int id = page_of(j, kpart);
+        const uint8_t* const p = khead + static_cast<uint64_t>(known(id) ? static_cast<uint32_t>(id) : 0u) * page_bytes +
+                                 static_cast<uint32_t>((tk & (c.page - 1)) * D);
+        kreg = *reinterpret_cast<const u32x4*>(p + koff);
       }
       if (does_v) {
-        const uint8_t* const p = vbase + static_cast<uint64_t>(known(vid) ? static_cast<uint32_t>(vid) : 0u) * page_bytes +
-                                 ((t - 64 + 16 * vpart) & (c.page - 1));
-        __builtin_amdgcn_global_load_lds((gbl_void*)p, (lds_void*)(to + kBytes), 16, 0, 0);
+        const int id = page_of(j > 0 ? j - 1 : 0, vpart);
+        const uint8_t* const p = vhead + static_cast<uint64_t>(known(id) ? static_cast<uint32_t>(id) : 0u) * page_bytes +
+                                 static_cast<uint32_t>(tv & (c.page - 1));
+        vreg = *reinterpret_cast<const u32x4*>(p + voff);
+        held = known(id) && j > 0 ? top - tv + 1 : 0;  // (the tile before the first: none)
       }
     };
-    // Scales of this lane's 16 keys in each half of a tile, requested a tile
-    // ahead, their pages two.
-    int sid[2], okid[2];
-    float ks[2], vs[2];
-    auto request_scale_pages = [&](int j) {
-#pragma unroll
-      for (int a = 0; a < 2; ++a) sid[a] = page_at(64 * (span.first + j) + 32 * a + 16 * h);
+    // 16-byte chunk positions are XOR-ed by the row, so that a fragment read of
+    // 32 rows meets no bank twice: K rows of 256 bytes by 16 rows, of 128 bytes
+    // (and V rows) by pairs of rows.
+    auto k_chunk = [](int row, int ch) {
+      return row * kKRow + 16 * (D == 128 ? ch ^ (row & 15) : ch ^ ((row >> 1) & 7));
     };
-    auto request_scales = [&]() {
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        okid[a] = known(sid[a]);
-        const size_t unit = static_cast<size_t>(okid[a] ? sid[a] : 0) * c.kv_heads + head;
-        ks[a] = c.k_scales[unit];
-        vs[a] = c.v_scales[unit];
+    auto v_chunk = [](int row, int ch) { return kKBytes + row * 128 + 16 * (ch ^ ((row >> 1) & 7)); };
+    const int kto0 = k_chunk(krow, 2 * kch), kto1 = k_chunk(krow, 2 * kch + 1);
+    const int vto0 = v_chunk(vrow, 2 * vpart), vto1 = v_chunk(vrow, 2 * vpart + 1);
+    // One of the four steps that bring pair j from the registers to LDS.
+    auto stage = [&](int j, int step) {
+      lds_u8* const to = lds + (j & 1) * kBuf;
+      if (step < 2) {
+        if (does_k)
+          *(lds_u32x4*)(to + (step == 0 ? kto0 : kto1)) =
+              __builtin_bit_cast(u32x4, widen<kBf16>(kreg[2 * step], kreg[2 * step + 1]));
+      } else if (does_v) {
+        if (step == 2 && held < 16) vreg = first_bytes(vreg, held);
+        *(lds_u32x4*)(to + (step == 2 ? vto0 : vto1)) =
+            __builtin_bit_cast(u32x4, widen<false>(vreg[2 * step - 4], vreg[2 * step - 3]));
       }
     };
     auto phase_end = [&]() {
-      wait_counts<63, 0>();  // LDS only: what was requested stays in flight
+      wait_counts<63, 0>();  // LDS only: the codes on their way stay in flight
       bare_barrier();
     };
 
-    // Fragment reads: this lane's K row and its piece 2 kk + h, V row and piece 2 p + h.
-    const int ktok = ((i & 4) << 2) | ((i >> 1) & 12) | (i & 3);
-    int kat[kKk], vat[2];
+    const int wave_low = __builtin_amdgcn_readfirstlane(
+        min(seq.len - seq.n + min(kRows * rt + 32 * wave, rows - 1) / group, seq.seen - 1));  // first row's last key
+    const int wave_whole = kRows * rt + 32 * wave + 31 < rows ? wave_low : -1;  // keys that every lane sees
+    const int ktok = (i & 19) | ((i & 4) << 1) | ((i & 8) >> 1);  // bits 2 and 3 exchanged
+    int kat[kKs], vat[4];
 #pragma unroll
-    for (int kk = 0; kk < kKk; ++kk) kat[kk] = ktok * D + 16 * k_piece(ktok, 2 * kk + h);
+    for (int x = 0; x < kKs; ++x) kat[x] = k_chunk(ktok, 2 * x + h);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) vat[p] = kBytes + i * 64 + 16 * v_piece(i, 2 * p + h);
+    for (int p = 0; p < 4; ++p) vat[p] = v_chunk(i, 2 * p + h);
 
-    int count[2] = {0, 0};  // keys of this lane's V pieces that exist; before the first tile none
-    bool ragged = true;     // some lane's are fewer than 16
-
-    // A product phase. Reads go out ahead of the MFMAs that use them; the
-    // fences keep them there (one at a time would leave the matrix unit waiting
-    // for each).
-    auto products = [&](int j, auto with_scores) {
-      const lds_u8* const src = lds + (j % kSlots) * 2 * kBytes;
-      u32x4 rv[2][kDt], rk[2][kKk];
+    // A product phase: fragments come from LDS in groups of four, two groups
+    // ahead of their MFMAs (the fences hold that order; one read at a time
+    // would leave the matrix unit waiting for every one of them).
+    constexpr int kV = 4 * kDt, kAll = kV + 2 * kKs;  // fragments of V, of both
+    auto products = [&](int j, int batch, auto with_scores) {
+      constexpr int kGroups = (with_scores ? kAll : kV) / 4;
+      const lds_u8* const src = lds + (j & 1) * kBuf;
+      u32x4 f[3][4];
+      auto read = [&](int gr) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int d = 0; d < kDt; ++d) rv[p][d] = *(const lds_u32x4*)(src + vat[p] + d * 32 * 64);
-      auto read_k = [&](int a) {
-        if constexpr (with_scores) {
-#pragma unroll
-          for (int kk = 0; kk < kKk; ++kk) rk[a][kk] = *(const lds_u32x4*)(src + kat[kk] + a * 32 * D);
+        for (int e = 0; e < 4; ++e) {
+          const int n = 4 * gr + e;
+          f[gr % 3][e] = n < kV ? *(const lds_u32x4*)(src + vat[n / kDt % 4] + (n % kDt) * 32 * 128)
+                                : *(const lds_u32x4*)(src + kat[(n - kV) / 2 % kKs] + ((n - kV) & 1) * 32 * kKRow);
         }
       };
-      if (ragged) {
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int d = 0; d < kDt; ++d) rv[p][d] = first_bytes(rv[p][d], count[p]);
-      }
-      read_k(0);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-#pragma unroll
-        for (int d = 0; d < kDt; ++d) {
-          o[d] = mfma_32x32x16<false>(widen<false>(rv[p][d][0], rv[p][d][1]), w[2 * p], o[d]);
-          o[d] = mfma_32x32x16<false>(widen<false>(rv[p][d][2], rv[p][d][3]), w[2 * p + 1], o[d]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        if (p == 0) read_k(1);
-      }
       if constexpr (with_scores) {
         s[0] = f32x16{};
         s[1] = f32x16{};
+      }
+      read(0);
+      read(1);
 #pragma unroll
-        for (int kk = 0; kk < kKk; ++kk)
+      for (int gr = 0; gr < kGroups; ++gr) {
+        if (gr + 2 < kGroups) read(gr + 2);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int a = 0; a < 2; ++a) {
-            s[a] = mfma_32x32x16<kBf16>(widen<kBf16>(rk[a][kk][0], rk[a][kk][1]), qf[2 * kk], s[a]);
-            s[a] = mfma_32x32x16<kBf16>(widen<kBf16>(rk[a][kk][2], rk[a][kk][3]), qf[2 * kk + 1], s[a]);
+        for (int e = 0; e < 4; ++e) {
+          const int n = 4 * gr + e;
+          const f16x8 x = __builtin_bit_cast(f16x8, f[gr % 3][e]);
+          if (n < kV) {
+            o[n % kDt] = mfma_32x32x16<false>(x, w[n / kDt % 4], o[n % kDt]);
+          } else {
+            s[(n - kV) & 1] = mfma_32x32x16<kBf16>(x, qf[(n - kV) / 2 % kKs], s[(n - kV) & 1]);
           }
+          if (with_scores && gr == 1) {
+            __builtin_amdgcn_sched_barrier(0);
+            stage(j + 1, e);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        if (with_scores && gr == 2) fetch(j + 2, batch);
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
 
     auto softmax = [&](int j) {
-      const int t0 = 64 * (span.first + j) + 16 * h;
-      float f[2], lv[2], iv[2];
-      int see[2];
-      // Everything that was requested two steps ago has arrived: the pair
-      // that the next phases read, the scales, the page numbers.
-      wait_counts<0, 15>();
+      const int t0 = 64 * (first + j);
+      const int part = 4 * (j & 15);
+      const int seen = static_cast<int>(ok >> part) & 15;
+      float f[4], off[4], iv[4];
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const float v = held_scale(vs[a]);
-        f[a] = fmaxf(ks[a] * scale_log2, 0x1p-126f);  // (0 would turn a masked score's infinity into NaN)
-        lv[a] = __builtin_amdgcn_logf(v);
-        iv[a] = __builtin_amdgcn_rcpf(v);
-        see[a] = okid[a] ? limit - (t0 + 32 * a) : -1;
-        count[a] = okid[a] ? top - (t0 + 32 * a) + 1 : 0;
+      for (int p = 0; p < 4; ++p) {
+        f[p] = lane_float(f0, part + p);
+        off[p] = lane_float(off0, part + p);
+        iv[p] = lane_float(iv0, part + p);
       }
-      ragged = __any(min(count[0], count[1]) < 16);
-      request_pair(j + 2 + half);
-      request_pages(j + 3 + half);
-      request_scales();
-      request_scale_pages(j + 2);
-
-      if (__any(min(see[0], see[1]) < 15)) {
+      if (seen != 15 || t0 + 63 > wave_whole) {
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[a][e] = e <= see[a] ? s[a][e] : kNegInf;
+          for (int e = 0; e < 16; ++e) {
+            const int p = 2 * a + e / 8;
+            s[a][e] = ((seen >> p) & 1) && t0 + 16 * p + 8 * h + e % 8 <= limit ? s[a][e] : kNegInf;
+          }
       }
       float mt = kNegInf;
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        float ma = s[a][0];
+      for (int p = 0; p < 4; ++p) {
+        float mp = s[p / 2][8 * (p % 2)];
 #pragma unroll
-        for (int e = 1; e < 16; ++e) ma = fmaxf(ma, s[a][e]);
-        mt = fmaxf(mt, fmaf(ma, f[a], lv[a]));
+        for (int e = 1; e < 8; ++e) mp = fmaxf(mp, s[p / 2][8 * (p % 2) + e]);
+        mt = fmaxf(mt, fmaf(mp, f[p], off[p]));
       }
       mt = halves_max(mt);
       if (__any(mt > base + kLazy)) {
@@ -629,48 +685,49 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
       }
       const float ref = base == kNegInf ? 0.f : base;
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const float off = lv[a] - ref;
-        float sum[2] = {0.f, 0.f};
+      for (int p = 0; p < 4; ++p) {
+        const float b0 = off[p] - ref;
+        f32x8 x;
+        float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          f32x8 x;
-#pragma unroll
-          for (int z = 0; z < 8; ++z) {
-            x[z] = __builtin_amdgcn_exp2f(fmaf(s[a][8 * e + z], f[a], off));
-            sum[e] += x[z];
-          }
-          w[2 * a + e] = to_f16(x);
-          asm volatile("" : "+v"(w[2 * a + e]));  // formed in this phase, not where it is used
+        for (int e = 0; e < 8; ++e) {
+          x[e] = __builtin_amdgcn_exp2f(fmaf(s[p / 2][8 * (p % 2) + e], f[p], b0));
+          sum += x[e];
         }
-        l = fmaf(sum[0] + sum[1], iv[a], l);
+        l = fmaf(sum, iv[p], l);
+        w[p] = to_f16(x);
       }
     };
 
-    request_pages(0);
-    request_pair(0);
-    request_pages(1);
-    request_pair(1);
-    request_pages(2);
-    request_scale_pages(0);
-    request_scales();
-    request_scale_pages(1);
-    wait_counts<0, 0>();
-    bare_barrier();
-    if (half == 1) {  // the second half's first step: it has nothing to compute yet
-      request_pair(2);
-      request_pages(3);
-      phase_end();
-    }
+    id1 = batch_pages(0);
+    ks1 = c.k_scales[unit(id1)];
+    vs1 = c.v_scales[unit(id1)];
+    enter_batch();
+    fetch(0, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) stage(0, e);
+    fetch(1, 0);
+    phase_end();
+    if (half == 1) phase_end();  // the second half is a step behind
     for (int j = 0; j < tiles; ++j) {
-      products(j, std::true_type{});
+      const int batch = j >> 4;
+      if ((j & 15) == 0) {
+        if (j > 0) enter_batch();
+        id1 = batch_pages(batch + 1);
+      }
+      if ((j & 15) == 6) {
+        ks1 = c.k_scales[unit(id1)];
+        vs1 = c.v_scales[unit(id1)];
+      }
+      __builtin_amdgcn_s_setprio(1);  // its MFMAs go before the other half's vector work
+      products(j, batch, std::true_type{});
+      __builtin_amdgcn_s_setprio(0);
       phase_end();
       softmax(j);
       phase_end();
     }
-    products(tiles, std::false_type{});
+    products(tiles, 0, std::false_type{});
     if (half == 0) phase_end();  // the second half's last softmax phase
-    wait_counts<0, 0>();         // nothing may arrive in LDS after the workgroup has ended
   }
 
   l += __shfl_xor(l, 32, kWave);
@@ -722,11 +779,11 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, ui
     e = launch_kernel(kv8_decode_kernel<D, kBf16>, grid, dim3(256), 0, stream, c, q, q_stride, out, parts, group,
                       row_tiles, plan.splits, scale_log2);
   } else {
-    const int row_tiles = static_cast<int>((rows + 255) / 256);
-    const dim3 grid(static_cast<uint32_t>(row_tiles * plan.splits), static_cast<uint32_t>(c.kv_heads),
-                    static_cast<uint32_t>(c.batch));
+    constexpr int64_t kWide = int64_t{1} << 22;  // a dimension of the grid stays under 2^32 work-items
+    const dim3 grid(static_cast<uint32_t>(plan.prompt_blocks < kWide ? plan.prompt_blocks : kWide),
+                    static_cast<uint32_t>((plan.prompt_blocks + kWide - 1) / kWide));
     e = launch_kernel(kv8_prompt_kernel<D, kBf16>, grid, dim3(512), 0, stream, c, q, q_stride, out, parts, group,
-                      row_tiles, plan.splits, scale_log2);
+                      plan.splits, scale_log2);
   }
   if (e != hipSuccess || plan.splits == 1) return e;
   return launch_kernel(kv8_join_kernel<D, kBf16>, dim3(static_cast<uint32_t>((all + 3) / 4)), dim3(256), 0, stream, c,
@@ -746,7 +803,12 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
   const int64_t rows = static_cast<int64_t>(most) * group;
   p.decode = rows <= kDecodeRows;
   const int64_t tiles = (static_cast<int64_t>(c.table_width) * c.page + 63) / 64;
-  const int64_t groups = static_cast<int64_t>(c.batch) * c.kv_heads * (p.decode ? (rows + 15) / 16 : (rows + 255) / 256);
+  int64_t row_tiles = c.batch * (p.decode ? (rows + 15) / 16 : (rows + kPromptRows - 1) / kPromptRows);
+  if (!p.decode) {  // no more than if every sequence left the last of its tiles all but empty
+    const int64_t bound = (static_cast<int64_t>(c.tokens) * group + int64_t{kPromptRows - 1} * c.batch) / kPromptRows;
+    if (row_tiles > bound) row_tiles = bound;
+  }
+  const int64_t groups = row_tiles * c.kv_heads;
   const int64_t target = p.decode ? 2048 : 256, least = p.decode ? 4 : 8;
   int64_t splits = groups > 0 ? target / groups : 1;
   const int64_t fit = (tiles + least - 1) / least;
@@ -755,6 +817,7 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
   // the joining kernel takes four rows per workgroup of 256: under 2^32 work-items
   if (static_cast<int64_t>(c.tokens) * q_heads >= (int64_t{1} << 26)) splits = 1;
   p.splits = splits < 1 ? 1 : static_cast<int>(splits);
+  p.prompt_blocks = p.decode ? 0 : groups * p.splits;
   p.workspace_bytes =
       p.splits > 1 ? static_cast<size_t>(p.splits) * c.tokens * q_heads * (c.head_dim + 2) * sizeof(float) : 0;
   return p;

@@ -108,6 +108,7 @@ hipError_t launch_kv8_append(const Kv8Cache& c, const uint16_t* k, const uint16_
 struct Kv8Plan {
   bool decode;  // the rows of one kv head fit a few tiles of 16: the streaming form
   int splits;
+  int64_t prompt_blocks;  // workgroups of the other form
   size_t workspace_bytes;
 };
 Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads);
