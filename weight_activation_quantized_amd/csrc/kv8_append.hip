@@ -16,15 +16,18 @@
 // every time). K rows go out as they come. V pages are stored transposed,
 // [head_dim, page]: the attention's second product then reads 16 tokens of one
 // dimension with one load; the transposition happens here, once per token, in
-// LDS.
+// registers and LDS.
+//
+// Bound by latency (lengths, page, rows, maximum, codes follow from each other)
+// for few tokens, 5.1 us for 64 sequences of one; for prompts by that and HBM:
+// 3 x 2048 tokens of 8 heads of 128 take 11.9 us, 2.9 TB/s (with single codes
+// into unpadded LDS, 16 lanes on one bank, and IEEE divisions 18.5 us).
 #include "device_common.h"
 #include "launch.h"
 #include "quant_codes.h"
 
 namespace mq {
 namespace {
-
-constexpr int kThreads = 256;
 
 // Smallest power of two s with a <= 448 s, its exponent held in [-100, 120].
 // 448 = 1.75 * 2^8: with a = 1.m * 2^e the exponent is e - 8 for a fraction up
@@ -45,14 +48,32 @@ __device__ __forceinline__ uint32_t moved(uint32_t w, float ratio) {
   return e4m3x4(clamp448(a[0] * ratio), clamp448(a[1] * ratio), clamp448(b[0] * ratio), clamp448(b[1] * ratio));
 }
 
-// CPT: 16-byte chunks (8 values) of a page's rows per thread.
-template <int D, int CPT, bool kBf16>
+// The bytes of four words as columns: byte e of word t becomes byte t of out[e].
+__device__ __forceinline__ void turned(const uint32_t (&w)[4], uint32_t (&out)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400), b = __builtin_amdgcn_perm(w[3], w[2], 0x05010400);
+  const uint32_t c = __builtin_amdgcn_perm(w[1], w[0], 0x07030602), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602);
+  out[0] = __builtin_amdgcn_perm(b, a, 0x05040100);
+  out[1] = __builtin_amdgcn_perm(b, a, 0x07060302);
+  out[2] = __builtin_amdgcn_perm(d, c, 0x05040100);
+  out[3] = __builtin_amdgcn_perm(d, c, 0x07060302);
+}
+
+constexpr int kSmallPage = 4096;  // bytes of a page's head that one wavefront takes at most
+
+// CPT: 16-byte chunks (8 values) of a page's rows per thread. With four or more
+// a thread of V takes them from four consecutive tokens (of the page: from a
+// multiple of four), turns the 4 x 8 codes in registers and writes words to
+// LDS; with fewer it writes single codes.
+template <int D, int kThreads, int CPT, bool kBf16>
 __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, const uint16_t* __restrict__ k,
                                                               const uint16_t* __restrict__ v, int64_t k_stride,
                                                               int64_t v_stride, int span) {
   constexpr int kDc = D / 8;  // chunks per row
   __shared__ float wmax[kThreads / 64];
-  __shared__ __attribute__((aligned(16))) uint8_t tile[D * (128 + 16)];
+  constexpr bool kQuads = CPT % 4 == 0;
+  // V of the page as [D, page], 16 bytes of padding after every 8 rows: lanes
+  // that write the same token of rows 8 apart meet no bank twice
+  __shared__ __attribute__((aligned(16))) uint8_t tile[(kThreads == 64 ? kSmallPage : D * 128) + D / 8 * 16];
 
   // blockIdx.x = ((sequence * span + page) * kv_heads + head) * 2 + (0: K, 1: V)
   unsigned at = blockIdx.x;
@@ -69,61 +90,80 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, const 
   const int64_t pos0 = static_cast<int64_t>(slot) * c.page;
   if (pos0 >= len) return;
   const int id = c.table[static_cast<size_t>(b) * c.table_width + slot];
-  if (id < 0 || id >= c.num_pages) return;
+  const bool known = id >= 0 && id < c.num_pages;
   const int lo = max(start - static_cast<int>(pos0), 0);                    // first new token of the page
   // behind the last (a sequence longer than max_q_len is cut to what the
   // registers hold, never read or written past them)
-  const int hi = min(min(len - static_cast<int>(pos0), c.page), lo + CPT * kThreads / kDc);
+  const int hi = min(min(len - static_cast<int>(pos0), c.page), (kQuads ? lo & ~3 : lo) + CPT * kThreads / kDc);
   const int64_t row0 = first_row + pos0 - start;  // row of the page's token 0
+  const size_t unit = static_cast<size_t>(known ? id : 0) * c.kv_heads + head;
+  float* const scale_at = (is_v ? c.v_scales : c.k_scales) + unit;
+  uint8_t* const out = (is_v ? c.v : c.k) + unit * c.page * D;
+  const float old = lo > 0 ? *scale_at : 0.f;
 
+  // Token and first dimension of this thread's chunk i.
+  const bool quads = kQuads && is_v;
+  auto token = [&](int i) {
+    return quads ? (lo & ~3) + 4 * ((static_cast<int>(threadIdx.x) + kThreads * (i / 4)) / kDc) + i % 4
+                 : lo + (static_cast<int>(threadIdx.x) + kThreads * i) / kDc;
+  };
+  const int d = 8 * (static_cast<int>(threadIdx.x) % kDc);  // (kDc divides kThreads)
   const uint16_t* const x = is_v ? v : k;
   const int64_t stride = is_v ? v_stride : k_stride;
   u32x4 w[CPT];
-  float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
-    const int ch = static_cast<int>(threadIdx.x) + kThreads * i;
-    const int t = lo + ch / kDc;
+    const int t = token(i);
     const int64_t row = row0 + t;
     w[i] = u32x4{0u, 0u, 0u, 0u};
-    if (t < hi && row >= 0 && row < c.tokens)
-      w[i] = *reinterpret_cast<const u32x4*>(x + row * stride + head * D + 8 * (ch % kDc));
+    if (t >= lo && t < hi && row >= 0 && row < c.tokens)
+      w[i] = *reinterpret_cast<const u32x4*>(x + row * stride + head * D + d);
+  }
+  if (!known) return;  // (the page's number was on its way with the rows)
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float a, z;
       word_to_floats<kBf16>(w[i][e], a, z);
       amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(z)));
     }
-  }
   amax = wave_max(amax);
   if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = amax;
   __syncthreads();
-  amax = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) amax = fmaxf(amax, wmax[i]);
 
-  const size_t unit = static_cast<size_t>(id) * c.kv_heads + head;
-  float* const scale_at = (is_v ? c.v_scales : c.k_scales) + unit;
-  uint8_t* const out = (is_v ? c.v : c.k) + unit * c.page * D;
   float s = page_scale(amax);
   if (lo > 0) {  // the page holds older tokens
-    const float old = *scale_at;
     if (s > old) {
       const float ratio = old / s;
-      if (!is_v) {
-        for (int i = threadIdx.x; i < lo * D / 4; i += kThreads) {
-          uint32_t* const p = reinterpret_cast<uint32_t*>(out) + i;
-          *p = moved(*p, ratio);
+      // 16 bytes at a time, a thread's loads together: of K rows all bytes, of
+      // V rows (one dimension, `page` tokens) those of tokens before lo; the
+      // others keep theirs (new codes are written after the barrier)
+      const int per = is_v ? (lo + 15) / 16 : D / 16, all = (is_v ? D : lo) * per, pitch = is_v ? c.page : D;
+      constexpr int kAtOnce = CPT >= 4 ? 2 : 4;
+      for (int i0 = threadIdx.x; i0 < all; i0 += kAtOnce * kThreads) {
+        int at[kAtOnce], keep[kAtOnce];
+        u32x4 v[kAtOnce];
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+          const int i = min(i0 + e * kThreads, all - 1), row = i / per, col = i - row * per;
+          at[e] = row * pitch + 16 * col;
+          keep[e] = i0 + e * kThreads < all ? (is_v ? min(lo - 16 * col, 16) : 16) : 0;
+          v[e] = *reinterpret_cast<const u32x4*>(out + at[e]);
         }
-      } else {
-        // words of four tokens of one dimension; the tokens from lo on keep
-        // their bytes (new ones are written after the barrier)
-        const int words = (lo + 3) / 4;
-        for (int i = threadIdx.x; i < words * D; i += kThreads) {
-          const int d = i / words, wd = i - d * words;
-          uint32_t* const p = reinterpret_cast<uint32_t*>(out + static_cast<size_t>(d) * c.page + 4 * wd);
-          const int keep = min(lo - 4 * wd, 4);
-          const uint32_t mask = keep == 4 ? 0xffffffffu : (1u << (8 * keep)) - 1u;
-          const uint32_t before = *p;
-          *p = (moved(before, ratio) & mask) | (before & ~mask);
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+          if (keep[e] == 0) continue;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int k = min(max(keep[e] - 4 * q, 0), 4);
+            const uint32_t mask = k == 4 ? 0xffffffffu : (1u << (8 * k)) - 1u;
+            v[e][q] = (moved(v[e][q], ratio) & mask) | (v[e][q] & ~mask);
+          }
+          *reinterpret_cast<u32x4*>(out + at[e]) = v[e];
         }
       }
     } else {
@@ -133,35 +173,64 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, const 
   __syncthreads();  // every lane has read the old scale, and older codes are in place
   if (threadIdx.x == 0) *scale_at = s;
 
+  // x / s. The scales that this kernel makes are powers of two of normal
+  // reciprocal: their product is the quotient, bit for bit (one exact scaling
+  // and at most one rounding in both). Others may stand in a cache that was
+  // filled otherwise.
+  const uint32_t sb = __builtin_bit_cast(uint32_t, s);
+  const bool simple = (sb & 0x7fffffu) == 0 && sb >= 0x01000000u && sb <= 0x7e000000u;
+  const float r = 1.f / s;
+  auto quotient = [&](float a) { return clamp448(simple ? a * r : a / s); };
+  u32x2 codes[CPT];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
-    const int ch = static_cast<int>(threadIdx.x) + kThreads * i;
-    const int t = lo + ch / kDc, d = 8 * (ch % kDc);
     float f[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float a, z;
       word_to_floats<kBf16>(w[i][e], a, z);
-      f[2 * e] = clamp448(a / s);
-      f[2 * e + 1] = clamp448(z / s);
+      f[2 * e] = quotient(a);
+      f[2 * e + 1] = quotient(z);
     }
-    const u32x2 codes = {e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7])};
-    if (t >= hi) continue;
-    if (!is_v) {
-      *reinterpret_cast<u32x2*>(out + static_cast<size_t>(t) * D + d) = codes;
-    } else {
+    codes[i] = u32x2{e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7])};
+  }
+  if (!is_v) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) tile[(d + e) * (128 + 16) + t] = static_cast<uint8_t>(codes[e >> 2] >> (8 * (e & 3)));
+    for (int i = 0; i < CPT; ++i)
+      if (token(i) < hi) *reinterpret_cast<u32x2*>(out + static_cast<size_t>(token(i)) * D + d) = codes[i];
+    return;
+  }
+  uint8_t* const rows = tile + d * c.page + 2 * d;  // (16 bytes for every 8 rows)
+  if constexpr (kQuads) {
+#pragma unroll
+    for (int i = 0; i < CPT; i += 4) {
+      const int t = token(i);
+      if (t >= hi) continue;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t in[4] = {codes[i][p], codes[i + 1][p], codes[i + 2][p], codes[i + 3][p]};
+        uint32_t turn[4];
+        turned(in, turn);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t*>(rows + (4 * p + e) * c.page + t) = turn[e];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int t = token(i);
+      if (t >= hi) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) rows[e * c.page + t] = static_cast<uint8_t>(codes[i][e >> 2] >> (8 * (e & 3)));
     }
   }
-  if (!is_v) return;
   __syncthreads();
   // 16 tokens of one dimension per store where all of them are new
   const int g0 = lo / 16, groups = (hi + 15) / 16 - g0;
   for (int i = threadIdx.x; i < groups * D; i += kThreads) {
-    const int d = i / groups, g = g0 + i - d * groups;
-    const uint8_t* const src = tile + d * (128 + 16) + 16 * g;
-    uint8_t* const dst = out + static_cast<size_t>(d) * c.page + 16 * g;
+    const int row = i / groups, g = g0 + i - row * groups;
+    const uint8_t* const src = tile + row * c.page + 16 * (row / 8) + 16 * g;
+    uint8_t* const dst = out + static_cast<size_t>(row) * c.page + 16 * g;
     if (16 * g >= lo && 16 * g + 16 <= hi) {
       *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(src);
     } else {
@@ -184,16 +253,21 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* k, const uint16_t* v, i
   const int span = page_span(c);
   const int64_t blocks = kv8_append_blocks(c);
   if (blocks >= (int64_t{1} << 24)) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<uint32_t>(blocks)), block(kThreads);
-  // a call of few tokens per sequence never fills a page: its rows need fewer registers
+  const dim3 grid(static_cast<uint32_t>(blocks));
+  // A call of few tokens per sequence never fills a page: its rows need fewer
+  // registers, and with little to move in a page one wavefront does (64
+  // sequences of one token, pages of 16: 5.1 us, with four wavefronts 5.6).
+  // Three more tokens where threads take four at a time.
   const int rows = most < c.page ? most : c.page;
-  const int chunks = rows * (D / 8);
-#define MQ_APPEND(CPT)                                                                                            \
-  return launch_kernel(kv8_append_kernel<D, CPT, kBf16>, grid, block, 0, stream, c, k, v, k_stride, v_stride, span)
-  if (chunks <= kThreads) MQ_APPEND(1);
-  if (chunks <= 2 * kThreads) MQ_APPEND(2);
-  if (chunks <= 4 * kThreads) MQ_APPEND(4);
-  MQ_APPEND(8);
+  const int chunks = rows * (D / 8), padded = (rows + 3 < c.page ? rows + 3 : c.page) * (D / 8);
+#define MQ_APPEND(TH, CPT)                                                                                         \
+  return launch_kernel(kv8_append_kernel<D, TH, CPT, kBf16>, grid, dim3(TH), 0, stream, c, k, v, k_stride, v_stride, \
+                       span)
+  if (chunks <= 64 && c.page * D <= kSmallPage) MQ_APPEND(64, 1);
+  if (chunks <= 256) MQ_APPEND(256, 1);
+  if (chunks <= 512) MQ_APPEND(256, 2);
+  if (padded <= 1024) MQ_APPEND(256, 4);
+  MQ_APPEND(256, 8);
 #undef MQ_APPEND
 }
 
