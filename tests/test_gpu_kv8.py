@@ -325,6 +325,15 @@ def test_split_keys(news):
     _check_attention(rng, news, [0], 1, 4, 64, 16, "fp16", "wide table, nothing cached", width=4096)
 
 
+@pytest.mark.parametrize("tiles", [9, 17, 65, 66, 67, 129, 133, 261])
+def test_every_number_of_splits(tiles):
+    """From two to all of the splits, odd numbers too; the last key alone in its
+    tile. Beside it a short sequence, whose splits are mostly without keys."""
+    rng = np.random.default_rng(tiles)
+    _check_attention(rng, [1], [64 * tiles - 63], 1, 2, 64, 64, "bf16", f"{tiles} tiles", qamp=3.0)
+    _check_attention(rng, [1, 1], [64 * tiles - 63, 70], 1, 4, 128, 32, "fp16", f"{tiles} tiles and two", qamp=3.0)
+
+
 def test_one_query_row_is_its_value():
     """A sequence of one token: the output is that token's value, rounded once."""
     rng = np.random.default_rng(12)

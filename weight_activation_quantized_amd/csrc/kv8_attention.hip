@@ -129,9 +129,11 @@ __global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint1
   __shared__ float so[4][16][D + 4];
   __shared__ float sm[4][16], sl[4][16];
 
-  const int split = static_cast<int>(blockIdx.x) % splits;
-  const int head = static_cast<int>(blockIdx.y) % c.kv_heads, rt = static_cast<int>(blockIdx.y) / c.kv_heads;
-  const int b = static_cast<int>(blockIdx.z);
+  // splits come last: those that find no keys (wide tables, short sequences)
+  // follow those that do, instead of taking the turns of some XCDs, and only
+  // say so (16 sequences of 500 keys, tables for 32768: 25.8 -> 11.0 us)
+  const int head = static_cast<int>(blockIdx.x) % c.kv_heads, rt = static_cast<int>(blockIdx.x) / c.kv_heads;
+  const int b = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z);
   const Seq seq = sequence(c, b);
   const int rows = seq.n * group;
   if (16 * rt >= rows) return;  // uniform: the whole workgroup leaves
@@ -157,6 +159,14 @@ __global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint1
   const int last_t = min(16 * rt + 15, rows - 1) / group;
   const int top = min(seq.len - seq.n + last_t, seq.seen - 1);  // the row tile's last key
   const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, 4);
+  const size_t all_rows = static_cast<size_t>(c.tokens) * heads;
+  if (splits > 1 && span.first >= span.end) {  // no keys: sums of zero, whose outputs nobody reads
+    if (threadIdx.x < 16 && live) {
+      const size_t to = static_cast<size_t>(seq.row0 + tq) * heads + head * group + g;
+      *reinterpret_cast<f32x2*>(parts.ml + 2 * (split * all_rows + to)) = f32x2{kNegInf, 0.f};
+    }
+    return;
+  }
   const int32_t* const table = c.table + static_cast<size_t>(b) * c.table_width;
 
   f32x4 o[kDt];
@@ -290,7 +300,6 @@ __global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint1
     sl[wave][i] = l;
   }
   __syncthreads();
-  const size_t all_rows = static_cast<size_t>(c.tokens) * heads;
   for (int at = threadIdx.x; at < 16 * (D / 4); at += 256) {
     const int rr = at / (D / 4), d = 4 * (at % (D / 4));
     const int row = 16 * rt + rr;
@@ -323,9 +332,13 @@ __global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint1
 }
 
 // ---------------------------------------------------------------------------
-// Joins the splits of every row: weights 2^(m_z - m), in split order. Rows of
-// no sequence are left alone. One wavefront takes one row.
+// Joins the splits of every row, at most 64: weights 2^(m_z - m), the same
+// order every time. Rows of no sequence are left alone. One wavefront takes one
+// row; lane z forms the weight of split z, half the lanes then add the outputs
+// of even splits, half those of odd ones, eight loads at a time.
 // ---------------------------------------------------------------------------
+
+constexpr int kMaxSplits = 64;
 
 template <int D, bool kBf16>
 __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __restrict__ out, Parts parts, int heads,
@@ -335,25 +348,41 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
   if (row >= rows) return;
   const int token = static_cast<int>(row / heads);
   if (token < c.cu[0] || token >= c.cu[c.batch]) return;
-  const int lane = threadIdx.x & 63;
-  constexpr int kE = D / 64;
-  float m = kNegInf;
-  for (int z = lane; z < splits; z += 64) m = fmaxf(m, parts.ml[2 * (z * rows + row)]);
-  m = wave_max(m);
-  const float base = m == kNegInf ? 0.f : m;
-  float total = 0.f, v[kE] = {};
-  for (int z = 0; z < splits; ++z) {
-    const f32x2 ml = *reinterpret_cast<const f32x2*>(parts.ml + 2 * (z * rows + row));
-    if (!(ml[1] > 0.f)) continue;  // a split without keys for this row (its output is not read)
-    const float f = __builtin_amdgcn_exp2f(ml[0] - base);
-    total = fmaf(ml[1], f, total);
-    const float* const p = parts.o + (z * rows + row) * D + kE * lane;
+  const int lane = threadIdx.x & 63, i = lane & 31, h = lane >> 5;
+  constexpr int kE = D / 32;  // dimensions per lane
+  typedef float part __attribute__((ext_vector_type(kE)));
+  f32x2 ml = {kNegInf, 0.f};
+  if (lane < splits) ml = *reinterpret_cast<const f32x2*>(parts.ml + 2 * (lane * rows + row));
+  const float m = wave_max(ml[0]);
+  // a split without keys for this row (sum 0) weighs nothing
+  const float f = ml[1] > 0.f ? __builtin_amdgcn_exp2f(ml[0] - (m == kNegInf ? 0.f : m)) : 0.f;
+  float total = ml[1] * f;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) v[e] = fmaf(p[e], f, v[e]);
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d, kWave);
+  part v = {};
+  for (int z0 = 0; z0 < splits; z0 += 16) {  // (the same steps in both halves: weights come from any lane)
+    part p[8];
+    float w[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int z = z0 + 2 * u + h;
+      const float weight = __shfl(f, z & 63, kWave);
+      w[u] = z < splits ? weight : 0.f;
+      p[u] = part{};
+      if (w[u] > 0.f) p[u] = *reinterpret_cast<const part*>(parts.o + (z * rows + row) * D + kE * i);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int e = 0; e < kE; ++e) v[e] = fmaf(p[u][e], w[u], v[e]);
   }
   const float inv = total > 0.f ? 1.f / total : 0.f;
 #pragma unroll
-  for (int e = 0; e < kE; ++e) out[row * D + kE * lane + e] = half_bits<kBf16>(v[e] * inv);
+  for (int e = 0; e < kE; ++e) v[e] = (v[e] + __shfl_xor(v[e], 32, kWave)) * inv;
+  if (h != 0) return;
+  uint32_t* const to = reinterpret_cast<uint32_t*>(out + row * D + kE * i);
+#pragma unroll
+  for (int e = 0; e < kE; e += 2) to[e / 2] = half_bits<kBf16>(v[e]) | (static_cast<uint32_t>(half_bits<kBf16>(v[e + 1])) << 16);
 }
 
 // ---------------------------------------------------------------------------
@@ -457,7 +486,7 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
   unsigned at = blockIdx.y * gridDim.x + blockIdx.x;
   const int head = static_cast<int>(at % c.kv_heads);
   at /= c.kv_heads;
-  const int split = static_cast<int>(at % splits);
+  const int split = static_cast<int>(at % splits);  // (few: prompts that need splits have few row tiles)
   const RowTile tile = row_tile(c, group, static_cast<int>(at / splits));
   if (tile.b < 0) return;
   const int b = tile.b, rt = tile.rt;
@@ -757,7 +786,6 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 }
 
 constexpr int kDecodeRows = 64;  // rows of one kv head that the decode form takes (four tiles of 16)
-constexpr int kMaxSplits = 64;
 
 template <int D, bool kBf16>
 hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, uint16_t* out, int q_heads, float scale,
@@ -774,8 +802,8 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, ui
   hipError_t e;
   if (plan.decode) {
     const int row_tiles = static_cast<int>((rows + 15) / 16);
-    const dim3 grid(static_cast<uint32_t>(plan.splits), static_cast<uint32_t>(c.kv_heads * row_tiles),
-                    static_cast<uint32_t>(c.batch));
+    const dim3 grid(static_cast<uint32_t>(c.kv_heads * row_tiles), static_cast<uint32_t>(c.batch),
+                    static_cast<uint32_t>(plan.splits));
     e = launch_kernel(kv8_decode_kernel<D, kBf16>, grid, dim3(256), 0, stream, c, q, q_stride, out, parts, group,
                       row_tiles, plan.splits, scale_log2);
   } else {
@@ -792,10 +820,17 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, ui
 
 }  // namespace
 
-// The keys of a sequence are split over workgroups until the launch holds
-// about kTarget of them; a split keeps at least four tiles of 64 keys (eight
-// for prompts), of the longest sequence that the tables can hold. How long
-// the sequences are is known on the GPU only: there each is cut evenly.
+// The keys of a sequence are split over workgroups. For prompts until the
+// launch holds 256 workgroups, a split keeping at least eight tiles of 64 keys
+// of the longest sequence that the tables can hold. For decode (8 kv heads):
+// - up to eight tiles stay whole: the joining kernel costs more than it saves
+//   (one sequence of 300 keys: 6.8 us, in two splits 8.0; 16 of 500: 8.7, 9.5),
+// - until 512 workgroups, at least four tiles each, one per wavefront (one
+//   sequence of 777 keys: four splits 8.3 us, two 10.2, one 10.9; 64 of 1000:
+//   whole 20.9 us, in two splits 24.6, in four 29.4),
+// - until 2048 where 32 tiles are left to each, which evens out sequences of
+//   different lengths (64 of up to 8192 keys: four splits 137 us, one 146).
+// How long the sequences are is known on the GPU only: there each is cut evenly.
 Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
   Kv8Plan p;
   const int group = q_heads / c.kv_heads;
@@ -809,10 +844,15 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
     if (row_tiles > bound) row_tiles = bound;
   }
   const int64_t groups = row_tiles * c.kv_heads;
-  const int64_t target = p.decode ? 2048 : 256, least = p.decode ? 4 : 8;
-  int64_t splits = groups > 0 ? target / groups : 1;
-  const int64_t fit = (tiles + least - 1) / least;
-  if (splits > fit) splits = fit;
+  auto until = [&](int64_t workgroups, int64_t least) {
+    const int64_t fill = groups > 0 ? workgroups / groups : 1, fit = (tiles + least - 1) / least;
+    return fill < fit ? fill : fit;
+  };
+  int64_t splits = until(256, 8);
+  if (p.decode) {
+    const int64_t few = until(512, 4), many = until(2048, 32);
+    splits = tiles <= 8 ? 1 : few > many ? few : many;
+  }
   if (splits > kMaxSplits) splits = kMaxSplits;
   // the joining kernel takes four rows per workgroup of 256: under 2^32 work-items
   if (static_cast<int64_t>(c.tokens) * q_heads >= (int64_t{1} << 26)) splits = 1;
