@@ -40,9 +40,11 @@
 // PFLOP/s): the matrix unit is busy 45% of the time. Without the multiply-adds
 // the call takes 380 us, without the fills 343; the rest is the start of every
 // stage, when all wavefronts meet at the barrier and wait for their first
-// fragments. Reading the next stage's fragments before the barrier (possible
-// for the smaller tiles, which have the registers) changed nothing there: they
-// are bound by the fills, about 60 GB/s per CU.
+// fragments. The smaller tiles are bound by LDS: two 64 x 128 workgroups on a
+// CU read 96 KB of fragments and fill 48 KB per pair of stages, in some 1500
+// cycles. What was tried and changed nothing there: the next stage's fragments
+// read before the barrier, more stages in flight, scales brought with the fills
+// (they help 48 to 200 tokens by 4-8% and cost the larger calls as much).
 #include "device_common.h"
 #include "launch.h"
 
@@ -389,7 +391,7 @@ hipError_t launch_shape(const uint8_t* xq, const float* s_x, const uint8_t* wq, 
 
 typedef Shape<256, 256, 2, 4, 2> Big;
 typedef Shape<128, 128, 2, 4, 2> Mid;   // two workgroups per CU
-typedef Shape<64, 128, 2, 4, 3> Low;    // two
+typedef Shape<64, 128, 1, 4, 3> Low;    // two; a weight row is read by one wavefront (2 x 4 of them: 4% slower)
 typedef Shape<64, 64, 2, 2, 4> Small;   // two
 
 }  // namespace
@@ -401,8 +403,8 @@ typedef Shape<64, 64, 2, 2, 4> Small;   // two
 // 4096 tokens: per stage with one workgroup on a CU, with two of them, and the
 // fixed part. For example 48 tokens at K = 12288, N = 4096: 64 x 64 tiles in 8
 // ranges 19 us, 64 x 128 in 8 20 us, unsplit over 45; 1000 tokens at 4096 x
-// 4096: 64 x 128 26.6, 128 x 128 30, 64 x 64 36, 256 x 256 over 100; 4096 tokens
-// at 4096 x 24576: 256 x 256 415, 128 x 128 490, 64 x 128 620, 64 x 64 900.
+// 4096: 64 x 128 24.6, 128 x 128 30, 64 x 64 36, 256 x 256 over 100; 4096 tokens
+// at 4096 x 24576: 256 x 256 415, 128 x 128 490, 64 x 128 600, 64 x 64 900.
 Fp8Plan plan_fp8_block_mm(int64_t M, int64_t N, int64_t K) {
   Fp8Plan p = {Fp8Form::kGemv, 1, 0};
   if (fp8_use_gemv(M, K)) return p;
@@ -413,7 +415,7 @@ Fp8Plan plan_fp8_block_mm(int64_t M, int64_t N, int64_t K) {
   };
   constexpr Cost kCosts[] = {{Fp8Form::kBig, 256, 256, 2.1, 4.2},
                              {Fp8Form::kMid, 128, 128, 0.80, 1.07},
-                             {Fp8Form::kLow, 64, 128, 0.47, 0.70},
+                             {Fp8Form::kLow, 64, 128, 0.47, 0.67},
                              {Fp8Form::kSmall, 64, 64, 0.36, 0.47}};
   const int64_t blocks = (K + kBK - 1) / kBK;
   double best = 1e300;
