@@ -534,8 +534,9 @@ mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* 
  * fewer tokens cached than new) is 0; rows of no sequence are left as they
  * are. Keys whose page number is outside [0, num_pages) count for nothing, as
  * do bytes past a sequence's last token, whatever they hold. Scores, softmax
- * statistics and sums are binary32, weights (at most 1) are rounded once to
- * fp16 for the second product, the output once. Scales must lie in
+ * statistics and sums are binary32, weights (at most 1, or 2^8 where the
+ * reference of a row's exponentials lags behind its maximum) are rounded once
+ * to fp16 for the second product, the output once. Scales must lie in
  * [2^-100, 2^120] (as the append leaves them; V scales are held to that
  * range), codes of a sequence's tokens must not be NaN, and q must be finite.
  * Keys of long sequences are split over workgroups, their parts joined by a
@@ -550,8 +551,9 @@ mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* 
  * Requires: D in {64, 128}, page in {16, 32, 64, 128} (else
  * MQ_ERR_UNSUPPORTED); 0 <= T <= 2^26; 0 <= B <= 65535; 1 <= Hkv <= Hq <=
  * 1024, Hq % Hkv == 0; num_pages >= 1; 1 <= table_width * page <= 2^30;
- * max_q_len >= 1; 0 <= softmax_scale <= 1e6; for the append B * Hkv * (max_q_len / page + 2) below about
- * 2^23; q, k, v, caches, out 16-byte aligned, the rest 4-byte. _bf16: k, v, q
+ * max_q_len >= 1; 0 <= softmax_scale <= 1e6; for the append B * Hkv *
+ * (max_q_len / page + 2) below about 2^23, for the attention Hkv * (T * Hq /
+ * Hkv / 256 + B) below about 2^31; q, k, v, caches, out 16-byte aligned, the rest 4-byte. _bf16: k, v, q
  * and out are bf16.
  */
 mq_status mq_kv8_append(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, uint8_t* k_cache,
