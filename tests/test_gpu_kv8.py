@@ -346,6 +346,16 @@ def test_one_query_row_is_its_value():
     assert np.array_equal(got.reshape(2, 3, 128), np.repeat(want[:, None], 3, 1))  # exact: 4 bits times a power of two
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_short_sequences(D):
+    """From 128 workgroups on, sequences of up to 16 tiles of keys go unsplit
+    over eight wavefronts."""
+    rng = np.random.default_rng(D + 20)
+    totals = [int(n) for n in rng.integers(1, 1025, 66)]
+    totals[0], totals[1], totals[2] = 1024, 1, 961
+    _check_attention(rng, [1] * 66, totals, 2, 4, D, 32, "bf16", "many short")
+
+
 def test_cache_past_four_gigabytes():
     """Pages whose byte offsets pass 2^32: append and both attention forms, at
     the far end of a pool whose other pages are never written."""

@@ -110,8 +110,8 @@ struct Parts {
 
 // ---------------------------------------------------------------------------
 // Decode: the rows of one kv head (its query heads times the new tokens) stand
-// in tiles of 16. A workgroup of four wavefronts takes one such tile and a
-// range of keys, a wavefront every fourth tile of 64 keys. Bound by the cache
+// in tiles of 16. A workgroup of four or eight wavefronts takes one such tile
+// and a range of keys, a wavefront every fourth or eighth tile of 64 keys. Bound by the cache
 // read: K and V go from memory straight into registers (16-byte loads, whole
 // 64-byte pieces of a page row), K of the next tile is requested as soon as
 // this tile's scores are formed, V as soon as its product is, and several
@@ -121,13 +121,14 @@ struct Parts {
 // row i of Q for tokens 16 h .. 16 h + 15, in order.
 // ---------------------------------------------------------------------------
 
-template <int D, bool kBf16>
-__global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint16_t* __restrict__ q, int64_t q_stride,
-                                                         uint16_t* __restrict__ out, Parts parts, int group,
-                                                         int row_tiles, int splits, float scale_log2) {
+template <int D, int kWaves, bool kBf16>
+__global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, const uint16_t* __restrict__ q,
+                                                                 int64_t q_stride, uint16_t* __restrict__ out,
+                                                                 Parts parts, int group, int splits,
+                                                                 float scale_log2) {
   constexpr int kKs = D / 32, kDt = D / 16;  // k-steps of a score, 16-dimension tiles of the output
-  __shared__ float so[4][16][D + 4];
-  __shared__ float sm[4][16], sl[4][16];
+  __shared__ float so[kWaves][16][D + 4];
+  __shared__ float sm[kWaves][16], sl[kWaves][16];
 
   // splits come last: those that find no keys (wide tables, short sequences)
   // follow those that do, instead of taking the turns of some XCDs, and only
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint1
   u32x4 kc[4][kKs / 2], vc[kDt];
   int tile = span.first + wave;
   int kid = page_id(tile, i >> 2), vid = page_id(tile, h);            // this tile's pages
-  int kid1 = page_id(tile + 4, i >> 2), vid1 = page_id(tile + 4, h);  // and the next one's
+  int kid1 = page_id(tile + kWaves, i >> 2), vid1 = page_id(tile + kWaves, h);  // and the next one's
   float ksc = 0.f, vsc = 1.f;
   if (tile < span.end) {
     load_k(tile, kid, kc);
@@ -213,8 +214,8 @@ __global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint1
     vsc = c.v_scales[unit];
     load_v(tile, vid, vc);
   }
-  for (; tile < span.end; tile += 4) {
-    const int kid2 = page_id(tile + 8, i >> 2), vid2 = page_id(tile + 8, h);
+  for (; tile < span.end; tile += kWaves) {
+    const int kid2 = page_id(tile + 2 * kWaves, i >> 2), vid2 = page_id(tile + 2 * kWaves, h);
     f32x4 s[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -226,8 +227,8 @@ __global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint1
         s[j] = mfma_16x16x32<kBf16>(kf, qf[ks], s[j]);
       }
     }
-    const bool more = tile + 4 < span.end;
-    if (more) load_k(tile + 4, kid1, kc);
+    const bool more = tile + kWaves < span.end;
+    if (more) load_k(tile + kWaves, kid1, kc);
     const float vs = held_scale(vsc);
     const float f = ksc * scale_log2, lv = __builtin_amdgcn_logf(vs), iv = 1.f / vs;
     float nks = 0.f, nvs = 1.f;
@@ -281,7 +282,7 @@ __global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint1
       o[d] = mfma_16x16x32<false>(widen<false>(vc[d][0], vc[d][1]), p0, o[d]);
       o[d] = mfma_16x16x32<false>(widen<false>(vc[d][2], vc[d][3]), p1, o[d]);
     }
-    if (more) load_v(tile + 4, vid1, vc);
+    if (more) load_v(tile + kWaves, vid1, vc);
     vid = vid1;
     kid1 = kid2;
     vid1 = vid2;
@@ -291,7 +292,7 @@ __global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint1
   l += __shfl_xor(l, 16, kWave);
   l += __shfl_xor(l, 32, kWave);
 
-  // The four wavefronts' parts meet in LDS; lane (i, h) holds dimensions
+  // The wavefronts' parts meet in LDS; lane (i, h) holds dimensions
   // 16 d + 4 h .. + 3 of row i.
 #pragma unroll
   for (int d = 0; d < kDt; ++d) *reinterpret_cast<f32x4*>(&so[wave][i][16 * d + 4 * h]) = o[d];
@@ -300,16 +301,18 @@ __global__ __launch_bounds__(256) void kv8_decode_kernel(Kv8Cache c, const uint1
     sl[wave][i] = l;
   }
   __syncthreads();
-  for (int at = threadIdx.x; at < 16 * (D / 4); at += 256) {
+  for (int at = threadIdx.x; at < 16 * (D / 4); at += 64 * kWaves) {
     const int rr = at / (D / 4), d = 4 * (at % (D / 4));
     const int row = 16 * rt + rr;
     if (row >= rows) continue;
-    const float mx = fmaxf(fmaxf(sm[0][rr], sm[1][rr]), fmaxf(sm[2][rr], sm[3][rr]));
+    float mx = sm[0][rr];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, sm[w][rr]);
     const float base = mx == kNegInf ? 0.f : mx;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     float total = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kWaves; ++w) {
       const float f = __builtin_amdgcn_exp2f(sm[w][rr] - base);
       total = fmaf(sl[w][rr], f, total);
       const f32x4 part = *reinterpret_cast<const f32x4*>(&so[w][rr][d]);
@@ -804,8 +807,10 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, ui
     const int row_tiles = static_cast<int>((rows + 15) / 16);
     const dim3 grid(static_cast<uint32_t>(c.kv_heads * row_tiles), static_cast<uint32_t>(c.batch),
                     static_cast<uint32_t>(plan.splits));
-    e = launch_kernel(kv8_decode_kernel<D, kBf16>, grid, dim3(256), 0, stream, c, q, q_stride, out, parts, group,
-                      row_tiles, plan.splits, scale_log2);
+    e = plan.waves == 8 ? launch_kernel(kv8_decode_kernel<D, 8, kBf16>, grid, dim3(512), 0, stream, c, q, q_stride, out,
+                                        parts, group, plan.splits, scale_log2)
+                        : launch_kernel(kv8_decode_kernel<D, 4, kBf16>, grid, dim3(256), 0, stream, c, q, q_stride, out,
+                                        parts, group, plan.splits, scale_log2);
   } else {
     constexpr int64_t kWide = int64_t{1} << 22;  // a dimension of the grid stays under 2^32 work-items
     const dim3 grid(static_cast<uint32_t>(plan.prompt_blocks < kWide ? plan.prompt_blocks : kWide),
@@ -824,7 +829,10 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, ui
 // launch holds 256 workgroups, a split keeping at least eight tiles of 64 keys
 // of the longest sequence that the tables can hold. For decode (8 kv heads):
 // - up to eight tiles stay whole: the joining kernel costs more than it saves
-//   (one sequence of 300 keys: 6.8 us, in two splits 8.0; 16 of 500: 8.7, 9.5),
+//   (one sequence of 300 keys: 6.8 us, in two splits 8.0; 16 of 500: 8.7, 9.5);
+//   with eight wavefronts where CUs are free for them (6.5, 7.9), which also
+//   spares up to 16 tiles the splits from 128 workgroups on (16 sequences of 900:
+//   11.5 us, split 12.3; 32: 13.1, 16.6; but 8: 11.0, 9.2),
 // - until 512 workgroups, at least four tiles each, one per wavefront (one
 //   sequence of 777 keys: four splits 8.3 us, two 10.2, one 10.9; 64 of 1000:
 //   whole 20.9 us, in two splits 24.6, in four 29.4),
@@ -837,6 +845,7 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
   const int most = c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
   const int64_t rows = static_cast<int64_t>(most) * group;
   p.decode = rows <= kDecodeRows;
+  p.waves = p.decode ? 4 : 8;
   const int64_t tiles = (static_cast<int64_t>(c.table_width) * c.page + 63) / 64;
   int64_t row_tiles = c.batch * (p.decode ? (rows + 15) / 16 : (rows + kPromptRows - 1) / kPromptRows);
   if (!p.decode) {  // no more than if every sequence left the last of its tiles all but empty
@@ -852,6 +861,10 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
   if (p.decode) {
     const int64_t few = until(512, 4), many = until(2048, 32);
     splits = tiles <= 8 ? 1 : few > many ? few : many;
+    if (groups <= 256 && tiles > 4 && tiles <= (groups >= 128 ? 16 : 8)) {
+      p.waves = 8;
+      splits = 1;
+    }
   }
   if (splits > kMaxSplits) splits = kMaxSplits;
   // the joining kernel takes four rows per workgroup of 256: under 2^32 work-items

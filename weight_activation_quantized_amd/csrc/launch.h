@@ -107,6 +107,7 @@ hipError_t launch_kv8_append(const Kv8Cache& c, const uint16_t* k, const uint16_
 // a second kernel joins them.
 struct Kv8Plan {
   bool decode;  // the rows of one kv head fit a few tiles of 16: the streaming form
+  int waves;    // wavefronts of a workgroup
   int splits;
   int64_t prompt_blocks;  // workgroups of the other form
   size_t workspace_bytes;
