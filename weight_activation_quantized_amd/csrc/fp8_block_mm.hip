@@ -36,16 +36,17 @@
 //   of tiles in groups of kGroupM token tiles, so that what a run shares stays
 //   in its L2.
 //
-// What bounds it, at 4096 tokens x 4096 x 24576 (256 x 256 tiles, 415 us, 1.99
+// What bounds it, at 4096 tokens x 4096 x 24576 (256 x 256 tiles, 412 us, 2.0
 // PFLOP/s): the matrix unit is busy 45% of the time. Without the multiply-adds
-// the call takes 380 us, without the fills 343; the rest is the start of every
-// stage, when all wavefronts meet at the barrier and wait for their first
-// fragments. The smaller tiles are bound by their fills: two 64 x 128
-// workgroups on a CU bring 48 KB per pair of stages in some 0.65 us, 75 GB/s,
-// where the same loads by themselves reach about 94 GB/s per CU. What was tried
-// and changed nothing there: the next stage's fragments read before the barrier,
-// more stages in flight, scales brought with the fills (they help 48 to 200
-// tokens by 4-8% and cost the larger calls as much).
+// the call takes some 35 us less, without the fills 70; the rest is the start of
+// every stage, when all wavefronts meet at the barrier and wait for their first
+// fragments. Two halves of the workgroup half a stage apart, one reading while
+// the other multiplies, took 438 us: a single wavefront reads its fragments
+// more slowly than the other's MFMAs run. The smaller tiles are bound by their
+// fills: two 64 x 128 workgroups on a CU bring 48 KB per pair of stages in
+// some 0.65 us, 75 GB/s, where the same loads by themselves reach
+// about 94 GB/s per CU. The next stage's fragments read before the barrier
+// changed nothing there.
 #include "device_common.h"
 #include "launch.h"
 
@@ -54,6 +55,7 @@ namespace {
 
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) float lds_float;
 typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
 typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
@@ -78,17 +80,21 @@ struct Shape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kSlots = SLOTS_;
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int TB = BM / WM / 32, TA = BN / WN / 32;
-  static constexpr int kStage = (BM + BN) * kBK;
+  static constexpr int kTiles = (BM + BN) * kBK;               // bytes of the operands in a stage
+  static constexpr int kStage = kTiles + 4 * BM + 256;         // behind them scales: of the tokens, of the channel blocks
   static constexpr int kPitch = BN * 2 + 16;  // staged output rows
   static constexpr int kLds = kSlots * kStage > BM * kPitch ? kSlots * kStage : BM * kPitch;
   static constexpr int kLoadsX = BM / 8 / kWaves;              // fills per wavefront and stage (8 rows of 128 bytes each)
-  static constexpr int kLoads = kLoadsX + BN / 8 / kWaves;
+  static constexpr int kLoadsT = kLoadsX + BN / 8 / kWaves;
+  static constexpr int kLoads = kLoadsT + 1;                   // the last one: scales
   static constexpr int kAhead = (kSlots - 2) * kLoads;         // fills that may be in flight at a round's end
   static_assert(kLds <= 160 * 1024, "LDS capacity");
   static_assert(TA >= 1 && TB >= 1 && BM == 32 * TB * WM && BN == 32 * TA * WN, "wavefront tiles");
   static_assert(BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0, "a wavefront's fills do not straddle the operands");
   static_assert(128 % BN == 0 || BN % 128 == 0, "a tile of 32 channels lies in one scale block");
   static_assert(kAhead < 63, "vmcnt range");
+  static_assert(BM % 64 == 0 && kWaves > BM / 64, "a wavefront for every 64 tokens' scales and one for the channels'");
+  static_assert(128 % (32 * TA) == 0, "the channels of a wavefront lie in one block");
 };
 
 // kSplit: the stages of a tile are cut into `splits` contiguous ranges of
@@ -122,16 +128,27 @@ __global__ __launch_bounds__(S::kThreads) void fp8_block_mm_kernel(
   const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(xq + static_cast<size_t>(m0) * K, min(BM, M - m0) * K);
   const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(wq + static_cast<size_t>(n0) * K, min(BN, N - n0) * K);
 
-  // Scales: this lane's token of each 32-token tile (tokens past M take the
-  // last one's; their results are not stored), this wavefront's channel block.
   const int blocks = (K + kBK - 1) / kBK;
   const int first = kSplit ? split * share : 0, nst = kSplit ? min(share, blocks - first) : blocks;
-  int tok[S::TB];
-#pragma unroll
-  for (int b = 0; b < S::TB; ++b) tok[b] = min(m0 + wm * 32 * S::TB + 32 * b + fi, M - 1);
-  int nblk[S::TA];
-#pragma unroll
-  for (int a = 0; a < S::TA; ++a) nblk[a] = min(n0 + wn * 32 * S::TA + 32 * a, N - 1) / 128;
+
+  // A stage's scales come with its tiles, by the same kind of load: wavefronts
+  // below BM / 64 bring those of 64 tokens each, the others those of the
+  // channel blocks (lane r: block r of the tile), zeros past M and N. Loads
+  // into registers would be waited for by count, and so for every fill before
+  // them, however many stages ahead those are (48 tokens at K = 12288, N = 4096:
+  // 19.4 us, 17.2 with this; 300 at 4096 x 4096: 19.4, 16.0). (The addresses are uniform;
+  // said, so that the loads need no loop over lanes.)
+  const bool of_tokens = wave < BM / 64;
+  const uint64_t scales_from = reinterpret_cast<uint64_t>(of_tokens ? s_x + static_cast<size_t>(first) * M + m0 + 64 * wave
+                                                                    : s_w + static_cast<size_t>(n0 / 128) * blocks + first);
+  const uint8_t* const scales = reinterpret_cast<const uint8_t*>(
+      (static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(scales_from >> 32))) << 32) |
+      static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(scales_from))));
+  const uint32_t scale_step = __builtin_amdgcn_readfirstlane(of_tokens ? 4u * static_cast<uint32_t>(M) : 4u);
+  const int scale_bytes = __builtin_amdgcn_readfirstlane(
+      of_tokens ? 4 * min(max(M - m0 - 64 * wave, 0), 64) : 4 * (((min(BN, N - n0) + 127) / 128 - 1) * blocks + 1));
+  const uint32_t scale_off = 4u * static_cast<uint32_t>(lane) * static_cast<uint32_t>(of_tokens ? 1 : blocks);
+  const int scale_at = S::kTiles + (of_tokens ? 256 * wave : 4 * BM);
 
   // Fill l covers rows 8 (wave + kWaves l) .. + 7 of its operand's tile; lane L
   // writes physical chunk L % 8 of row L / 8, so it fetches the logical chunk
@@ -145,12 +162,15 @@ __global__ __launch_bounds__(S::kThreads) void fp8_block_mm_kernel(
     const uint32_t base = fk < K - k0 ? foff : kOob;
     lds_u8* const dst = sm + (s % S::kSlots) * S::kStage + wave * 1024;
 #pragma unroll
-    for (int l = 0; l < S::kLoads; ++l) {
+    for (int l = 0; l < S::kLoadsT; ++l) {
       const int u = l < kLoadsX ? l : l - kLoadsX;
       const uint32_t off = base + static_cast<uint32_t>(8 * kWaves * u * K + k0);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           l < kLoadsX ? rx : rw, (lds_void*)(dst + (l < kLoadsX ? 0 : BM * kBK) + kWaves * u * 1024), 16, off, 0, 0, 0);
     }
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(scales + static_cast<uint64_t>(s) * scale_step, scale_bytes);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(sm + (s % S::kSlots) * S::kStage + scale_at), 4, scale_off, 0, 0,
+                                             0);
   };
 
   // Fragment chunk c (0..3, two per k-step) of a row: logical chunk 2 c + fh.
@@ -166,12 +186,7 @@ __global__ __launch_bounds__(S::kThreads) void fp8_block_mm_kernel(
 #pragma unroll
     for (int b = 0; b < S::TB; ++b) acc[a][b] = f32x16{};
 
-  float sx[S::TB], sw[S::TA], sxn[S::TB], swn[S::TA];
-#pragma unroll
-  for (int b = 0; b < S::TB; ++b) sx[b] = s_x[static_cast<size_t>(first) * M + tok[b]];
-#pragma unroll
-  for (int a = 0; a < S::TA; ++a) sw[a] = s_w[static_cast<size_t>(nblk[a]) * blocks + first];
-
+  float sx[S::TB], sw = 0.f;
 #pragma unroll
   for (int s = 0; s < S::kSlots - 1; ++s)
     if (s < nst) fill(s);
@@ -194,27 +209,22 @@ __global__ __launch_bounds__(S::kThreads) void fp8_block_mm_kernel(
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w[1], x[1], v, 0, 0, 0, 0, 0, 0);
   };
   auto add = [&](int a, int b, const f32x16& v) {
-    const float sc = sx[b] * sw[a];
+    const float sc = sx[b] * sw;
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[a][b][i] = fmaf(v[i], sc, acc[a][b][i]);
   };
-  // What every round s begins with: the scales of stage s + 1 and the fill of
-  // the stage kSlots - 1 ahead, into the slot that every wavefront finished
-  // reading before the barrier that ended round s - 1.
+  // What every round s begins with: the fill of the stage kSlots - 1 ahead,
+  // into the slot that every wavefront finished reading before the barrier
+  // that ended round s - 1, and this stage's scales.
   auto begin = [&](int s) {
-    const int s1 = min(s + 1, nst - 1);
-#pragma unroll
-    for (int b = 0; b < S::TB; ++b) sxn[b] = s_x[static_cast<size_t>(first + s1) * M + tok[b]];
-#pragma unroll
-    for (int a = 0; a < S::TA; ++a) swn[a] = s_w[static_cast<size_t>(nblk[a]) * blocks + first + s1];
     if (s + S::kSlots - 1 < nst) fill(s + S::kSlots - 1);
+    const lds_u8* const src = sm + (s % S::kSlots) * S::kStage + S::kTiles;
+    sw = *(const lds_float*)(src + 4 * BM + 4 * (wn * 32 * S::TA / 128));
+#pragma unroll
+    for (int b = 0; b < S::TB; ++b) sx[b] = *(const lds_float*)(src + 4 * (wm * 32 * S::TB + 32 * b + fi));
   };
   // And ends with: this wavefront's share of the next stage needed is there.
   auto end = [&](int s) {
-#pragma unroll
-    for (int b = 0; b < S::TB; ++b) sx[b] = sxn[b];
-#pragma unroll
-    for (int a = 0; a < S::TA; ++a) sw[a] = swn[a];
     if (s + S::kSlots - 1 < nst) {
       wait_counts<S::kAhead, 0>();
     } else {
@@ -347,10 +357,15 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(const float* __restrict__
   const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (at + 4 <= outputs && (outputs & 3) == 0) {
     f32x4 v = *reinterpret_cast<const f32x4*>(part + at);
-    for (int z = 1; z < splits; ++z) {
-      const f32x4 p = *reinterpret_cast<const f32x4*>(part + z * outputs + at);
+    for (int z0 = 1; z0 < splits; z0 += 4) {  // four loads at a time
+      f32x4 p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += p[i];
+      for (int u = 0; u < 4; ++u)
+        p[u] = z0 + u < splits ? *reinterpret_cast<const f32x4*>(part + (z0 + u) * outputs + at) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = z0 + u < splits ? v[i] + p[u][i] : v[i];
     }
     uint32_t h[4];
 #pragma unroll
@@ -391,9 +406,9 @@ hipError_t launch_shape(const uint8_t* xq, const float* s_x, const uint8_t* wq, 
 }
 
 typedef Shape<256, 256, 2, 4, 2> Big;
-typedef Shape<128, 128, 2, 4, 2> Mid;   // two workgroups per CU
-typedef Shape<64, 128, 1, 4, 3> Low;    // two; a weight row is read by one wavefront (2 x 4 of them: 4% slower)
-typedef Shape<64, 64, 2, 2, 4> Small;   // two
+typedef Shape<128, 128, 2, 2, 2> Mid;   // two workgroups per CU, here and below
+typedef Shape<64, 128, 2, 2, 3> Low;
+typedef Shape<64, 64, 2, 2, 4> Small;
 
 }  // namespace
 
@@ -401,11 +416,14 @@ typedef Shape<64, 64, 2, 2, 4> Small;   // two
 // larger it is, a launch takes as many of them as its fullest CU holds, and
 // splitting K adds a second kernel and the sums' way through memory. The
 // figures (microseconds) are fitted to timed launches of every form over 17 to
-// 4096 tokens: per stage with one workgroup on a CU, with two of them, and the
-// fixed part. For example 48 tokens at K = 12288, N = 4096: 64 x 64 tiles in 8
-// ranges 19 us, 64 x 128 in 8 20 us, unsplit over 45; 1000 tokens at 4096 x
-// 4096: 64 x 128 24.6, 128 x 128 30, 64 x 64 36, 256 x 256 over 100; 4096 tokens
-// at 4096 x 24576: 256 x 256 415, 128 x 128 490, 64 x 128 600, 64 x 64 900.
+// 4096 tokens: per stage with one workgroup on a CU, with two of them, and what
+// a split adds. For example 48 tokens at K = 12288, N = 4096: 64 x 64 tiles in 4
+// ranges 16.8 us, in 8 18.1, 64 x 128 in 8 17.6; 300 tokens at 4096 x 4096: 64 x
+// 64 16.2, 64 x 128 20.4; 517 at 4096 x 6144: 64 x 128 26.8 (128 x 64, which is
+// not among the forms, 24.0 there and 1.2 us more behind the quantizer), 64 x 64
+// 30.6, 128 x 128 30.8; 2048 at 4096
+// x 4096: 128 x 128 36.3, 64 x 128 48, 256 x 256 58.6; 4096 at 4096 x 24576:
+// 256 x 256 412, 128 x 128 470, 64 x 128 580.
 Fp8Plan plan_fp8_block_mm(int64_t M, int64_t N, int64_t K) {
   Fp8Plan p = {Fp8Form::kGemv, 1, 0};
   if (fp8_use_gemv(M, K)) return p;
@@ -414,10 +432,10 @@ Fp8Plan plan_fp8_block_mm(int64_t M, int64_t N, int64_t K) {
     int bm, bn;
     double one, two;
   };
-  constexpr Cost kCosts[] = {{Fp8Form::kBig, 256, 256, 2.1, 4.2},
-                             {Fp8Form::kMid, 128, 128, 0.80, 1.07},
-                             {Fp8Form::kLow, 64, 128, 0.47, 0.67},
-                             {Fp8Form::kSmall, 64, 64, 0.36, 0.47}};
+  constexpr Cost kCosts[] = {{Fp8Form::kBig, 256, 256, 1.75, 3.5},
+                             {Fp8Form::kMid, 128, 128, 0.82, 0.90},
+                             {Fp8Form::kLow, 64, 128, 0.54, 0.64},
+                             {Fp8Form::kSmall, 64, 64, 0.33, 0.45}};
   const int64_t blocks = (K + kBK - 1) / kBK;
   double best = 1e300;
   for (const Cost& c : kCosts) {
@@ -427,7 +445,7 @@ Fp8Plan plan_fp8_block_mm(int64_t M, int64_t N, int64_t K) {
       if (splits > 1 && (share * (splits - 1) >= blocks || tiles * splits > 1024)) break;
       const int64_t on = (tiles * splits + 255) / 256;  // workgroups of the fullest CU
       double t = static_cast<double>(share) * (static_cast<double>(on / 2) * c.two + static_cast<double>(on % 2) * c.one);
-      if (splits > 1) t += 3.0 + static_cast<double>(splits) * static_cast<double>(M * N) * 2e-6;
+      if (splits > 1) t += 2.0 + static_cast<double>(splits) * (0.5 + static_cast<double>(M * N) * 1.6e-6);
       if (t < best) {
         best = t;
         p.form = c.form;
