@@ -552,9 +552,8 @@ mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* 
  * MQ_ERR_UNSUPPORTED); 0 <= T <= 2^26; 0 <= B <= 65535; 1 <= Hkv <= Hq <=
  * 1024, Hq % Hkv == 0; num_pages >= 1; 1 <= table_width * page <= 2^30;
  * max_q_len >= 1; 0 <= softmax_scale <= 1e6; for the append B * Hkv *
- * (max_q_len / page + 2) below about 2^23, for the attention Hkv * (T * Hq /
- * Hkv / 256 + B) below about 2^31; q, k, v, caches, out 16-byte aligned, the rest 4-byte. _bf16: k, v, q
- * and out are bf16.
+ * (max_q_len / page + 2) below about 2^23; q, k, v, caches, out 16-byte
+ * aligned, the rest 4-byte. _bf16: k, v, q and out are bf16.
  */
 mq_status mq_kv8_append(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, uint8_t* k_cache,
                         uint8_t* v_cache, float* k_scales, float* v_scales, const int32_t* block_table,

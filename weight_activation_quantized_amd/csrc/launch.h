@@ -109,7 +109,7 @@ struct Kv8Plan {
   bool decode;  // the rows of one kv head fit a few tiles of 16: the streaming form
   int waves;    // wavefronts of a workgroup
   int splits;
-  int64_t prompt_blocks;  // workgroups of the other form
+  int64_t prompt_blocks;  // workgroups of the other form (under 2^29 within the entry's limits)
   size_t workspace_bytes;
 };
 Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads);

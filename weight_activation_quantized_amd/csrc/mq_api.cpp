@@ -937,9 +937,6 @@ static mq_status kv8_attention_impl(const uint16_t* q, int64_t q_stride, const u
   const Range outs[] = {{out, static_cast<size_t>(T) * Hq * D * 2, "out"}, {ws ? workspace : nullptr, ws, "workspace"}};
   MQ_TRY(check_alias(in, outs));
   if (empty) return ok();
-  if (plan.prompt_blocks >= (int64_t{1} << 31))
-    return fail(MQ_ERR_SHAPE, "Hkv * tiles of 256 rows of every sequence = %lld must stay below 2^31",
-                (long long)plan.prompt_blocks);
   return hip_status(mq::launch_kv8_attention(c, q, q_stride, out, static_cast<int>(Hq), softmax_scale, plan,
                                              ws ? workspace : nullptr, bf16, as_stream(stream)),
                     "kv8_attention launch");
