@@ -241,6 +241,25 @@ def test_prompts(page, D, half):
     _check_attention(rng, [100, 1, 64, 65], [100, 50, 200, 65], 2, 4, D, page, half, "prompts")
 
 
+@pytest.mark.parametrize("half", ["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_prompts_in_wide_tables(page, D, half):
+    """Tables for 64 K tokens: what they could hold decides for the prompt form
+    and many splits, most of them without keys."""
+    rng = np.random.default_rng(page + D + 2)
+    _check_attention(rng, [100, 1, 64, 65], [100, 50, 200, 65], 2, 4, D, page, half, "wide", width=65536 // page)
+    _check_attention(rng, [90, 0, 30], [40, 0, 0], 2, 3, D, page, half, "wide, empty rows", pad=2, width=65536 // page)
+    _check_attention(rng, [300], [2111], 1, 5, D, page, half, "wide, longer", qamp=6.0, width=65536 // page)
+
+
+@pytest.mark.parametrize("news,totals,G", [([1030, 999], [1030, 1500], 8), ([513, 200, 777], [1100, 200, 2000], 4)])
+def test_prompts_large(news, totals, G):
+    """Large enough for the prompt form by what they hold."""
+    rng = np.random.default_rng(G)
+    _check_attention(rng, news, totals, 4, G, 128, 64, "bf16", "large")
+
+
 @pytest.mark.parametrize("G", [1, 3, 8])
 def test_prompt_long(G):
     rng = np.random.default_rng(G)
@@ -286,6 +305,31 @@ def test_unknown_pages_count_for_nothing():
         cache = _cache(rng, 11, 2, 16, 128)
         _fill(rng, cache, table, totals)
         _check_attention(rng, news, totals, 2, G, 128, 16, "bf16", "unknown pages", cache=cache, table=table)
+
+
+def test_unknown_pages_in_prompts():
+    rng = np.random.default_rng(21)
+    totals = [150, 75]
+    table = np.full((2, 4096), -1, np.int32)
+    table[:, :10] = [[3, -1, 5, 1, 99, 2, 7, 8, 9, 10], [4, 2 ** 31 - 1, 6, 0, -7, 0, 0, 0, 0, 0]]
+    cache = _cache(rng, 11, 2, 16, 128)
+    _fill(rng, cache, table[:, :10], totals)
+    _check_attention(rng, [90, 3], totals, 2, 2, 128, 16, "bf16", "unknown pages, prompt form", cache=cache, table=table)
+
+
+@pytest.mark.parametrize("news", [[250], [200, 70]])
+def test_wide_scales_in_prompts(news):
+    """As the next test, through the prompt form."""
+    rng = np.random.default_rng(22)
+    totals = [900, 333][:len(news)]
+    for what, qamp, klo, vlo in (("wide v", 1.0, -8, -30), ("peaked", 12.0, -6, -12), ("wide v and peaked", 8.0, -6, -30)):
+        P = 100
+        cache = _cache(rng, P, 2, 16, 128)
+        cache = (cache[0], cache[1], np.exp2(rng.integers(klo, -4, (P, 2))).astype(np.float32),
+                 np.exp2(rng.integers(vlo, 6, (P, 2))).astype(np.float32))
+        table = _table(rng, totals, 16, P, 4096)
+        _fill(rng, cache, table, totals)
+        _check_attention(rng, news, totals, 2, 4, 128, 16, "bf16", what, qamp=qamp, cache=cache, table=table)
 
 
 @pytest.mark.parametrize("news", [[1, 1], [80, 70]])

@@ -516,7 +516,7 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 
   const int last_t = min(kRows * rt + kRows - 1, rows - 1) / group;
   const int top = __builtin_amdgcn_readfirstlane(min(seq.len - seq.n + last_t, seq.seen - 1));  // the last key
-  const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, 8);
+  const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, 2);
   const int first = __builtin_amdgcn_readfirstlane(span.first);
   const int tiles = __builtin_amdgcn_readfirstlane(span.end - span.first);
 
@@ -788,7 +788,15 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
   }
 }
 
-constexpr int kDecodeRows = 64;  // rows of one kv head that the decode form takes (four tiles of 16)
+// The decode form takes calls of few rows per kv head, and small prompts: a
+// prompt workgroup walks its keys one tile after the other, some 2 us each, and
+// a small call has few of them. Measured against row tiles of 16 (summed over
+// sequences and kv heads) times tiles of 64 keys: 9000 (512 new tokens, 32 query
+// heads on 8) 18 us, as a prompt 38; 17500 17.4, 34; 33000 42, 47; 41000 (512
+// over 2000) 75, 45. Up to 64 rows it reads the keys hardly more often than the
+// prompt form, whatever their number.
+constexpr int kDecodeRows = 64;
+constexpr int64_t kDecodeTiles = 24576;
 
 template <int D, bool kBf16>
 hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, uint16_t* out, int q_heads, float scale,
@@ -826,7 +834,7 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, ui
 }  // namespace
 
 // The keys of a sequence are split over workgroups. For prompts until the
-// launch holds 256 workgroups, a split keeping at least eight tiles of 64 keys
+// launch holds 256 workgroups, a split keeping at least two tiles of 64 keys
 // of the longest sequence that the tables can hold. For decode (8 kv heads):
 // - up to eight tiles stay whole: the joining kernel costs more than it saves
 //   (one sequence of 300 keys: 6.8 us, in two splits 8.0; 16 of 500: 8.7, 9.5);
@@ -844,20 +852,22 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
   const int group = q_heads / c.kv_heads;
   const int most = c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
   const int64_t rows = static_cast<int64_t>(most) * group;
-  p.decode = rows <= kDecodeRows;
-  p.waves = p.decode ? 4 : 8;
   const int64_t tiles = (static_cast<int64_t>(c.table_width) * c.page + 63) / 64;
-  int64_t row_tiles = c.batch * (p.decode ? (rows + 15) / 16 : (rows + kPromptRows - 1) / kPromptRows);
-  if (!p.decode) {  // no more than if every sequence left the last of its tiles all but empty
-    const int64_t bound = (static_cast<int64_t>(c.tokens) * group + int64_t{kPromptRows - 1} * c.batch) / kPromptRows;
-    if (row_tiles > bound) row_tiles = bound;
-  }
-  const int64_t groups = row_tiles * c.kv_heads;
+  // row tiles of all sequences: no more than if every one left the last of its
+  // tiles all but empty
+  auto row_tiles = [&](int64_t size) {
+    const int64_t even = c.batch * ((rows + size - 1) / size);
+    const int64_t bound = (static_cast<int64_t>(c.tokens) * group + (size - 1) * c.batch) / size;
+    return even < bound ? even : bound;
+  };
+  p.decode = rows <= kDecodeRows || row_tiles(16) * c.kv_heads * tiles <= kDecodeTiles;
+  p.waves = p.decode ? 4 : 8;
+  const int64_t groups = row_tiles(p.decode ? 16 : kPromptRows) * c.kv_heads;
   auto until = [&](int64_t workgroups, int64_t least) {
     const int64_t fill = groups > 0 ? workgroups / groups : 1, fit = (tiles + least - 1) / least;
     return fill < fit ? fill : fit;
   };
-  int64_t splits = until(256, 8);
+  int64_t splits = until(256, 2);
   if (p.decode) {
     const int64_t few = until(512, 4), many = until(2048, 32);
     splits = tiles <= 8 ? 1 : few > many ? few : many;
