@@ -540,7 +540,9 @@ mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* 
  * [2^-100, 2^120] (as the append leaves them; V scales are held to that
  * range), codes of a sequence's tokens must not be NaN, and q must be finite.
  * Keys of long sequences are split over workgroups, their parts joined by a
- * second kernel in a fixed order: deterministic.
+ * second kernel in a fixed order: deterministic. The form is chosen by the
+ * longest sequence of a call: prompts and single tokens of many sequences are
+ * best passed in calls of their own.
  *
  *   k, v, q   [T, heads, D] fp16, rows `*_stride` values apart (a multiple of
  *             8, at least heads * D: slices of a fused projection's output)

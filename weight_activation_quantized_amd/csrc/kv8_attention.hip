@@ -790,7 +790,7 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 
 // The decode form takes calls of few rows per kv head, and small prompts: a
 // prompt workgroup walks its keys one tile after the other, some 2 us each, and
-// a small call has few of them. Measured against row tiles of 16 (summed over
+// a small call has few of them. Measured against row tiles of 16 (times
 // sequences and kv heads) times tiles of 64 keys: 9000 (512 new tokens, 32 query
 // heads on 8) 18 us, as a prompt 38; 17500 17.4, 34; 33000 42, 47; 41000 (512
 // over 2000) 75, 45. Up to 64 rows it reads the keys hardly more often than the
@@ -860,7 +860,8 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
     const int64_t bound = (static_cast<int64_t>(c.tokens) * group + (size - 1) * c.batch) / size;
     return even < bound ? even : bound;
   };
-  p.decode = rows <= kDecodeRows || row_tiles(16) * c.kv_heads * tiles <= kDecodeTiles;
+  // (what its grid covers counts, the longest sequence's row tiles for every one)
+  p.decode = rows <= kDecodeRows || c.batch * ((rows + 15) / 16) * c.kv_heads * tiles <= kDecodeTiles;
   p.waves = p.decode ? 4 : 8;
   const int64_t groups = row_tiles(p.decode ? 16 : kPromptRows) * c.kv_heads;
   auto until = [&](int64_t workgroups, int64_t least) {
