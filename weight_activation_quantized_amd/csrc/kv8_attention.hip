@@ -119,6 +119,9 @@ struct Parts {
 // v_mfma_16x16x32: lane (i = lane % 16, h = lane / 16). Row i of K tile j is
 // token 16 (i / 4) + 4 j + i % 4, so lane (i, h) ends up with the scores of
 // row i of Q for tokens 16 h .. 16 h + 15, in order.
+//
+// 64 sequences of up to 8193 keys, 32 query heads on 8 of 128: 134 us with the
+// joining kernel, 5.1 TB/s. One of 778 keys: 8.5 us, both launches' latency.
 // ---------------------------------------------------------------------------
 
 template <int D, int kWaves, bool kBf16>

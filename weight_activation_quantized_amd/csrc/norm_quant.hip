@@ -19,6 +19,9 @@
 // consecutive chunks, one row of 16 lanes, so their maximum takes four DPP
 // steps and no LDS. The scales go out transposed, [K / 128, M]: the product
 // that reads them wants the scales of neighbouring tokens side by side.
+//
+// 8192 rows of 4096 with a residual: 41 us, 5.7 TB/s. Small calls are a launch
+// and two passes of latency: one row of 4096 4.25 us, 333 of 5008 5.5 us.
 #include "device_common.h"
 #include "launch.h"
 #include "quant_codes.h"
