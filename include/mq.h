@@ -534,9 +534,9 @@ mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* 
  * fewer tokens cached than new) is 0; rows of no sequence are left as they
  * are. Keys whose page number is outside [0, num_pages) count for nothing, as
  * do bytes past a sequence's last token, whatever they hold. Scores, softmax
- * statistics and sums are binary32, weights (at most 1, or 2^8 where the
- * reference of a row's exponentials lags behind its maximum) are rounded once
- * to fp16 for the second product, the output once. Scales must lie in
+ * statistics and sums are binary32, weights are rounded once to fp16 for the
+ * second product (11 bits; weights times V scale below 2^-25 of a row's largest
+ * to fewer, below 2^-36 not at all), the output once. Scales must lie in
  * [2^-100, 2^120] (as the append leaves them; V scales are held to that
  * range), codes of a sequence's tokens must not be NaN, and q must be finite.
  * Keys of long sequences are split over workgroups, their parts joined by a

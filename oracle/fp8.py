@@ -206,3 +206,52 @@ def kv8_attention_bound(q, k_absmax, scale, D, length, o64, mag, sub, half):
     rel = 2.0 ** -11 + 4 * ds + 2.0 ** -14 + 2 * length * 2.0 ** -23
     err = rel * mag + 2.0 ** -25 * sub
     return u * (np.abs(o64) + err) + err + (2.0 ** -25 if half == "fp16" else 2.0 ** -133)
+
+
+def kv8_attention_rows(q, k_cache, v_cache, k_scales, v_scales, table, cu, lens, scale, half):
+    """(o64, bound): ``kv8_attention_ref``'s output and the largest |o - o64| of
+    the kernel's arithmetic, row by row from what the row sees.
+
+    With S = max_t scale sum_d |q_d k_td| and V = max_t |log2 v_scale| over the
+    keys of the row, and T their tiles of 64:
+    - a score sums D products in binary32, 2^-23 of their magnitude each; its
+      factor has four roundings of 2^-24, the multiply-add, the reference and the
+      difference to it three more of 2^-24 of at most 2 (log2(e) S + V) + 16, the
+      logarithm errs by 2^-22 of V. An exponent (base 2) is off by at most
+        d = 2^-23 ((D + 8) log2(e) S + 4 V + 16)
+      which moves a weight by ln 2 d of itself, the sum of the weights likewise;
+    - a weight is rounded to fp16 (2^-11 of itself; the largest weight of a row is
+      2^11 or more, so one too small for fp16's normal range is off by 2^-25, at
+      most 2^-36 of the largest: `sub`); the sum is of unrounded ones;
+    - exp2 errs by 2^-22, where the reference moves all sums by as much again;
+      the matrix unit adds eight groups of 8 products per tile, each addition off
+      by 2^-23 of the sum; parts of wavefronts and splits join with fewer than 100
+      more: 2^-23 (12 T + 128) in all;
+    - the output is rounded once (2^-11, bf16 2^-8 of itself)."""
+    T, Hq, D = q.shape
+    P, H, page, _ = k_cache.shape
+    o64, mag, sub = kv8_attention_ref(q, k_cache, v_cache, k_scales, v_scales, table, cu, lens, scale)
+    rel = np.zeros((T, Hq, 1))
+    for b in range(len(lens)):
+        n, L = int(cu[b + 1] - cu[b]), int(lens[b])
+        length = max(0, min(L, table.shape[1] * page))
+        if n <= 0 or length <= 0:
+            continue
+        pos = np.arange(length)
+        ids = table[b, pos // page]
+        good = (ids >= 0) & (ids < P)
+        ids = np.where(good, ids, 0)
+        seen = (pos[None, :] <= (L - n + np.arange(n))[:, None]) & good[None, :]
+        tiles = np.clip(L - n + np.arange(n), 0, length) // 64 + 1
+        for hq in range(Hq):
+            h = hq // (Hq // H)
+            k = np.abs(e4m3_decode(k_cache[ids, h, pos % page])) * k_scales[ids, h].astype(np.float64)[:, None]
+            s = np.abs(q[int(cu[b]):int(cu[b + 1]), hq].astype(np.float64)) @ np.where(good[:, None], k, 0.0).T * abs(scale)
+            S = np.max(np.where(seen, s, 0.0), axis=1)
+            with np.errstate(divide="ignore", invalid="ignore"):
+                V = np.max(np.where(seen, np.abs(np.log2(v_scales[ids, h].astype(np.float64)))[None, :], 0.0), axis=1)
+            d = 2.0 ** -23 * ((D + 8) * np.log2(np.e) * S + 4 * V + 16)
+            rel[int(cu[b]):int(cu[b + 1]), hq, 0] = 2.0 ** -11 + 2 * np.log(2) * d + 2.0 ** -23 * (12 * tiles + 128)
+    u = 2.0 ** -8 if half == "bf16" else 2.0 ** -11
+    err = 1.01 * (rel * mag + 2.0 ** -36 * sub)
+    return o64, u * (np.abs(o64) + err) + err + (2.0 ** -25 if half == "fp16" else 2.0 ** -133)

@@ -15,11 +15,15 @@
 //
 // Codes are widened exactly: K to the type of q, V to fp16. Scores and their
 // statistics are binary32. The page's V scale joins the exponent: with
-//   x_t = score_t log2(e) + log2(v_scale_t),   m = max x_t,   w_t = 2^(x_t - m) <= 1
-// the second product is sum w_t code_t in units of 2^m whatever the scales of
-// the pages are, and the sum of the weights is sum w_t / v_scale_t. w is
-// rounded once, to fp16 (11 bits; bf16 would lose three more and gains
-// nothing, as w <= 1).
+//   x_t = score_t log2(e) + log2(v_scale_t),   m = max x_t,   w_t = 2^(x_t - m + 15)
+// the second product is sum w_t code_t in units of 2^(m - 15) whatever the
+// scales of the pages are, and the sum of the weights is 2^-15 sum w_t / v_scale_t.
+// w is rounded once, to fp16 (11 bits; bf16 would lose three more). The 2^15
+// puts the largest weight at the top of fp16's range: with weights of at most 1
+// those 2^-25 below the largest were lost to the output, though the sum counted
+// them (one key of weight 0.999 and value 0 before 32767 others, which then are
+// the whole output: nothing of it was left). Now that is 2^-40, in prompts (whose
+// reference follows the maximum lazily) 2^-36.
 //
 // Keys that a row does not see get the weight 0 by a select, and V codes
 // behind the last token are cleared, so whatever a page holds there (NaN codes
@@ -37,6 +41,9 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kNegInf = -__builtin_inff();
 // Scales outside what the append writes would carry sums out of binary32.
 constexpr float kMinScale = 0x1p-100f, kMaxScale = 0x1p120f;
+// What the decode form's weights are raised by, as an exponent and as the
+// factor that takes it back.
+constexpr float kRaise = 15.f, kLower = 0x1p-15f;
 
 typedef float f32x8 __attribute__((ext_vector_type(8)));
 
@@ -265,8 +272,9 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, con
     mt = fmaxf(mt, __shfl_xor(mt, 16, kWave));
     mt = fmaxf(mt, __shfl_xor(mt, 32, kWave));
     const float mn = fmaxf(m, mt);
-    const float base = mn == kNegInf ? 0.f : mn;
-    const float shrink = __builtin_amdgcn_exp2f(m - base);  // 0 for the first keys
+    const float ref = mn == kNegInf ? 0.f : mn;
+    const float shrink = __builtin_amdgcn_exp2f(m - ref);  // 0 for the first keys
+    const float base = ref - kRaise;
     m = mn;
     f32x8 w[2];
     float sum = 0.f;
@@ -276,7 +284,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, con
       w[e / 8][e % 8] = p;
       sum += p;
     }
-    l = fmaf(sum, iv, l * shrink);
+    l = fmaf(sum * kLower, iv, l * shrink);
     const f16x8 p0 = to_f16(w[0]), p1 = to_f16(w[1]);
 #pragma unroll
     for (int d = 0; d < kDt; ++d) {
@@ -320,7 +328,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, con
       total = fmaf(sl[w][rr], f, total);
       const f32x4 part = *reinterpret_cast<const f32x4*>(&so[w][rr][d]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = fmaf(part[e], f, v[e]);
+      for (int e = 0; e < 4; ++e) v[e] = fmaf(part[e], f * kLower, v[e]);
     }
     const int t = row / group, gg = row - t * group;
     const size_t to = static_cast<size_t>(seq.row0 + t) * heads + head * group + gg;
@@ -411,8 +419,9 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
 //   are handed out by v_readlane (scalar loads in every softmax phase, that
 //   each phase had to wait for: 597 us where this took 536),
 // - the reference of the exponentials follows the maximum lazily: it moves (and
-//   the sums are rescaled) only when a score passes it by more than 2^8, so
-//   weights stay at most 2^8 and nearly every tile goes without rescaling.
+//   the sums are rescaled) only when a score passes it by more than 2^4, so
+//   nearly every tile goes without rescaling. Weights are raised by 2^11: at
+//   most 2^15, the largest of a row at least 2^11.
 //
 // The two wavefronts of a SIMD take turns: wavefronts 0-3 and 4-7 (one of each
 // per SIMD) walk the same tiles half a step apart, one half in its product
@@ -431,7 +440,7 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
-constexpr float kLazy = 8.f;
+constexpr float kLazy = 4.f, kLazyRaise = kRaise - kLazy, kLazyLower = 0x1p-11f;
 
 // The larger of x in lanes l and l ^ 32, in both: the swap leaves the lower
 // half's values in one register and the upper half's in the other. (Written
@@ -560,14 +569,14 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
     int id0, id1;             // pages of this batch and of the next
     uint64_t ok;              // parts whose page is known
     float ks1, vs1;           // scales of the next batch
-    float f0, off0, iv0;      // of this one: times scale_log2; V's, as log2 and reciprocal
+    float f0, off0, iv0;      // of this one: times scale_log2; V's, as log2 and lowered reciprocal
     auto enter_batch = [&]() {
       id0 = id1;
       ok = __ballot(known(id0));
       const float v = held_scale(vs1);
       f0 = fmaxf(ks1 * scale_log2, 0x1p-126f);  // (0 would turn a masked score's infinity into NaN)
       off0 = __builtin_amdgcn_logf(v);
-      iv0 = __builtin_amdgcn_rcpf(v);
+      iv0 = __builtin_amdgcn_rcpf(v) * kLazyLower;
     };
     auto lane_float = [](float v, int at) {
       return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), at));
@@ -718,7 +727,7 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[d][e] *= shrink;
       }
-      const float ref = base == kNegInf ? 0.f : base;
+      const float ref = (base == kNegInf ? 0.f : base) - kLazyRaise;
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         const float b0 = off[p] - ref;
@@ -767,6 +776,10 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 
   l += __shfl_xor(l, 32, kWave);
   if (!live) return;
+#pragma unroll
+  for (int d = 0; d < kDt; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[d][e] *= kLazyLower;
   const size_t to = static_cast<size_t>(seq.row0 + tq) * heads + head * group + g;
   if (splits == 1) {
     const float inv = l > 0.f ? 1.f / l : 0.f;
