@@ -1,0 +1,78 @@
+"""NaN and infinities in the paged e4m3 cache's inputs: what is not a number is
+never turned into one, whatever form and number of splits a call takes, and does
+not reach other sequences."""
+
+import numpy as np
+import pytest
+
+import weight_activation_quantized_amd as mq
+from oracle import fp8 as o8
+from tests.fp8_util import half_tensor
+from tests.kv8_util import attend, empty_cache
+
+pytestmark = pytest.mark.gpu
+
+# new tokens of each of two sequences, their keys, table width in pages of 64:
+# unsplit decode of four and eight wavefronts, split decode, prompts split and not
+FORMS = {"decode": (1, 200, 4, 2), "decode, eight wavefronts": (1, 500, 8, 2), "decode, split": (1, 5000, 100, 2),
+         "decode of five, split": (5, 2000, 64, 2), "prompt, split": (90, 3000, 2048, 2), "prompt": (64, 700, 512, 128)}
+
+
+def _two(rng, form, D, half):
+    """Two sequences (the second one plain) of a form and their dense inputs."""
+    new, keys, width, Hkv = FORMS[form]
+    n = -(-keys // 64)
+    cache = empty_cache(2 * n, Hkv, 64, D)
+    cache[0][:] = o8.e4m3_encode(np.clip(rng.standard_normal(cache[0].shape) * 60, -448, 448))
+    cache[1][:] = o8.e4m3_encode(np.clip(rng.standard_normal(cache[1].shape) * 60, -448, 448))
+    table = np.full((2, width), -1, np.int32)
+    table[:, :n] = rng.permutation(2 * n).reshape(2, n)
+    tq, _ = half_tensor(rng.standard_normal((2 * new, 4 * Hkv, D)), half)
+    needs = mq.kv8_attention_workspace_bytes(2 * new, 2, 4 * Hkv, Hkv, D, 64, width, new)
+    assert (needs > 0) == ("split" in form)
+    return new, keys, cache, table, tq
+
+
+@pytest.mark.parametrize("half,D", [("fp16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("form", FORMS)
+def test_nan_in_a_row_of_q(form, D, half):
+    rng = np.random.default_rng(1)
+    new, keys, cache, table, tq = _two(rng, form, D, half)
+    args = cache, table, [0, new, 2 * new], [keys, keys]
+    plain = attend(tq, *args, f"{form}: finite")
+    assert np.isfinite(plain).all()
+    tq[new - 1, 1, 3] = float("nan")
+    got = attend(tq, *args, f"{form}: NaN in q")
+    bad = np.isnan(got)
+    assert bad[new - 1, 1].all()
+    bad[new - 1, 1] = False
+    assert not bad.any() and np.array_equal(got[~np.isnan(got)], plain[~np.isnan(got)])
+
+
+@pytest.mark.parametrize("half,D", [("fp16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("at", [0, 100, -1])
+def test_nan_codes(form, at, D, half):
+    """One K code: every row that sees its token, all dimensions; one V code: that
+    dimension of them. The other head and the other sequence keep every bit."""
+    rng = np.random.default_rng(2)
+    new, keys, cache, table, tq = _two(rng, form, D, half)
+    cu, lens = [0, new, 2 * new], [keys, keys]
+    plain = attend(tq, cache, table, cu, lens, f"{form}: finite")
+    t = keys - 1 if at < 0 else at
+    first = max(t - (keys - new), 0)  # rows from here on see it
+    p = table[0, t // 64]
+    for what in ("K", "V"):
+        c = [a.copy() for a in cache]
+        if what == "K":
+            c[0][p, 1, t % 64, 5] = 0x7F
+        else:
+            c[1][p, 1, 5, t % 64] = 0xFF
+        got = attend(tq, c, table, cu, lens, f"{form}: NaN {what} code of token {t}")
+        bad = np.isnan(got)
+        assert bad[first:new, 4:8][..., slice(None) if what == "K" else 5].all()
+        assert np.array_equal(got[new:], plain[new:])
+        others = np.delete(np.arange(tq.shape[1]), np.arange(4, 8))
+        assert np.array_equal(got[:new, others], plain[:new, others])
+        if what == "V":
+            assert np.array_equal(np.delete(got, 5, 2), np.delete(plain, 5, 2))

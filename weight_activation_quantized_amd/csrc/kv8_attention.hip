@@ -333,7 +333,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, con
     const int t = row / group, gg = row - t * group;
     const size_t to = static_cast<size_t>(seq.row0 + t) * heads + head * group + gg;
     if (splits == 1) {
-      const float inv = total > 0.f ? 1.f / total : 0.f;
+      const float inv = total == 0.f ? 0.f : 1.f / total;  // (a NaN stays one)
       const uint32_t lo = half_bits<kBf16>(v[0] * inv) | (static_cast<uint32_t>(half_bits<kBf16>(v[1] * inv)) << 16);
       const uint32_t hi = half_bits<kBf16>(v[2] * inv) | (static_cast<uint32_t>(half_bits<kBf16>(v[3] * inv)) << 16);
       *reinterpret_cast<u32x2*>(out + to * D + d) = u32x2{lo, hi};
@@ -368,9 +368,10 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
   f32x2 ml = {kNegInf, 0.f};
   if (lane < splits) ml = *reinterpret_cast<const f32x2*>(parts.ml + 2 * (lane * rows + row));
   const float m = wave_max(ml[0]);
-  // a split without keys for this row (sum 0) weighs nothing
-  const float f = ml[1] > 0.f ? __builtin_amdgcn_exp2f(ml[0] - (m == kNegInf ? 0.f : m)) : 0.f;
-  float total = ml[1] * f;
+  // a split without keys for this row (sum 0) counts for nothing: -1. Every other
+  // one is read whatever its weight, so that a NaN reaches the output (0 NaN = NaN).
+  const float f = ml[1] == 0.f ? -1.f : __builtin_amdgcn_exp2f(ml[0] - (m == kNegInf ? 0.f : m));
+  float total = f < 0.f ? 0.f : ml[1] * f;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d, kWave);
   part v = {};
@@ -381,16 +382,16 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
     for (int u = 0; u < 8; ++u) {
       const int z = z0 + 2 * u + h;
       const float weight = __shfl(f, z & 63, kWave);
-      w[u] = z < splits ? weight : 0.f;
+      w[u] = z < splits ? weight : -1.f;
       p[u] = part{};
-      if (w[u] > 0.f) p[u] = *reinterpret_cast<const part*>(parts.o + (z * rows + row) * D + kE * i);
+      if (w[u] >= 0.f) p[u] = *reinterpret_cast<const part*>(parts.o + (z * rows + row) * D + kE * i);
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u)
 #pragma unroll
       for (int e = 0; e < kE; ++e) v[e] = fmaf(p[u][e], w[u], v[e]);
   }
-  const float inv = total > 0.f ? 1.f / total : 0.f;
+  const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
   for (int e = 0; e < kE; ++e) v[e] = (v[e] + __shfl_xor(v[e], 32, kWave)) * inv;
   if (h != 0) return;
@@ -782,7 +783,7 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
     for (int e = 0; e < 16; ++e) o[d][e] *= kLazyLower;
   const size_t to = static_cast<size_t>(seq.row0 + tq) * heads + head * group + g;
   if (splits == 1) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int d = 0; d < kDt; ++d)
 #pragma unroll
