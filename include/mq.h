@@ -539,9 +539,9 @@ mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* 
  * to fewer, below 2^-36 not at all), the output once. Scales must lie in
  * [2^-100, 2^120] (as the append leaves them; V scales are held to that
  * range), codes of a sequence's tokens must not be NaN, and q must be finite. A
- * NaN among them is not lost: in q or a K code it makes the outputs of the rows
- * that see it NaN, in a V code those of its dimension, whatever the plan; other
- * rows of the same sequence and call may turn NaN with them.
+ * NaN among them is not lost: in q, a K code or a scale it makes the outputs of
+ * the rows that see it NaN, in a V code those of its dimension, whatever the
+ * plan; other rows of the same sequence and call may turn NaN with them.
  * Keys of long sequences are split over workgroups, their parts joined by a
  * second kernel in a fixed order: deterministic. The form is chosen by the
  * longest sequence of a call: prompts and single tokens of many sequences are

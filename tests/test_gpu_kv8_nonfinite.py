@@ -76,3 +76,45 @@ def test_nan_codes(form, at, D, half):
         assert np.array_equal(got[:new, others], plain[:new, others])
         if what == "V":
             assert np.array_equal(np.delete(got, 5, 2), np.delete(plain, 5, 2))
+
+
+@pytest.mark.parametrize("half,D", [("fp16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("form", FORMS)
+def test_nan_scales(form, D, half):
+    """A page's scale of K or V: every row that sees one of its tokens."""
+    rng = np.random.default_rng(3)
+    new, keys, cache, table, tq = _two(rng, form, D, half)
+    cu, lens = [0, new, 2 * new], [keys, keys]
+    plain = attend(tq, cache, table, cu, lens, f"{form}: finite")
+    for which in (2, 3):
+        c = [a.copy() for a in cache]
+        c[which][table[0, 1], 1] = np.nan
+        got = attend(tq, c, table, cu, lens, f"{form}: NaN scale {which}")
+        assert np.isnan(got[:new, 4:8]).all()
+        assert np.array_equal(got[new:], plain[new:])
+        others = np.delete(np.arange(tq.shape[1]), np.arange(4, 8))
+        assert np.array_equal(got[:new, others], plain[:new, others])
+
+
+@pytest.mark.parametrize("half,D", [("fp16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("form", FORMS)
+def test_what_no_row_sees_may_be_nan(form, D, half):
+    """Page 0, which unknown page numbers and tiles past the end read in their
+    place, and everything behind the last tokens: NaN codes and scales there
+    change no bit."""
+    rng = np.random.default_rng(4)
+    new, keys, cache, table, tq = _two(rng, form, D, half)
+    P, H = cache[2].shape
+    table = np.where(table >= 0, table + 1, table)
+    table[1, 0] = P + 1  # of no pool: the second sequence misses its first page
+    c = [np.concatenate([a[:1], a]) for a in cache]
+    args = table, [0, new, 2 * new], [keys, keys - 7]
+    plain = attend(tq, c, *args, f"{form}: finite")
+    c[0][0], c[1][0], c[2][0], c[3][0] = 0x7F, 0x7F, np.nan, np.nan
+    for b, n in enumerate(args[2]):
+        if n % 64:
+            p = table[b, n // 64]
+            c[0][p, :, n % 64:] = 0xFF
+            c[1][p, :, :, n % 64:] = 0xFF
+    got = attend(tq, c, *args, f"{form}: NaN that no row sees")
+    assert np.isfinite(plain).all() and np.array_equal(got, plain)

@@ -80,6 +80,11 @@ __device__ __forceinline__ u32x4 first_bytes(u32x4 v, int n) {
 }
 
 __device__ __forceinline__ float held_scale(float s) { return fminf(fmaxf(s, kMinScale), kMaxScale); }
+// The logarithm of a held scale; a NaN, which held_scale hides, stays one here.
+__device__ __forceinline__ float log_scale(float s) {
+  const float l = __builtin_amdgcn_logf(held_scale(s));
+  return s == s ? l : s;
+}
 
 // A sequence as the kernels see it.
 struct Seq {
@@ -239,8 +244,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, con
     }
     const bool more = tile + kWaves < span.end;
     if (more) load_k(tile + kWaves, kid1, kc);
-    const float vs = held_scale(vsc);
-    const float f = ksc * scale_log2, lv = __builtin_amdgcn_logf(vs), iv = 1.f / vs;
+    const float f = ksc * scale_log2, lv = log_scale(vsc), iv = 1.f / held_scale(vsc);
     float nks = 0.f, nvs = 1.f;
     if (more) {
       const size_t unit = static_cast<size_t>(known(vid1) ? vid1 : 0) * c.kv_heads + head;
@@ -574,10 +578,12 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
     auto enter_batch = [&]() {
       id0 = id1;
       ok = __ballot(known(id0));
-      const float v = held_scale(vs1);
-      f0 = fmaxf(ks1 * scale_log2, 0x1p-126f);  // (0 would turn a masked score's infinity into NaN)
-      off0 = __builtin_amdgcn_logf(v);
-      iv0 = __builtin_amdgcn_rcpf(v) * kLazyLower;
+      // (page 0's, where there is no page: a factor of 0 or NaN would turn a masked
+      // score's infinity into NaN)
+      const float v = known(id0) ? vs1 : 1.f, f = known(id0) ? ks1 * scale_log2 : 1.f;
+      f0 = f < 0x1p-126f ? 0x1p-126f : f;
+      off0 = log_scale(v);
+      iv0 = __builtin_amdgcn_rcpf(held_scale(v)) * kLazyLower;
     };
     auto lane_float = [](float v, int at) {
       return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), at));
