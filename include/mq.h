@@ -517,12 +517,13 @@ mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* 
  * sequence. Sequences may share pages that no call writes to.
  *
  * mq_kv8_append writes the new tokens' k and v. For a page with a = largest
- * |value| among its new tokens (K and V apart, per head):
+ * finite |value| among its new tokens (K and V apart, per head):
  *     s_new = 2^e, the smallest with a <= 448 * 2^e, -100 <= e <= 120
  *     s     = s_new if the page holds no older token, else max(s_old, s_new)
  *     new codes    e4m3_rne(clamp(fl32(x / s), -448, 448))
  *     older codes  unchanged if s = s_old, else e4m3_rne(code * s_old / s)
- * Bit-exact to that. Bytes of the page that belong to no token yet, and
+ * A new NaN or infinity gets the code 0x7F (NaN), an older NaN code stays as it
+ * is. Bit-exact to that. Bytes of the page that belong to no token yet, and
  * everything else, stay as they are. Each page written must belong to one
  * sequence only. A page number outside [0, num_pages), or a token past
  * table_width * page, is skipped.

@@ -133,16 +133,20 @@ def kv8_append_ref(k, v, k_cache, v_cache, k_scales, v_scales, table, cu, lens):
                 for x, c, s, tr in ((k, kc, ks, False), (v, vc, vs, True)):
                     new = np.asarray(x[rows, h], np.float32)
                     tile = c[p, h].T if tr else c[p, h]  # [page, D] view
+                    odd = ~np.isfinite(new)  # counts for no scale, becomes the NaN code
+                    new = np.where(odd, np.float32(0), new)
                     scale = page_scale(np.max(np.abs(new)))
                     if lo > pos0:
                         old = s[p, h]
                         if scale > old:
-                            moved = e4m3_decode(tile[:lo - pos0]) * np.float64(np.float32(old / scale))
-                            tile[:lo - pos0] = e4m3_encode(np.clip(moved, -E4M3_MAX, E4M3_MAX))
+                            had = tile[:lo - pos0].copy()
+                            nan = (had & 0x7F) == 0x7F
+                            moved = e4m3_decode(np.where(nan, 0, had)) * np.float64(np.float32(old / scale))
+                            tile[:lo - pos0] = np.where(nan, had, e4m3_encode(np.clip(moved, -E4M3_MAX, E4M3_MAX)))
                         else:
                             scale = old
-                    tile[lo - pos0:hi - pos0] = e4m3_encode(np.clip(new.astype(np.float64) / np.float64(scale),
-                                                                    -E4M3_MAX, E4M3_MAX))
+                    codes = e4m3_encode(np.clip(new.astype(np.float64) / np.float64(scale), -E4M3_MAX, E4M3_MAX))
+                    tile[lo - pos0:hi - pos0] = np.where(odd, np.uint8(0x7F), codes)
                     s[p, h] = scale
     return kc, vc, ks, vs
 

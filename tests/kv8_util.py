@@ -4,7 +4,7 @@ import numpy as np
 
 import weight_activation_quantized_amd as mq
 from oracle import fp8 as o8
-from tests.fp8_util import codes_tensor, half_tensor
+from tests.fp8_util import codes_of, codes_tensor, half_tensor
 from tests.gpu_util import announce, host
 
 
@@ -27,6 +27,22 @@ def put(cache, table, b, t, k=None, v=None):
         cache[0][p, :, t % page] = k
     if v is not None:
         cache[1][p, :, :, t % page] = v
+
+
+def append(k, v, half, cache, table, news, totals, what):
+    """kv8_append on a copy of a host cache, every byte against the oracle: the
+    cache after it."""
+    cu, lens = np.concatenate([[0], np.cumsum(news)]).astype(np.int32), np.array(totals, np.int32)
+    (tk, kf), (tv, vf) = half_tensor(k, half), half_tensor(v, half)
+    announce(f"kv8_append {what} {half} {cache[0].shape} new={news[:5]} total={totals[:5]}")
+    dev = codes_tensor(cache[0]), codes_tensor(cache[1]), up(cache[2]), up(cache[3])
+    mq.kv8_append(tk, tv, *dev, up(table), up(cu), up(lens), max_q_len=max(news))
+    got = codes_of(dev[0]), codes_of(dev[1]), host(dev[2]), host(dev[3])
+    want = o8.kv8_append_ref(kf, vf, *cache, table, cu, lens)
+    for name, a, b in zip(("K codes", "V codes", "K scales", "V scales"), got, want):
+        bad = np.argwhere(a != b)
+        assert bad.size == 0, f"{what}: {len(bad)} {name} differ, first at {bad[:3].tolist()}"
+    return got
 
 
 def attend(tq, cache, table, cu, lens, what, scale=None, most=None):

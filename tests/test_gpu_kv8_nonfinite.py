@@ -8,7 +8,7 @@ import pytest
 import weight_activation_quantized_amd as mq
 from oracle import fp8 as o8
 from tests.fp8_util import half_tensor
-from tests.kv8_util import attend, empty_cache
+from tests.kv8_util import append, attend, empty_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +118,33 @@ def test_what_no_row_sees_may_be_nan(form, D, half):
             c[1][p, :, :, n % 64:] = 0xFF
     got = attend(tq, c, *args, f"{form}: NaN that no row sees")
     assert np.isfinite(plain).all() and np.array_equal(got, plain)
+
+
+@pytest.mark.parametrize("half", ["fp16", "bf16"])
+@pytest.mark.parametrize("news,olds", [([1, 1, 1], [0, 5, 15]), ([3, 2, 40], [0, 13, 3]), ([130, 64, 200], [0, 9, 130])])
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_of_what_is_not_finite(D, page, news, olds, half):
+    """NaN and both infinities among the new tokens, NaN codes among the older
+    ones whose page changes its scale: bit for bit, each spoils itself only."""
+    rng = np.random.default_rng(page + D + sum(news))
+    totals = [n + o for n, o in zip(news, olds)]
+    T, H = sum(news), 2
+    P = sum(-(-t // page) for t in totals)
+    table = np.full((3, 40), -1, np.int32)
+    at = 0
+    for b, t in enumerate(totals):
+        n = -(-t // page)
+        table[b, :n] = range(at, at + n)
+        at += n
+    cache = empty_cache(P, H, page, D, 2.0 ** -9)
+    for c in cache[:2]:
+        c[:] = o8.e4m3_encode(np.clip(rng.standard_normal(c.shape) * 90, -448, 448))
+        c.reshape(-1)[::37] = 0x7F
+        c.reshape(-1)[5::41] = 0xFF
+    k, v = (rng.standard_normal((T, H, D)) * 3 for _ in range(2))
+    for x in (k, v):
+        for bad in (np.nan, np.inf, -np.inf):
+            x[rng.integers(0, T, 3), rng.integers(0, H, 3), rng.integers(0, D, 3)] = bad
+        x[0, 0, :] = np.inf  # a token of nothing else
+    append(k, v, half, cache, table, news, totals, "not finite")

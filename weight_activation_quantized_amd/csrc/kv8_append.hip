@@ -9,6 +9,8 @@
 // rne_e4m3(code * s_old / s). Powers of two: a 4-bit significand loses nothing
 // to a scale up to twice too large, and moving older codes to a larger scale
 // only shifts their exponents (codes that fall below 2^-6 round, nothing else).
+// A NaN or infinity takes no part in a and becomes the code of NaN, which no
+// change of scale touches: it spoils its own token and no other of the page.
 //
 // A workgroup owns one (sequence, page, head, K or V): the new rows of the
 // page stay in registers between the maximum and the codes, so they are read
@@ -29,6 +31,8 @@
 namespace mq {
 namespace {
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
 // Smallest power of two s with a <= 448 s, its exponent held in [-100, 120].
 // 448 = 1.75 * 2^8: with a = 1.m * 2^e the exponent is e - 8 for a fraction up
 // to .75 and e - 7 above, which the carry out of the fraction adds.
@@ -41,11 +45,17 @@ __device__ __forceinline__ float page_scale(float a) {
 
 __device__ __forceinline__ float clamp448(float v) { return __builtin_amdgcn_fmed3f(v, -kE4m3Max, kE4m3Max); }
 
-// The four codes of a word times ratio, rounded to e4m3 again.
+constexpr uint32_t kNanCode = 0x7f;
+
+// The four codes of a word times ratio, rounded to e4m3 again; NaN stays as it is.
 __device__ __forceinline__ uint32_t moved(uint32_t w, float ratio) {
   const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false);
   const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
-  return e4m3x4(clamp448(a[0] * ratio), clamp448(a[1] * ratio), clamp448(b[0] * ratio), clamp448(b[1] * ratio));
+  const uint32_t to = e4m3x4(clamp448(a[0] * ratio), clamp448(a[1] * ratio), clamp448(b[0] * ratio), clamp448(b[1] * ratio));
+  // bytes of seven ones below the sign: adding 1 carries into the sign's place
+  const uint32_t nan = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+  const uint32_t keep = nan * 0xffu;
+  return (to & ~keep) | (w & keep);
 }
 
 // The bytes of four words as columns: byte e of word t becomes byte t of out[e].
@@ -120,15 +130,29 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, const 
       w[i] = *reinterpret_cast<const u32x4*>(x + row * stride + head * D + d);
   }
   if (!known) return;  // (the page's number was on its way with the rows)
-  float amax = 0.f;
+  // The largest magnitude, as 16-bit patterns, whose order is the values' (with
+  // infinity and NaN above all others).
+  constexpr uint32_t kInfinite = kBf16 ? 0x7f80 : 0x7c00;
+  u16x2 top = {0, 0};
 #pragma unroll
   for (int i = 0; i < CPT; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float a, z;
-      word_to_floats<kBf16>(w[i][e], a, z);
-      amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(z)));
-    }
+    for (int e = 0; e < 4; ++e)
+      top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, w[i][e] & 0x7fff7fffu));
+  uint32_t most = max(static_cast<uint32_t>(top[0]), static_cast<uint32_t>(top[1]));
+  const bool odd = most >= kInfinite;  // some value of this thread is not finite
+  if (odd) {
+    most = 0;
+#pragma unroll
+    for (int i = 0; i < CPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t m = (w[i][e / 2] >> (16 * (e % 2))) & 0x7fffu;
+        most = m < kInfinite ? max(most, m) : most;
+      }
+  }
+  float amax, unused;
+  word_to_floats<kBf16>(most, amax, unused);
   amax = wave_max(amax);
   if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = amax;
   __syncthreads();
@@ -193,6 +217,15 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, const 
       f[2 * e + 1] = quotient(z);
     }
     codes[i] = u32x2{e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7])};
+  }
+  if (odd) {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t m = (w[i][e / 2] >> (16 * (e % 2))) & 0x7fffu, at = 8 * (e % 4);
+        if (m >= kInfinite) codes[i][e / 4] = (codes[i][e / 4] & ~(0xffu << at)) | (kNanCode << at);
+      }
   }
   if (!is_v) {
 #pragma unroll
