@@ -436,7 +436,8 @@ mq_status mq_kv_quant_bf16(const uint16_t* x, uint8_t* codes, float* params, int
  *                block, the tokens side by side, as mq_fp8_block_mm reads it)
  * Requires: 0 <= M < 2^22; 16 <= K <= 65536, K % 16 == 0; 0 <= eps <= 1 (else
  * MQ_ERR_UNSUPPORTED); 16-byte aligned pointers (scales 4-byte). Inputs, and
- * the sums h, must be finite. _bf16: x, residual, weight and h are bf16.
+ * the sums h, must be finite: a row of h that is not gets NaN for its scales and
+ * 0 for its codes. _bf16: x, residual, weight and h are bf16.
  */
 mq_status mq_rmsnorm_int8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, double eps, uint16_t* h,
                           int8_t* xq, float* s_tok, int64_t M, int64_t K, void* stream);

@@ -110,6 +110,9 @@ __global__ __launch_bounds__(kTh == 64 ? 256 : kTh) void rmsnorm_quant_kernel(
     for (int w = 1; w < kWaves; ++w) sum += wsum[w];
   }
   const float r = static_cast<float>(1.0 / sqrt(sum / static_cast<double>(K) + eps));
+  // A NaN or infinity in the row (a residual sum past fp16's range, say): maxima
+  // skip NaN and the codes have none, so the scales say it.
+  const bool lost = !(sum < static_cast<double>(__builtin_inff()));
 
   float f[CPT][8];
 #pragma unroll
@@ -129,7 +132,7 @@ __global__ __launch_bounds__(kTh == 64 ? 256 : kTh) void rmsnorm_quant_kernel(
       float m = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[i][e]));
-      const float s = row16_max(m) / kE4m3Max;
+      const float s = lost ? __builtin_nanf("") : row16_max(m) / kE4m3Max;
       const int c = t + kTh * i;
       if (c >= nchunk) continue;
       *reinterpret_cast<u32x2*>(codes + base + 8 * c) = e4m3_codes(f[i], s, __builtin_amdgcn_rcpf(s));
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(kTh == 64 ? 256 : kTh) void rmsnorm_quant_kernel(
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) m = fmaxf(m, wmax[w]);
     }
-    const float s = m / 127.0f;
+    const float s = lost ? __builtin_nanf("") : m / 127.0f;
     const float rc = code_rcp(s);
     if (t == 0) scales[row] = s;
 #pragma unroll
