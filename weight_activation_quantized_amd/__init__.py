@@ -523,9 +523,13 @@ def _native():
     return _native_module
 
 
-def _on(stream):
+def _on(stream, t):
     """The given stream as the current one: outputs and workspace come from its
-    own pool and the kernels run on it."""
+    own pool and the kernels run on it. It has to be one of the GPU that holds
+    the tensors (t is one of them): the kernels run on that GPU's current stream."""
+    device = getattr(t, "device", None)  # (what is no tensor is refused by the call itself)
+    if device is not None and stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
     return _torch().cuda.stream(stream)
 
 
@@ -537,7 +541,7 @@ def rmsnorm_int8(x, weight, eps=1e-6, residual=None, out=None, s_out=None, h_out
     fn = (_native_module or _native()).rmsnorm
     if stream is None:
         return fn(x, weight, eps, residual, out, s_out, h_out, False)
-    with _on(stream):
+    with _on(stream, x):
         return fn(x, weight, eps, residual, out, s_out, h_out, False)
 
 
@@ -548,7 +552,7 @@ def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, out=None, s_out=None, h_out=
     fn = (_native_module or _native()).rmsnorm
     if stream is None:
         return fn(x, weight, eps, residual, out, s_out, h_out, True)
-    with _on(stream):
+    with _on(stream, x):
         return fn(x, weight, eps, residual, out, s_out, h_out, True)
 
 
@@ -558,7 +562,7 @@ def quant_fp8_blocks(x, out=None, s_out=None, stream=None):
     fn = (_native_module or _native()).quant_fp8_blocks
     if stream is None:
         return fn(x, out, s_out)
-    with _on(stream):
+    with _on(stream, x):
         return fn(x, out, s_out)
 
 
@@ -579,7 +583,7 @@ def fp8_block_mm(xq, s_x, wq, s_w, out=None, workspace=None, stream=None, out_dt
     fn, bf = (_native_module or _native()).fp8_block_mm, out_dtype == torch.bfloat16
     if stream is None:
         return fn(xq, s_x, wq, s_w, out, workspace, bf)
-    with _on(stream):
+    with _on(stream, xq):
         return fn(xq, s_x, wq, s_w, out, workspace, bf)
 
 
@@ -595,7 +599,7 @@ def fp8_linear(x, wq, s_w, out=None, workspace=None, stream=None):
     fn = (_native_module or _native()).fp8_linear
     if stream is None:
         return fn(x, wq, s_w, out, workspace)
-    with _on(stream):
+    with _on(stream, x):
         return fn(x, wq, s_w, out, workspace)
 
 
@@ -608,7 +612,7 @@ def kv8_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv
     fn = (_native_module or _native()).kv8_append
     if stream is None:
         return fn(k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len)
-    with _on(stream):
+    with _on(stream, k):
         return fn(k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len)
 
 
@@ -628,7 +632,7 @@ def kv8_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv
     if stream is None:
         return fn(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, softmax_scale, out,
                   workspace)
-    with _on(stream):
+    with _on(stream, q):
         return fn(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, softmax_scale, out,
                   workspace)
 
