@@ -8,7 +8,6 @@ without a GPU.
 """
 
 import argparse
-import importlib.util
 import os
 import subprocess
 import sys
@@ -68,16 +67,22 @@ def _run(cmd):
     return out
 
 
-def build_binding(out=BINDING_PATH, build_dir=BUILD_DIR):
+def build_binding(out=None):
     """The native half of the torch wrappers (host code only): a CPython
-    extension against the installed torch's headers."""
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    extension against the installed torch's headers and C++ ABI. Returns its
+    path, or None without a torch: the C library needs none."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    out = out or BINDING_PATH
+    torch_dir = os.path.dirname(torch.__file__)
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     rocm = os.path.dirname(os.path.dirname(HIPCC))
     tmp = out + ".tmp"
     _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
-          "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-D_GLIBCXX_USE_CXX11_ABI=1", f"-I{INCLUDE}",
-          "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+          "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+          f"-I{INCLUDE}", "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
           "-isystem", os.path.join(rocm, "include"), "-isystem", sysconfig.get_paths()["include"],
           os.path.join(CSRC, "torch_binding.cpp"), "-o", tmp, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
           "-lc10_hip"])
@@ -104,10 +109,10 @@ def build(out=LIB_PATH, defines=(), build_dir=BUILD_DIR, jobs=None, verbose=Fals
     os.replace(tmp, out)
     if verbose:
         print(f"built {out}")
-    if out == LIB_PATH:  # one binding serves every build of the library
-        binding.result()
+    if binding:  # one binding serves every build of the library
+        made = binding.result()
         if verbose:
-            print(f"built {BINDING_PATH}")
+            print(f"built {made}" if made else "torch is not importable: its wrappers' native half is not built")
     return out
 
 
