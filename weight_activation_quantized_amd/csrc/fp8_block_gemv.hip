@@ -27,8 +27,8 @@
 //   block, blocks past the wavefront's range).
 //
 // One token, 4096 x 24576, quantizer inside: 18.7 us back to back, 5.4 TB/s.
+#include "block8_launch.h"
 #include "device_common.h"
-#include "launch.h"
 #include "quant_codes.h"
 
 namespace mq {

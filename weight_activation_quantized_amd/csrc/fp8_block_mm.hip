@@ -47,8 +47,8 @@
 // some 0.65 us, 75 GB/s, where the same loads by themselves reach
 // about 94 GB/s per CU. The next stage's fragments read before the barrier
 // changed nothing there.
+#include "block8_launch.h"
 #include "device_common.h"
-#include "launch.h"
 
 namespace mq {
 namespace {

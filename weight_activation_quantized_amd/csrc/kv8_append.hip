@@ -24,8 +24,8 @@
 // for few tokens, 5.1 us for 64 sequences of one; for prompts by that and HBM:
 // 3 x 2048 tokens of 8 heads of 128 take 11.9 us, 2.9 TB/s (with single codes
 // into unpadded LDS, 16 lanes on one bank, and IEEE divisions 18.5 us).
+#include "block8_launch.h"
 #include "device_common.h"
-#include "launch.h"
 #include "quant_codes.h"
 
 namespace mq {

@@ -31,8 +31,8 @@
 // A row that sees no key is 0.
 #include <type_traits>
 
+#include "block8_launch.h"
 #include "device_common.h"
-#include "launch.h"
 
 namespace mq {
 namespace {

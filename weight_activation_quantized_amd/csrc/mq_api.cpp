@@ -7,6 +7,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "block8_launch.h"
 #include "launch.h"
 
 namespace {

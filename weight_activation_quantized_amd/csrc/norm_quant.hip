@@ -22,8 +22,8 @@
 //
 // 8192 rows of 4096 with a residual: 41 us, 5.7 TB/s. Small calls are a launch
 // and two passes of latency: one row of 4096 4.25 us, 333 of 5008 5.5 us.
+#include "block8_launch.h"
 #include "device_common.h"
-#include "launch.h"
 #include "quant_codes.h"
 
 namespace mq {
