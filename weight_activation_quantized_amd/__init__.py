@@ -53,6 +53,7 @@ and the compositions used by a model's linear layer:
 import ctypes
 import importlib.util
 import os
+import sys
 
 __all__ = [
     "MqError", "library", "LIB_PATH",
@@ -145,6 +146,18 @@ _PROTOTYPES = {
 }
 
 
+def _torch_runtime():
+    """Loads the HIP runtime that torch brings along, without importing torch.
+    libmq.so takes whichever runtime the process has; loaded before torch it would
+    bring the system's, and torch then a second one beside it, whose streams and
+    memory the first does not know."""
+    spec = None if "torch" in sys.modules else importlib.util.find_spec("torch")
+    if spec is not None and spec.origin:
+        path = os.path.join(os.path.dirname(spec.origin), "lib", "libamdhip64.so")
+        if os.path.exists(path):
+            ctypes.CDLL(path)
+
+
 def library():
     """The loaded ``libmq.so`` (ctypes) with prototypes set. Raises if it is not built."""
     global _lib
@@ -152,6 +165,7 @@ def library():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(
                 f"{LIB_PATH} is not built; run `python -m weight_activation_quantized_amd._build`")
+        _torch_runtime()
         lib = ctypes.CDLL(LIB_PATH)
         for name, (res, args) in _PROTOTYPES.items():
             fn = getattr(lib, name)
