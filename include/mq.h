@@ -494,6 +494,9 @@ mq_status mq_fp8_linear(const uint16_t* x, const uint8_t* wq, const float* s_w, 
 mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* s_w, uint16_t* y, int64_t M, int64_t N,
                              int64_t K, void* workspace, size_t workspace_bytes, void* stream);
 
+/* The form of attention that a call takes: few rows per kv head, or prompts. */
+enum { MQ_KV8_FORM_NONE = 0, MQ_KV8_FORM_DECODE = 1, MQ_KV8_FORM_PROMPT = 2 };
+
 /*
  * Paged KV cache in e4m3, one scale per page and head: append and attention.
  * Source: LMDeploy toolkit overview, section 2.4 "KV Cache online
@@ -547,7 +550,9 @@ mq_status mq_fp8_linear_bf16(const uint16_t* x, const uint8_t* wq, const float* 
  * Keys of long sequences are split over workgroups, their parts joined by a
  * second kernel in a fixed order: deterministic. The form is chosen by the
  * longest sequence of a call: prompts and single tokens of many sequences are
- * best passed in calls of their own.
+ * best passed in calls of their own. mq_kv8_attention_form says which form a
+ * call of these sizes takes, for callers that sort theirs (MQ_KV8_FORM_NONE:
+ * it is refused, or there is nothing to do).
  *
  *   k, v, q   [T, heads, D] fp16, rows `*_stride` values apart (a multiple of
  *             8, at least heads * D: slices of a fused projection's output)
@@ -572,6 +577,8 @@ mq_status mq_kv8_append_bf16(const uint16_t* k, const uint16_t* v, int64_t k_str
                              int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len, void* stream);
 size_t mq_kv8_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
                                         int64_t table_width, int64_t max_q_len);
+int32_t mq_kv8_attention_form(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
+                              int64_t table_width, int64_t max_q_len);
 mq_status mq_kv8_attention(const uint16_t* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
                            const float* k_scales, const float* v_scales, const int32_t* block_table, const int32_t* cu_q,
                            const int32_t* kv_lens, uint16_t* out, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,

@@ -31,6 +31,7 @@ Entry points (same names as the C ABI, without the ``mq_`` prefix):
     kv8_append(k, v, <cache>, <batch>, max_q_len)    writes new tokens into the paged e4m3 cache
     kv8_attention(q, <cache>, <batch>, max_q_len)    -> out [T, Hq, D]: causal attention over that cache
     kv8_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len) -> int
+    kv8_attention_form(T, B, Hq, Hkv, D, page, table_width, max_q_len) -> "decode", "prompt" or None
 
     (<cache>: k_cache [P, Hkv, page, D] and v_cache [P, Hkv, D, page], e4m3, with
     k_scales and v_scales [P, Hkv]; <batch>: block_table [B, width], cu_q [B + 1]
@@ -65,7 +66,7 @@ __all__ = [
     "AWQ_FIELD_ORDER", "int4_reorder", "int4_transpose", "u16_transpose",
     "w8a8_linear_noalloc", "NOALLOC_SCRATCH_BYTES",
     "rmsnorm_int8", "rmsnorm_fp8", "quant_fp8_blocks", "fp8_block_mm", "fp8_block_mm_workspace_bytes", "fp8_linear", "fp8_linear_workspace_bytes",
-    "kv8_append", "kv8_attention", "kv8_attention_workspace_bytes",
+    "kv8_append", "kv8_attention", "kv8_attention_workspace_bytes", "kv8_attention_form",
 ]
 
 # The in-tree build; MQ_LIBRARY names another build of the same library (for
@@ -140,6 +141,7 @@ _PROTOTYPES = {
     "mq_kv8_append": (ctypes.c_int, _KV8_APPEND),
     "mq_kv8_append_bf16": (ctypes.c_int, _KV8_APPEND),
     "mq_kv8_attention_workspace_bytes": (ctypes.c_size_t, [_I64] * 8),
+    "mq_kv8_attention_form": (ctypes.c_int32, [_I64] * 8),
     "mq_kv8_attention": (ctypes.c_int, _KV8_ATTENTION),
     "mq_kv8_attention_bf16": (ctypes.c_int, _KV8_ATTENTION),
     "mq_fp8_linear_bf16": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
@@ -633,6 +635,12 @@ def kv8_append(k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv
 def kv8_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len):
     """Workspace bytes ``kv8_attention`` needs (0 if none)."""
     return int(library().mq_kv8_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len))
+
+
+def kv8_attention_form(T, B, Hq, Hkv, D, page, table_width, max_q_len):
+    """The form that a ``kv8_attention`` call of these sizes takes: "decode" (few
+    rows per kv head) or "prompt"; None where it is refused or does nothing."""
+    return (None, "decode", "prompt")[library().mq_kv8_attention_form(T, B, Hq, Hkv, D, page, table_width, max_q_len)]
 
 
 def kv8_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, softmax_scale=None,

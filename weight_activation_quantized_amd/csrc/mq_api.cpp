@@ -893,8 +893,9 @@ static mq_status kv8_heads(int64_t Hq, int64_t Hkv) {
   return MQ_OK;
 }
 
-size_t mq_kv8_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
-                                        int64_t table_width, int64_t max_q_len) {
+// The plan of a call of these sizes; false where it is refused or does nothing.
+static bool kv8_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t table_width,
+                     int64_t max_q_len, mq::Kv8Plan& plan) {
   // any addresses do: only sizes are looked at
   static const float some[4] = {};
   const uint8_t* const p = reinterpret_cast<const uint8_t*>(16);
@@ -902,8 +903,23 @@ size_t mq_kv8_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_
   mq::Kv8Cache c;
   if (kv8_cache(p, p, some, some, t, t, t, T, B, Hkv, D, page, 1, table_width, max_q_len, c) != MQ_OK ||
       kv8_heads(Hq, Hkv) != MQ_OK || T == 0 || B == 0)
-    return 0;
-  return mq::plan_kv8_attention(c, static_cast<int>(Hq)).workspace_bytes;
+    return false;
+  plan = mq::plan_kv8_attention(c, static_cast<int>(Hq));
+  return true;
+}
+
+size_t mq_kv8_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
+                                        int64_t table_width, int64_t max_q_len) {
+  mq::Kv8Plan plan;
+  return kv8_plan(T, B, Hq, Hkv, D, page, table_width, max_q_len, plan) ? plan.workspace_bytes : 0;
+}
+
+int32_t mq_kv8_attention_form(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
+                              int64_t table_width, int64_t max_q_len) {
+  mq::Kv8Plan plan;
+  return !kv8_plan(T, B, Hq, Hkv, D, page, table_width, max_q_len, plan) ? MQ_KV8_FORM_NONE
+         : plan.decode                                                  ? MQ_KV8_FORM_DECODE
+                                                                        : MQ_KV8_FORM_PROMPT;
 }
 
 static mq_status kv8_attention_impl(const uint16_t* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
