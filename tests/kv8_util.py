@@ -29,6 +29,71 @@ def put(cache, table, b, t, k=None, v=None):
         cache[1][p, :, :, t % page] = v
 
 
+def random_codes(rng, shape):
+    return o8.e4m3_encode(np.clip(rng.standard_normal(shape) * 90, -448, 448))
+
+
+def paged(rng, totals, Hkv, page, D, width=None, spare=1):
+    """(cache, table) for sequences of `totals` tokens and `spare` more: random
+    pages, numbers of no pool where none is needed, codes of normal values, NaN
+    codes in pages of no sequence."""
+    need = [-(-(t + spare) // page) for t in totals]
+    P = sum(need) + 2
+    cache = empty_cache(P, Hkv, page, D)
+    cache[0][:], cache[1][:] = 0x7F, 0xFF
+    table = np.full((len(totals), width or max(need)), 2 ** 31 - 1, np.int32)
+    ids = rng.permutation(P)
+    for b, n in enumerate(need):
+        table[b, :n], ids = ids[:n], ids[n:]
+        at = table[b, :n]
+        cache[0][at], cache[1][at] = random_codes(rng, (n, Hkv, page, D)), random_codes(rng, (n, Hkv, D, page))
+    for s in cache[2:]:
+        s[:] = np.exp2(rng.integers(-9, -5, (P, Hkv)))
+    return cache, table
+
+
+def planted(rng, news, totals, Hkv, G, D, page, width=None):
+    """(q, cache, table): peaked softmax where the last key that a row sees has
+    its largest score, and the key behind it, which it does not see, a larger one
+    still: a row that loses the one or takes the other is far off."""
+    cache, table = paged(rng, totals, Hkv, page, D, width)
+    cache[2][:] = 2.0 ** -3
+    cache[0][(cache[0] & 0x7F) != 0x7F] = 0  # score 0 but for the planted ones
+    q = np.empty((sum(news), Hkv * G, D))
+    at = 0
+    for b, (n, L) in enumerate(zip(news, totals)):
+        if n == 0:
+            continue
+        way = rng.choice([-1.0, 1.0], (Hkv, D))
+        q[at:at + n] = np.repeat(way, G, axis=0) * rng.uniform(0.5, 1.5, (n, Hkv * G, 1))
+        at += n
+        for i in range(n + 1):  # the last one: behind the sequence
+            put(cache, table, b, L - n + i, k=o8.e4m3_encode(way * (3 + 0.25 * i) / 2.0 ** -3))
+    return q, cache, table
+
+
+def counted(rng, news, totals, Hkv, G, D, page, width=None, half="bf16"):
+    """(q, cache, table, want) for softmax_scale = 0: every key that a row sees
+    weighs the same, and token t of kv head h holds 1 in dimension (t + 7 h) % D
+    alone, so that the output counts keys."""
+    cache, table = paged(rng, totals, Hkv, page, D, width)
+    cache[3][:] = 1.0
+    dims = np.arange(D)
+    for b, total in enumerate(totals):
+        for t in range(total):
+            put(cache, table, b, t, v=np.stack([np.where(dims == (t + 7 * h) % D, 0x38, 0) for h in range(Hkv)]))
+    want = np.zeros((sum(news), Hkv * G, D))
+    at = 0
+    for n, L in zip(news, totals):
+        for i in range(n):
+            sees = max(L - n + i + 1, 0)
+            for h in range(Hkv):
+                if sees:
+                    want[at + i, h * G:(h + 1) * G] = np.bincount((np.arange(sees) + 7 * h) % D, minlength=D) / sees
+        at += n
+    return rng.standard_normal((sum(news), Hkv * G, D)), cache, table, want
+
+
 def append(k, v, half, cache, table, news, totals, what):
     """kv8_append on a copy of a host cache, every byte against the oracle: the
     cache after it."""
