@@ -541,12 +541,15 @@ enum { MQ_KV8_FORM_NONE = 0, MQ_KV8_FORM_DECODE = 1, MQ_KV8_FORM_PROMPT = 2 };
  * do bytes past a sequence's last token, whatever they hold. Scores, softmax
  * statistics and sums are binary32, weights are rounded once to fp16 for the
  * second product (11 bits; weights times V scale below 2^-25 of a row's largest
- * to fewer, below 2^-36 not at all), the output once. Scales must lie in
- * [2^-100, 2^120] (as the append leaves them; V scales are held to that
- * range), codes of a sequence's tokens must not be NaN, and q must be finite. A
- * NaN among them is not lost: in q, a K code or a scale it makes the outputs of
- * the rows that see it NaN, in a V code those of its dimension, whatever the
- * plan; other rows of the same sequence and call may turn NaN with them.
+ * to fewer, below 2^-36 not at all), the output once. The sum of the weights
+ * takes all down to 2^-137 of the largest weight times V scale, so V scales of a
+ * sequence's pages should lie within 2^110 of each other (zeros have 2^-100).
+ * Scales must lie in [2^-100, 2^120] (as the append leaves them; V scales are
+ * held to that range), scores must fit binary32, codes of a sequence's tokens
+ * must not be NaN, and q must be finite. A NaN among them is not lost: in q, a K
+ * code or a scale it makes the outputs of the rows that see it NaN, in a V code
+ * those of its dimension, whatever the plan; other rows of the same sequence and
+ * call may turn NaN with them.
  * Keys of long sequences are split over workgroups, their parts joined by a
  * second kernel in a fixed order: deterministic. The form is chosen by the
  * longest sequence of a call: prompts and single tokens of many sequences are

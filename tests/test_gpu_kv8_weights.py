@@ -70,3 +70,16 @@ def test_values_of_zero(news, width):
     cache[1][:] = 0x38  # 1.0: 2^-100 in bf16
     got = check_rows(q, "bf16", cache, table, [0, news], [20000], "tiny", scale=1.0)
     assert np.all(got == 2.0 ** -100)
+
+
+@pytest.mark.parametrize("half", ["fp16", "bf16"])
+@pytest.mark.parametrize("news,width", [(1, None), (50, 8192)])
+def test_zero_values_beside_large_ones(news, width, half):
+    """Every other page holds zeros alone (scale 2^-100, as the append leaves
+    them), the others values of scale 2^0; the scores are the same everywhere, so
+    half of the sum of the weights comes from weights 2^-100 of the largest."""
+    rng = np.random.default_rng(7)
+    q, cache, table = _sink(rng, 9000, news, 1, 4, 128, 64, 0, 0, width=width, vscale=(0, 0))
+    for p in table[0, :141:2]:
+        cache[1][p], cache[3][p] = 0, 2.0 ** -100
+    check_rows(q, half, cache, table, [0, news], [9000], "zeros beside", scale=1.0)
