@@ -36,17 +36,21 @@
 //   of tiles in groups of kGroupM token tiles, so that what a run shares stays
 //   in its L2.
 //
-// What bounds it, at 4096 tokens x 4096 x 24576 (256 x 256 tiles, 412 us, 2.0
-// PFLOP/s): the matrix unit is busy 45% of the time. Without the multiply-adds
-// the call takes some 35 us less, without the fills 70; the rest is the start of
-// every stage, when all wavefronts meet at the barrier and wait for their first
-// fragments. Two halves of the workgroup half a stage apart, one reading while
-// the other multiplies, took 438 us: a single wavefront reads its fragments
-// more slowly than the other's MFMAs run. The smaller tiles are bound by their
-// fills: two 64 x 128 workgroups on a CU bring 48 KB per pair of stages in
-// some 0.65 us, 75 GB/s, where the same loads by themselves reach
-// about 94 GB/s per CU. The next stage's fragments read before the barrier
+// What bounds it, at 4096 tokens x 4096 x 24576 (256 x 256 tiles, 407 us, 2.0
+// PFLOP/s): the matrix unit is busy 46% of the time. Copies that skip work take
+// 351 us without the multiply-adds, 275 without the fills, 285 with the fills and
+// the output alone: neither hides behind the other, since all wavefronts meet at
+// the barrier that starts a stage and wait there for their first fragments. Two
+// halves of the workgroup half a stage apart, one reading while the other
+// multiplies, were 7% slower: a single wavefront reads its fragments more slowly
+// than the other's MFMAs run. The smaller tiles are bound by their fills: 517
+// tokens at 4096 x 6144 (64 x 128 tiles) take 26.4 us, without the fills 16.0,
+// with the fills and the output alone 24.2; 48 at 12288 x 4096 with the joining
+// kernel 15.0, 6.9 and 13.3. The next stage's fragments read before the barrier
 // changed nothing there.
+//
+// Times in this file: captured calls one after the other, over three sets of
+// inputs in turn.
 #include "block8_launch.h"
 #include "device_common.h"
 
@@ -135,8 +139,8 @@ __global__ __launch_bounds__(S::kThreads) void fp8_block_mm_kernel(
   // below BM / 64 bring those of 64 tokens each, the others those of the
   // channel blocks (lane r: block r of the tile), zeros past M and N. Loads
   // into registers would be waited for by count, and so for every fill before
-  // them, however many stages ahead those are (48 tokens at K = 12288, N = 4096:
-  // 19.4 us, 17.2 with this; 300 at 4096 x 4096: 19.4, 16.0). (The addresses are uniform;
+  // them, however many stages ahead those are (48 tokens at K = 12288, N = 4096
+  // were 13% slower so, 300 at 4096 x 4096 21%). (The addresses are uniform;
   // said, so that the loads need no loop over lanes.)
   const bool of_tokens = wave < BM / 64;
   const uint64_t scales_from = reinterpret_cast<uint64_t>(of_tokens ? s_x + static_cast<size_t>(first) * M + m0 + 64 * wave
@@ -418,12 +422,12 @@ typedef Shape<64, 64, 2, 2, 4> Small;
 // figures (microseconds) are fitted to timed launches of every form over 17 to
 // 4096 tokens: per stage with one workgroup on a CU, with two of them, and what
 // a split adds. For example 48 tokens at K = 12288, N = 4096: 64 x 64 tiles in 4
-// ranges 16.8 us, in 8 18.1, 64 x 128 in 8 17.6; 300 tokens at 4096 x 4096: 64 x
-// 64 16.2, 64 x 128 20.4; 517 at 4096 x 6144: 64 x 128 26.8 (128 x 64, which is
-// not among the forms, 24.0 there and 1.2 us more behind the quantizer), 64 x 64
-// 30.6, 128 x 128 30.8; 2048 at 4096
-// x 4096: 128 x 128 36.3, 64 x 128 48, 256 x 256 58.6; 4096 at 4096 x 24576:
-// 256 x 256 412, 128 x 128 470, 64 x 128 580.
+// ranges 14.8 us, in 8 15.9, 64 x 128 in 8 15.4; 300 tokens at 4096 x 4096: 64 x
+// 64 15.8, in 2 ranges 21.1, 64 x 128 19.8; 517 at 4096 x 6144: 64 x 128 26.0
+// (128 x 64, which is not among the forms, 26.2, and behind the quantizer 29.7
+// like it), 64 x 64 33.0, 128 x 128 31.2; 2048 at 4096 x 4096: 128 x 128 40.7,
+// 64 x 128 53.2, 256 x 256 60.2; 4096 at 4096 x 24576: 256 x 256 407, 128 x 128
+// 473, 64 x 128 583.
 Fp8Plan plan_fp8_block_mm(int64_t M, int64_t N, int64_t K) {
   Fp8Plan p = {Fp8Form::kGemv, 1, 0};
   if (fp8_use_gemv(M, K)) return p;

@@ -21,9 +21,11 @@
 // registers and LDS.
 //
 // Bound by latency (lengths, page, rows, maximum, codes follow from each other)
-// for few tokens, 5.1 us for 64 sequences of one; for prompts by that and HBM:
-// 3 x 2048 tokens of 8 heads of 128 take 11.9 us, 2.9 TB/s (with single codes
-// into unpadded LDS, 16 lanes on one bank, and IEEE divisions 18.5 us).
+// for few tokens, 4.0 us for 64 sequences of one; for prompts by that and HBM:
+// 3 x 2048 tokens of 8 heads of 128 take 10.6 us, 3.2 TB/s (single codes into
+// unpadded LDS, 16 lanes on one bank, and IEEE divisions took 1.55 times as
+// long). Times in this file: captured calls one after the other, over three
+// sets of inputs in turn.
 #include "block8_launch.h"
 #include "device_common.h"
 #include "quant_codes.h"
@@ -289,7 +291,7 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* k, const uint16_t* v, i
   const dim3 grid(static_cast<uint32_t>(blocks));
   // A call of few tokens per sequence never fills a page: its rows need fewer
   // registers, and with little to move in a page one wavefront does (64
-  // sequences of one token, pages of 16: 5.1 us, with four wavefronts 5.6).
+  // sequences of one token, pages of 16: 4.0 us, with four wavefronts 4.5).
   // Three more tokens where threads take four at a time.
   const int rows = most < c.page ? most : c.page;
   const int chunks = rows * (D / 8), padded = (rows + 3 < c.page ? rows + 3 : c.page) * (D / 8);

@@ -132,8 +132,10 @@ struct Parts {
 // token 16 (i / 4) + 4 j + i % 4, so lane (i, h) ends up with the scores of
 // row i of Q for tokens 16 h .. 16 h + 15, in order.
 //
-// 64 sequences of up to 8193 keys, 32 query heads on 8 of 128: 134 us with the
-// joining kernel, 5.1 TB/s. One of 778 keys: 8.5 us, both launches' latency.
+// 64 sequences of up to 8193 keys, 32 query heads on 8 of 128: 135 us with the
+// joining kernel, 5.0 TB/s. One of 778 keys: 8.1 us, both launches' latency.
+// (Times in this file: captured calls one after the other, over three sets of
+// inputs in turn.)
 // ---------------------------------------------------------------------------
 
 template <int D, int kWaves, bool kBf16>
@@ -147,7 +149,8 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, con
 
   // splits come last: those that find no keys (wide tables, short sequences)
   // follow those that do, instead of taking the turns of some XCDs, and only
-  // say so (16 sequences of 500 keys, tables for 32768: 25.8 -> 11.0 us)
+  // say so (16 sequences of 500 keys, tables for 32768: 11.7 us, with splits
+  // first more than twice that)
   const int head = static_cast<int>(blockIdx.x) % c.kv_heads, rt = static_cast<int>(blockIdx.x) / c.kv_heads;
   const int b = static_cast<int>(blockIdx.y), split = static_cast<int>(blockIdx.z);
   const Seq seq = sequence(c, b);
@@ -422,7 +425,7 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
 //   per wavefront and tile,
 // - pages and scales come 16 tiles at a time, one part of 16 keys per lane, and
 //   are handed out by v_readlane (scalar loads in every softmax phase, that
-//   each phase had to wait for: 597 us where this took 536),
+//   each phase had to wait for, took 11% longer),
 // - the reference of the exponentials follows the maximum lazily: it moves (and
 //   the sums are rescaled) only when a score passes it by more than 2^4, so
 //   nearly every tile goes without rescaling. Weights are raised by 2^11: at
@@ -438,8 +441,10 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
 // phase, between the MFMAs, from registers loaded a step earlier.
 //
 // Two sequences of about 4096 and 3000 new tokens over 2048, 32 query heads on
-// 8, D = 128: 447 us, 0.87 PFLOP/s. The products alone take 269 us, the softmax
-// alone 262; with both the clock falls to 2.0 GHz (2.2 with half the CUs idle).
+// 8, D = 128: 443 us, 0.88 PFLOP/s; the matrix unit is busy 37% of the time, the
+// clock at 2.1 GHz. In copies that skip the rest of the work the products and the
+// fills take 369 us, the softmax and the fills 250: the turns hide some two thirds
+// of the softmax behind the products.
 // ---------------------------------------------------------------------------
 
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
@@ -462,8 +467,8 @@ constexpr int kPromptRows = 256;  // rows of a row tile
 // number within it. Every wavefront counts the sequences' tiles, 64 sequences
 // at a time, so that the workgroups that have work are the first of the grid:
 // a grid of equal parts for every sequence left half of the CUs without any
-// while the other half worked (two sequences of 4096 and some 3000 tokens:
-// 536 us, 447 with this). Workgroups go to the shader engines in strict turn,
+// while the other half worked (two sequences of 4096 and some 3000 tokens took
+// a fifth longer). Workgroups go to the shader engines in strict turn,
 // those that end at once took the turns of some.
 struct RowTile {
   int b, rt;
@@ -813,10 +818,11 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 
 // The decode form takes calls of few rows per kv head, and small prompts: a
 // prompt workgroup walks its keys one tile after the other, some 2 us each, and
-// a small call has few of them. Measured against row tiles of 16 (times
-// sequences and kv heads) times tiles of 64 keys: 9000 (512 new tokens, 32 query
-// heads on 8) 18 us, as a prompt 38; 17500 17.4, 34; 33000 42, 47; 41000 (512
-// over 2000) 75, 45. Up to 64 rows it reads the keys hardly more often than the
+// a small call has few of them. Measured (one sequence, 32 query heads on 8 of
+// 128) against row tiles of 16 times kv heads times tiles of 64 keys: 3800 (160
+// new tokens over 574) 13.9 us, as a prompt 21.6; 9200 (512 alone) 17.3, 29.9;
+// 12600 (300 over 1000) 29.1, 28.5; 31000 (700 over 700) 48.0, 47.9; 35000 (1024
+// alone) 41.4, 47.8; 41000 (512 over 2000) 74.6, 45.0. Up to 64 rows it reads the keys hardly more often than the
 // prompt form, whatever their number.
 constexpr int kDecodeRows = 64;
 constexpr int64_t kDecodeTiles = 24576;
@@ -858,18 +864,18 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, ui
 
 // The keys of a sequence are split over workgroups. For prompts until the
 // launch holds 256 workgroups (512 new tokens over 2000, 32 query heads on 8:
-// 44.6 us; until 128 60.7, until 512 58.7), a split keeping at least two tiles
+// 45.0 us; until 128 61.0, until 512 60.8), a split keeping at least two tiles
 // of 64 keys of the longest sequence that the tables can hold. For decode (8 kv heads):
 // - up to eight tiles stay whole: the joining kernel costs more than it saves
-//   (one sequence of 300 keys: 6.8 us, in two splits 8.0; 16 of 500: 8.7, 9.5);
-//   with eight wavefronts where CUs are free for them (6.5, 7.9), which also
+//   (one sequence of 300 keys: 6.7 us, in two splits 8.1; 16 of 500: 8.2, 9.6);
+//   with eight wavefronts where CUs are free for them (6.4, 7.7), which also
 //   spares up to 16 tiles the splits from 128 workgroups on (16 sequences of 900:
-//   11.5 us, split 12.3; 32: 13.1, 16.6; but 8: 11.0, 9.2),
+//   11.3 us, split 12.0; 32: 12.7, 16.3; but 8: 10.7, 9.2),
 // - until 512 workgroups, at least four tiles each, one per wavefront (one
-//   sequence of 777 keys: four splits 8.3 us, two 10.2, one 10.9; 64 of 1000:
-//   whole 20.9 us, in two splits 24.6, in four 29.4),
+//   sequence of 777 keys: four splits 8.1 us, two 10.1, one 10.9; 64 of 1000:
+//   whole 20.4 us, in two splits 24.9, in four 26.7),
 // - until 2048 where 32 tiles are left to each, which evens out sequences of
-//   different lengths (64 of up to 8192 keys: four splits 137 us, one 146).
+//   different lengths (64 of up to 8192 keys: four splits 135 us, one 141-146).
 // How long the sequences are is known on the GPU only: there each is cut evenly.
 Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
   Kv8Plan p;

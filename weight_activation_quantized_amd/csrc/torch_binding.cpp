@@ -1,6 +1,6 @@
 // Native half of the Python wrappers of the RMS norm, e4m3 and KV-cache entry
 // points: the checks of the tensors' metadata, the outputs' allocation and the
-// call into libmq, which in Python cost 12-20 us a call, several times what
+// call into libmq, which in Python cost 12-21 us a call, several times what
 // the smaller kernels take. Same checks, messages and exceptions as the
 // wrappers written in Python; the computation is libmq's alone.
 //
