@@ -72,6 +72,17 @@ def test_values_of_zero(news, width):
     assert np.all(got == 2.0 ** -100)
 
 
+@pytest.mark.parametrize("exponent", [114, 117, 120])
+@pytest.mark.parametrize("news,width", [(1, None), (50, 8192)])
+def test_largest_scales(news, width, exponent):
+    """V scales at the upper end of their range: sums of weights over them are
+    small, and neither they nor their reciprocals are lost."""
+    rng = np.random.default_rng(8)
+    q, cache, table = _sink(rng, 3000, news, 1, 4, 128, 64, 3, 0, width=width, vscale=(exponent, exponent))
+    cache[1][:] = o8.e4m3_encode(rng.uniform(0.5, 100, cache[1].shape))
+    check_rows(q, "bf16", cache, table, [0, news], [3000], "largest scales", scale=1.0)
+
+
 @pytest.mark.parametrize("half", ["fp16", "bf16"])
 @pytest.mark.parametrize("news,width", [(1, None), (50, 8192)])
 def test_zero_values_beside_large_ones(news, width, half):

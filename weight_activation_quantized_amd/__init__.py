@@ -156,8 +156,10 @@ def _torch_runtime():
     spec = None if "torch" in sys.modules else importlib.util.find_spec("torch")
     if spec is not None and spec.origin:
         path = os.path.join(os.path.dirname(spec.origin), "lib", "libamdhip64.so")
-        if os.path.exists(path):
+        try:
             ctypes.CDLL(path)
+        except OSError:
+            pass  # no ROCm torch: there is only the system's
 
 
 def library():
