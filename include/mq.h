@@ -595,6 +595,140 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
                                 void* stream);
 
 /*
+ * A serving step with drafted tokens over the paged e4m3 cache: append with the
+ * position rotation (and head norms), masks and positions of draft trees,
+ * attention under such masks, verification, and the cache's clean-up after it.
+ * Source: LMDeploy toolkit overview, section 2.4 (the cache is quantized as it
+ * is written and read by the attention); the pages describe neither the
+ * rotation's place nor drafts. Sizes, the cache, cu_q, kv_lens, block_table and
+ * strided rows are those of mq_kv8_append and mq_kv8_attention above.
+ *
+ * mq_kv8_rope_append: for every row r of a sequence, at position
+ * p = positions[r] (positions NULL: the token's place, kv_lens[b] - n + i), with
+ * c_i = cos_sin[p, i], s_i = cos_sin[p, rot/2 + i]; x one head of q or k, in
+ * binary32, each product and sum rounded by itself:
+ *     x = fl32(fl32(x * r) * weight), r = fl32(1 / sqrt(sum x^2 / D + eps)) in
+ *         binary64                              (both weights given; else x as it is)
+ *     x_a' = x_a c_i - x_b s_i,  x_b' = x_b c_i + x_a s_i      for i < rot/2,
+ *         (a, b) = (i, i + rot/2), interleaved: (2 i, 2 i + 1); others unchanged
+ * q_out gets q' rounded once to 16 bits; k' (not rounded before) and v go into the
+ * cache as mq_kv8_append writes them, bit-exact to that definition. A position
+ * outside [0, max_pos) makes the rotated values NaN. q is rotated for every row of
+ * a sequence, also where its k and v are skipped; rows of no sequence stay as they
+ * are.
+ *   q, k, v     rows as above; q_out [T, Hq, D] rows q_out_stride apart, apart from
+ *               all other operands or q itself with its stride (in place: q, k and v
+ *               may then be slices of one tensor)
+ *   cos_sin     [max_pos, rot] fp32: rot/2 cosines, then rot/2 sines
+ *   positions   [T] int32 or NULL
+ *   q_weight, k_weight  [D] of q's type, both or neither (NULL)
+ * Requires, beside the append's: rot a multiple of 16 in [16, D]; 1 <= max_pos <=
+ * 2^30; 0 <= eps <= 1; interleaved 0 or 1 (else MQ_ERR_UNSUPPORTED);
+ * B * (max_q_len / page + 2) * (Hq + 2 Hkv) below about 2^24; cos_sin and weights
+ * 16-byte aligned.
+ *
+ * mq_kv8_tree_mask: node j of a sequence's n new tokens hangs on node
+ * parents[cu_q[b] + j] (the sequence's own numbers, less than j; anything else, such
+ * as -1: on the context). It sees itself and the nodes above it:
+ *     tree[r, w] bit e = 1 where node 32 w + e is j itself or above it
+ *     positions[r] = kv_lens[b] - n + (nodes above j)
+ * Rows of no sequence stay as they are. tree [T, tree_width] int32, positions [T]
+ * int32, tree_width >= ceil(max_q_len / 32), 1 <= max_q_len <= 1024.
+ *
+ * mq_kv8_tree_attention: mq_kv8_attention, but row i of sequence b sees the
+ * kv_lens[b] - n tokens before the new ones and of the new ones those j whose bit
+ * in tree[r] is set (its own too only if it is). Any bits may be set; a row that
+ * sees nothing is 0. The new tokens' NaN codes (a branch that went astray) reach
+ * only rows that see them: a K code makes the row NaN, a V code its dimension; NaN
+ * before the new tokens, in q and in scales as in mq_kv8_attention. tree
+ * [T, tree_width] as above, max_q_len <= 1024.
+ *
+ * mq_draft_verify: a sequence's node 0 is its last certain token; probs[r] is the
+ * target's distribution of the token after row r (each sums to 1 but for rounding),
+ * tokens[r] node r's token, uniform[r] a number of [0, 1). From node 0 on, the
+ * children of the last node taken are tried in ascending order; child c, token x, is
+ * taken iff, with p and q of the row of the last node taken,
+ *     uniform[c] * (1 - sum of p over the tokens of siblings rejected before) < p(x)
+ *         (draft_probs NULL: the drafts are taken as given; a token rejected before has
+ *         p = 0)
+ *     uniform[c] * q(x) < p(x)
+ *         (draft_probs [T, V]: chains whose tokens were drawn from draft_probs)
+ * The token after the last one taken comes from the rest that the rejections leave of
+ * its row: r = p without the rejected tokens, or max(0, p - q); r = p where nothing
+ * was rejected or nothing is left. It is the smallest v with
+ *     sum_{w <= v} r(w) > uniform[node 0] * sum_w r(w).
+ * All in binary64, each test exact; the sums' order moves the token only within some
+ * 2^-40 of a border. Both rules draw from the target's distribution whatever the
+ * drafts. NaN and negative probabilities count as 0; a row without mass gives token
+ * -1; tokens outside [0, V) are not taken. One-hot rows make it greedy.
+ *     kept[b] = nodes taken, node 0 among them (0: the sequence has no rows)
+ *     path[b, i] = the i-th of them, -1 from kept[b] on;  next_token[b]
+ *   probs, draft_probs [T, V] fp32 dense, tokens, parents [T] int32 (parents as in
+ *   mq_kv8_tree_mask; NULL: chains, j hangs on j - 1), uniform [T] fp32, kept,
+ *   next_token [B], path [B, max_q_len] int32. 1 <= V <= 2^24, max_q_len <= 1024,
+ *   T <= 2^26, B <= 65535; workspace >= mq_draft_verify_workspace_bytes(B, V,
+ *   max_q_len) bytes, 16-byte aligned; draft_probs and parents exclude each other.
+ *
+ * mq_kv8_tree_keep: in each of `layers` caches (k_cache [layers, P, Hkv, page, D],
+ * v_cache [layers, P, Hkv, D, page], scales [layers, P, Hkv], one block_table), new
+ * token i of sequence b becomes what new token path[b, i] was, for i < kept[b] (path
+ * and kept as mq_draft_verify leaves them; an entry outside [i, n) ends the path).
+ * kv_lens still counts all n new tokens of the step; afterwards the sequence has
+ * kv_lens[b] - n + kept[b]. Of every page that gets tokens, with a = largest finite
+ * |code * s_source| among those that move (path[b, i] != i), per head, K and V apart:
+ *     s = max(s_old, smallest 2^e with a <= 448 * 2^e, -100 <= e <= 120)
+ *     moved codes    e4m3_rne(clamp(fl32(code * (s_source / s))))
+ *     others         unchanged if s = s_old, else e4m3_rne(code * (s_old / s))
+ * NaN codes stay. Where a token's own page or its new one is none of the pool's it
+ * does not move. kept[b] <= 1, or a path 0, 1, 2, ..., changes nothing. Each page
+ * written must belong to one sequence only. path_width <= 1024, layers <= 65535,
+ * B * Hkv < 2^23.
+ */
+mq_status mq_kv8_rope_append(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, uint16_t* q_out, int64_t q_out_stride, const float* cos_sin,
+                             const int32_t* positions, const uint16_t* q_weight, const uint16_t* k_weight, double eps,
+                             int64_t max_pos, int64_t rot, int32_t interleaved, uint8_t* k_cache, uint8_t* v_cache,
+                             float* k_scales, float* v_scales, const int32_t* block_table, const int32_t* cu_q,
+                             const int32_t* kv_lens, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                             int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len, void* stream);
+mq_status mq_kv8_rope_append_bf16(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, uint16_t* q_out, int64_t q_out_stride,
+                                  const float* cos_sin, const int32_t* positions, const uint16_t* q_weight,
+                                  const uint16_t* k_weight, double eps, int64_t max_pos, int64_t rot,
+                                  int32_t interleaved, uint8_t* k_cache, uint8_t* v_cache, float* k_scales,
+                                  float* v_scales, const int32_t* block_table, const int32_t* cu_q,
+                                  const int32_t* kv_lens, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                  int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len,
+                                  void* stream);
+mq_status mq_kv8_tree_mask(const int32_t* parents, const int32_t* cu_q, const int32_t* kv_lens, int32_t* tree,
+                           int32_t* positions, int64_t T, int64_t B, int64_t tree_width, int64_t max_q_len,
+                           void* stream);
+size_t mq_kv8_tree_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
+                                             int64_t table_width, int64_t max_q_len);
+mq_status mq_kv8_tree_attention(const uint16_t* q, int64_t q_stride, const int32_t* tree, int64_t tree_width,
+                                const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scales,
+                                const float* v_scales, const int32_t* block_table, const int32_t* cu_q,
+                                const int32_t* kv_lens, uint16_t* out, int64_t T, int64_t B, int64_t Hq, int64_t Hkv,
+                                int64_t D, int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len,
+                                float softmax_scale, void* workspace, size_t workspace_bytes, void* stream);
+mq_status mq_kv8_tree_attention_bf16(const uint16_t* q, int64_t q_stride, const int32_t* tree, int64_t tree_width,
+                                     const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scales,
+                                     const float* v_scales, const int32_t* block_table, const int32_t* cu_q,
+                                     const int32_t* kv_lens, uint16_t* out, int64_t T, int64_t B, int64_t Hq,
+                                     int64_t Hkv, int64_t D, int64_t page, int64_t num_pages, int64_t table_width,
+                                     int64_t max_q_len, float softmax_scale, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+size_t mq_draft_verify_workspace_bytes(int64_t B, int64_t V, int64_t max_q_len);
+mq_status mq_draft_verify(const float* probs, const float* draft_probs, const int32_t* tokens, const int32_t* parents,
+                          const float* uniform, const int32_t* cu_q, int32_t* kept, int32_t* path, int32_t* next_token,
+                          int64_t T, int64_t B, int64_t V, int64_t max_q_len, void* workspace, size_t workspace_bytes,
+                          void* stream);
+mq_status mq_kv8_tree_keep(uint8_t* k_cache, uint8_t* v_cache, float* k_scales, float* v_scales,
+                           const int32_t* block_table, const int32_t* cu_q, const int32_t* kv_lens, const int32_t* path,
+                           const int32_t* kept, int64_t layers, int64_t B, int64_t Hkv, int64_t D, int64_t page,
+                           int64_t num_pages, int64_t table_width, int64_t path_width, void* stream);
+
+/*
  * Checkpoint-layout adapter: one-time conversions of 4-bit checkpoint
  * tensors into the layouts above.
  * Source: the LMDeploy overview (sections 4.1 and 5.5) loads 4-bit

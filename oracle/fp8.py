@@ -151,7 +151,19 @@ def kv8_append_ref(k, v, k_cache, v_cache, k_scales, v_scales, table, cu, lens):
     return kc, vc, ks, vs
 
 
-def kv8_attention_ref(q, k_cache, v_cache, k_scales, v_scales, table, cu, lens, scale):
+def _seen(pos, row0, n, L, tree):
+    """[n, len(pos)] truth values: which positions the n rows from row0 on, the last
+    of L tokens, see: those up to their own, or with words `tree` [T, W] every one
+    before the new tokens and of these the ones with a bit in the row's words."""
+    if tree is None:
+        return pos[None, :] <= (L - n + np.arange(n))[:, None]
+    j = pos - (L - n)
+    w = np.clip(j // 32, 0, tree.shape[1] - 1)
+    bits = (tree[row0:row0 + n].astype(np.int64)[:, w] >> (j % 32)[None, :]) & 1
+    return (j < 0)[None, :] | ((bits == 1) & (j < 32 * tree.shape[1])[None, :])
+
+
+def kv8_attention_ref(q, k_cache, v_cache, k_scales, v_scales, table, cu, lens, scale, tree=None):
     """(o64 [T, Hq, D], mag, sub): attention of q (float32 [T, Hq, D]) in
     float64; mag = sum_t p_t |v_t| and sub = max_t(p_t s_v,t) sum_t |code_t|,
     the terms of the error bound. Rows that see nothing are 0; rows of no
@@ -178,7 +190,7 @@ def kv8_attention_ref(q, k_cache, v_cache, k_scales, v_scales, table, cu, lens, 
             for g in range(G):
                 qq = q[int(cu[b]):int(cu[b + 1]), h * G + g].astype(np.float64)
                 s = qq @ np.where(good[:, None], kk, 0.0).T * scale
-                seen = (pos[None, :] <= (int(lens[b]) - n + np.arange(n))[:, None]) & good[None, :]
+                seen = _seen(pos, int(cu[b]), n, int(lens[b]), tree) & good[None, :]
                 s = np.where(seen, s, -np.inf)
                 top = np.max(s, axis=1, keepdims=True)
                 p = np.exp(s - np.where(np.isfinite(top), top, 0.0))
@@ -212,7 +224,7 @@ def kv8_attention_bound(q, k_absmax, scale, D, length, o64, mag, sub, half):
     return u * (np.abs(o64) + err) + err + (2.0 ** -25 if half == "fp16" else 2.0 ** -133)
 
 
-def kv8_attention_rows(q, k_cache, v_cache, k_scales, v_scales, table, cu, lens, scale, half):
+def kv8_attention_rows(q, k_cache, v_cache, k_scales, v_scales, table, cu, lens, scale, half, tree=None):
     """(o64, bound): ``kv8_attention_ref``'s output and the largest |o - o64| of
     the kernel's arithmetic, row by row from what the row sees.
 
@@ -234,7 +246,7 @@ def kv8_attention_rows(q, k_cache, v_cache, k_scales, v_scales, table, cu, lens,
     - the output is rounded once (2^-11, bf16 2^-8 of itself)."""
     T, Hq, D = q.shape
     P, H, page, _ = k_cache.shape
-    o64, mag, sub = kv8_attention_ref(q, k_cache, v_cache, k_scales, v_scales, table, cu, lens, scale)
+    o64, mag, sub = kv8_attention_ref(q, k_cache, v_cache, k_scales, v_scales, table, cu, lens, scale, tree)
     rel = np.zeros((T, Hq, 1))
     for b in range(len(lens)):
         n, L = int(cu[b + 1] - cu[b]), int(lens[b])
@@ -245,8 +257,9 @@ def kv8_attention_rows(q, k_cache, v_cache, k_scales, v_scales, table, cu, lens,
         ids = table[b, pos // page]
         good = (ids >= 0) & (ids < P)
         ids = np.where(good, ids, 0)
-        seen = (pos[None, :] <= (L - n + np.arange(n))[:, None]) & good[None, :]
-        tiles = np.clip(L - n + np.arange(n), 0, length) // 64 + 1
+        seen = _seen(pos, int(cu[b]), n, L, tree) & good[None, :]
+        last = L - n + np.arange(n) if tree is None else np.full(n, length)
+        tiles = np.clip(last, 0, length) // 64 + 1
         for hq in range(Hq):
             h = hq // (Hq // H)
             k = np.abs(e4m3_decode(k_cache[ids, h, pos % page])) * k_scales[ids, h].astype(np.float64)[:, None]

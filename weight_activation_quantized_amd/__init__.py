@@ -33,6 +33,17 @@ Entry points (same names as the C ABI, without the ``mq_`` prefix):
     kv8_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len) -> int
     kv8_attention_form(T, B, Hq, Hkv, D, page, table_width, max_q_len) -> "decode", "prompt" or None
 
+    a serving step with drafted tokens, chains or trees of them, in this order:
+
+    kv8_tree_mask(parents, cu_q, kv_lens, max_q_len) -> (tree [T, words], positions [T]) of the drafts
+    kv8_rope_append(q, k, v, <cache>, <batch>, max_q_len, cos_sin, ...) -> q rotated (and normed per head);
+                                                     k likewise and v written into the cache
+    kv8_tree_attention(q, tree, <cache>, <batch>, max_q_len) -> out [T, Hq, D]: attention under the tree's mask
+    kv8_tree_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len) -> int
+    draft_verify(probs, tokens, uniform, cu_q, max_q_len) -> (kept, path, next_token) of every sequence
+    draft_verify_workspace_bytes(B, V, max_q_len)    -> int
+    kv8_tree_keep(<cache>, <batch>, path, kept)      moves the kept drafts together, in all layers' caches
+
     (<cache>: k_cache [P, Hkv, page, D] and v_cache [P, Hkv, D, page], e4m3, with
     k_scales and v_scales [P, Hkv]; <batch>: block_table [B, width], cu_q [B + 1]
     and kv_lens [B], int32 on the GPU.)
@@ -67,6 +78,8 @@ __all__ = [
     "w8a8_linear_noalloc", "NOALLOC_SCRATCH_BYTES",
     "rmsnorm_int8", "rmsnorm_fp8", "quant_fp8_blocks", "fp8_block_mm", "fp8_block_mm_workspace_bytes", "fp8_linear", "fp8_linear_workspace_bytes",
     "kv8_append", "kv8_attention", "kv8_attention_workspace_bytes", "kv8_attention_form",
+    "kv8_rope_append", "kv8_tree_mask", "kv8_tree_attention", "kv8_tree_attention_workspace_bytes",
+    "draft_verify", "draft_verify_workspace_bytes", "kv8_tree_keep",
 ]
 
 # The in-tree build; MQ_LIBRARY names another build of the same library (for
@@ -97,6 +110,9 @@ _I64 = ctypes.c_int64
 _RMSNORM = [_P, _P, _P, ctypes.c_double, _P, _P, _P, _I64, _I64, _P]
 _KV8_APPEND = [_P, _P, _I64, _I64] + [_P] * 7 + [_I64] * 8 + [_P]
 _KV8_ATTENTION = [_P, _I64] + [_P] * 8 + [_I64] * 9 + [ctypes.c_float, _P, ctypes.c_size_t, _P]
+_KV8_TREE_ATTENTION = [_P, _I64, _P, _I64] + [_P] * 8 + [_I64] * 9 + [ctypes.c_float, _P, ctypes.c_size_t, _P]
+_KV8_ROPE_APPEND = ([_P] * 3 + [_I64] * 3 + [_P, _I64] + [_P] * 4 + [ctypes.c_double, _I64, _I64, ctypes.c_int32] + [_P] * 7
+                    + [_I64] * 9 + [_P])
 _PROTOTYPES = {
     "mq_abi_version": (ctypes.c_int, []),
     "mq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -144,6 +160,15 @@ _PROTOTYPES = {
     "mq_kv8_attention_form": (ctypes.c_int32, [_I64] * 8),
     "mq_kv8_attention": (ctypes.c_int, _KV8_ATTENTION),
     "mq_kv8_attention_bf16": (ctypes.c_int, _KV8_ATTENTION),
+    "mq_kv8_rope_append": (ctypes.c_int, _KV8_ROPE_APPEND),
+    "mq_kv8_rope_append_bf16": (ctypes.c_int, _KV8_ROPE_APPEND),
+    "mq_kv8_tree_mask": (ctypes.c_int, [_P] * 5 + [_I64] * 4 + [_P]),
+    "mq_kv8_tree_attention_workspace_bytes": (ctypes.c_size_t, [_I64] * 8),
+    "mq_kv8_tree_attention": (ctypes.c_int, _KV8_TREE_ATTENTION),
+    "mq_kv8_tree_attention_bf16": (ctypes.c_int, _KV8_TREE_ATTENTION),
+    "mq_draft_verify_workspace_bytes": (ctypes.c_size_t, [_I64] * 3),
+    "mq_draft_verify": (ctypes.c_int, [_P] * 9 + [_I64] * 4 + [_P, ctypes.c_size_t, _P]),
+    "mq_kv8_tree_keep": (ctypes.c_int, [_P] * 9 + [_I64] * 8 + [_P]),
     "mq_fp8_linear_bf16": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P]),
 }
 
@@ -520,7 +545,10 @@ BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_mq_tor
 _BOUND = ("mq_rmsnorm_int8", "mq_rmsnorm_int8_bf16", "mq_rmsnorm_fp8", "mq_rmsnorm_fp8_bf16", "mq_quant_fp8_blocks",
           "mq_quant_fp8_blocks_bf16", "mq_fp8_block_mm_workspace_bytes", "mq_fp8_block_mm", "mq_fp8_block_mm_bf16",
           "mq_fp8_linear_workspace_bytes", "mq_fp8_linear", "mq_fp8_linear_bf16", "mq_kv8_append",
-          "mq_kv8_append_bf16", "mq_kv8_attention_workspace_bytes", "mq_kv8_attention", "mq_kv8_attention_bf16")
+          "mq_kv8_append_bf16", "mq_kv8_attention_workspace_bytes", "mq_kv8_attention", "mq_kv8_attention_bf16",
+          "mq_kv8_rope_append", "mq_kv8_rope_append_bf16", "mq_kv8_tree_mask", "mq_kv8_tree_attention_workspace_bytes",
+          "mq_kv8_tree_attention", "mq_kv8_tree_attention_bf16", "mq_draft_verify_workspace_bytes", "mq_draft_verify",
+          "mq_kv8_tree_keep")
 _native_module = None
 
 
@@ -659,6 +687,93 @@ def kv8_attention(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv
     with _on(stream, q):
         return fn(q, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, softmax_scale, out,
                   workspace)
+
+
+def kv8_rope_append(q, k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, cos_sin,
+                    positions=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, out=None, stream=None):
+    """``kv8_append`` of k and v [T, Hkv, D] with the position rotation, and with
+    an RMS norm per head where weights [D] are given, on k's way into the cache;
+    q [T, Hq, D] rotated the same -> out in q's dtype (``out=q`` rotates in
+    place; q, k and v may be slices of one tensor). ``cos_sin`` fp32 [positions,
+    rot]: rot / 2 cosines, then as many sines; pairs lie rot / 2 apart, or next to
+    each other where ``interleaved``. ``positions`` int32 [T] defaults to the
+    tokens' places in their sequences."""
+    fn = (_native_module or _native()).kv8_rope_append
+    interleaved = bool(interleaved)
+    if stream is None:
+        return fn(q, k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, cos_sin,
+                  positions, q_weight, k_weight, eps, interleaved, out)
+    with _on(stream, k_cache):
+        return fn(q, k, v, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, cos_sin,
+                  positions, q_weight, k_weight, eps, interleaved, out)
+
+
+def kv8_tree_mask(parents, cu_q, kv_lens, max_q_len, mask=None, positions=None, stream=None):
+    """Masks and positions of drafted trees: ``parents`` int32 [T], in each
+    sequence's own numbers, a node's parent before the node (-1: it hangs on the
+    context) -> (tree int32 [T, ceil(max_q_len / 32)], positions int32 [T]). Bit j
+    of a row's words: the row's node sees the sequence's new token j, itself or
+    above it. At most 1024 new tokens per sequence."""
+    fn = (_native_module or _native()).kv8_tree_mask
+    if stream is None:
+        return fn(parents, cu_q, kv_lens, max_q_len, mask, positions)
+    with _on(stream, parents):
+        return fn(parents, cu_q, kv_lens, max_q_len, mask, positions)
+
+
+def kv8_tree_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len):
+    """Workspace bytes ``kv8_tree_attention`` needs (0 if none)."""
+    return int(library().mq_kv8_tree_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len))
+
+
+def kv8_tree_attention(q, tree, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len,
+                       softmax_scale=None, out=None, workspace=None, stream=None):
+    """``kv8_attention`` of drafted tokens: a row sees all tokens before its
+    sequence's new ones, and of the new ones those named by its words of ``tree``
+    (int32 [T, words], as ``kv8_tree_mask`` makes them; any bits may be set). A
+    row that sees nothing is 0. At most 1024 new tokens per sequence."""
+    fn = (_native_module or _native()).kv8_tree_attention
+    if stream is None:
+        return fn(q, tree, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, softmax_scale,
+                  out, workspace)
+    with _on(stream, q):
+        return fn(q, tree, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len, softmax_scale,
+                  out, workspace)
+
+
+def draft_verify_workspace_bytes(B, V, max_q_len):
+    """Workspace bytes ``draft_verify`` needs."""
+    return int(library().mq_draft_verify_workspace_bytes(B, V, max_q_len))
+
+
+def draft_verify(probs, tokens, uniform, cu_q, max_q_len, parents=None, draft_probs=None, kept=None, path=None,
+                 next_token=None, workspace=None, stream=None):
+    """Verifies drafted tokens against the target's probabilities, drawing from
+    the target's distribution: row r of ``probs`` (fp32 [T, V]) is the
+    distribution of the token after ``tokens[r]``; a sequence's first row is its
+    last certain token, the others its drafts, a tree of ``parents`` or (None) a
+    chain, for chains with the probabilities ``draft_probs`` [T, V] that they were
+    drawn from. ``uniform`` fp32 [T]: numbers of [0, 1) -> (kept [B]: rows taken,
+    the first among them, path [B, max_q_len]: which, then -1, next_token [B]),
+    int32. See ``mq.h`` for the rules."""
+    fn = (_native_module or _native()).draft_verify
+    if stream is None:
+        return fn(probs, tokens, uniform, cu_q, max_q_len, parents, draft_probs, kept, path, next_token, workspace)
+    with _on(stream, probs):
+        return fn(probs, tokens, uniform, cu_q, max_q_len, parents, draft_probs, kept, path, next_token, workspace)
+
+
+def kv8_tree_keep(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, path, kept, stream=None):
+    """Moves the drafts that ``draft_verify`` kept to the front of their
+    sequence's new tokens, in place: new token i becomes what new token
+    ``path[b, i]`` was, for i < ``kept[b]``. ``kv_lens`` still counts all new
+    tokens; afterwards the sequence has kv_lens - n + kept. With one dimension
+    more in front, the caches and scales are those of several layers."""
+    fn = (_native_module or _native()).kv8_tree_keep
+    if stream is None:
+        return fn(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, path, kept)
+    with _on(stream, k_cache):
+        return fn(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, path, kept)
 
 
 # Field order of AWQ-style checkpoint words: field j holds element

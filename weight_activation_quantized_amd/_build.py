@@ -26,7 +26,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["mq_api.cpp", "quant_int8.hip", "w8a8_gemm.hip", "w8a8_gemv.hip", "w4a16_gemv.hip",
            "w4a16_gemv_blocked.hip", "w4a16_gemv_blocked_prescaled.hip", "w4a16_gemm.hip", "kv_quant.hip",
            "int4_layout.hip", "w8a8_noalloc.hip", "norm_quant.hip", "fp8_block_mm.hip", "fp8_block_gemv.hip",
-           "kv8_append.hip", "kv8_attention.hip"]
+           "kv8_append.hip", "kv8_attention.hip", "kv8_tree.hip", "draft_verify.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

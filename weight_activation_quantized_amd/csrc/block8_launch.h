@@ -65,6 +65,25 @@ int64_t kv8_append_blocks(const Kv8Cache& c);  // workgroups of the launch
 hipError_t launch_kv8_append(const Kv8Cache& c, const uint16_t* k, const uint16_t* v, int64_t k_stride,
                              int64_t v_stride, bool bf16, hipStream_t stream);
 
+// The same with q and k [tokens, heads, head_dim] normed per head where weights
+// are given and rotated: the cosines and sines of position p are row p of
+// cos_sin, pairs lie rot / 2 apart or next to each other.
+struct Kv8Turn {
+  const uint16_t* q;
+  uint16_t* q_out;  // q itself (of the same stride) or apart from everything
+  int64_t q_stride, q_out_stride;
+  const float* cos_sin;        // [max_pos, rot]: rot / 2 cosines, rot / 2 sines
+  const int32_t* positions;    // [tokens]; NULL: a token's place in its sequence
+  const uint16_t* q_weight;    // [head_dim] both, or NULL both: no norm
+  const uint16_t* k_weight;
+  double eps;
+  int q_heads, max_pos, rot;  // rot: a multiple of 16, at most head_dim
+  bool next;
+};
+int64_t kv8_rope_append_blocks(const Kv8Cache& c, int q_heads);
+hipError_t launch_kv8_rope_append(const Kv8Cache& c, const uint16_t* k, const uint16_t* v, int64_t k_stride,
+                                  int64_t v_stride, const Kv8Turn& turning, bool bf16, hipStream_t stream);
+
 // out [tokens, q_heads, head_dim] = causal attention of q over the cache. With
 // plan.splits > 1 every split of the keys leaves its part in the workspace and
 // a second kernel joins them.
@@ -79,5 +98,46 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads);
 hipError_t launch_kv8_attention(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, uint16_t* out, int q_heads,
                                 float softmax_scale, const Kv8Plan& plan, void* workspace, bool bf16,
                                 hipStream_t stream);
+
+// Attention of drafted tokens: a row sees every token before the new ones, and of
+// those the ones that its words name (bit j of [tokens, words]: new token j).
+struct Kv8Tree {
+  const int32_t* mask;
+  int words;
+};
+constexpr int kKv8MaxTree = 1024;  // new tokens of a sequence
+Kv8Plan plan_kv8_tree_attention(const Kv8Cache& c, int q_heads);
+hipError_t launch_kv8_tree_attention(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, const Kv8Tree& tree,
+                                     uint16_t* out, int q_heads, float softmax_scale, const Kv8Plan& plan,
+                                     void* workspace, bool bf16, hipStream_t stream);
+
+// Those words and the tokens' positions, from each node's parent.
+hipError_t launch_kv8_tree_mask(const int32_t* parents, const int32_t* cu, const int32_t* lens, int32_t* mask,
+                                int32_t* positions, int tokens, int batch, int words, int max_q_len,
+                                hipStream_t stream);
+
+// New token i becomes what new token path[b, i] was, for i < kept[b], in each of
+// `layers` caches that lie one behind the other; path [batch, width].
+hipError_t launch_kv8_tree_keep(const Kv8Cache& c, int layers, const int32_t* path, const int32_t* kept, int width,
+                                hipStream_t stream);
+
+// Drafted tokens against the target's probabilities.
+struct VerifyArgs {
+  const float* probs;      // [tokens, vocab]
+  const float* draft;      // the same, or NULL
+  const int32_t* token;    // [tokens]
+  const int32_t* parents;  // [tokens], or NULL: chains
+  const float* uniform;    // [tokens]
+  const int32_t* cu;       // [batch + 1]
+  int32_t *kept, *path, *next;  // [batch], [batch, max_q_len], [batch]
+  int tokens, vocab, max_q_len;
+  // in the workspace, set by the launcher
+  double* sums;
+  void* walks;
+  int32_t* lists;
+};
+constexpr int kVerifyPiece = 4096;  // values of a row that a workgroup takes
+size_t verify_workspace(int batch, int vocab, int max_q_len);
+hipError_t launch_draft_verify(VerifyArgs a, int batch, void* workspace, hipStream_t stream);
 
 }  // namespace mq

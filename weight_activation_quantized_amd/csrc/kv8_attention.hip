@@ -29,6 +29,14 @@
 // behind the last token are cleared, so whatever a page holds there (NaN codes
 // too) counts for nothing; so do pages whose number is not one of the pool's.
 // A row that sees no key is 0.
+//
+// Drafted tokens (kTree): a row sees every key before the sequence's new ones and
+// of those the ones that its words name. Only tiles that reach the new tokens
+// look at the words, 16 or 8 bits per lane. A branch's NaN must not reach the
+// others there: masked scores go by the select as above, and V codes of NaN are
+// taken out of the product and counted in one of their own, of ones where a code
+// is NaN and ones where a row sees the key; where that count is not 0, the
+// output is NaN.
 #include <type_traits>
 
 #include "block8_launch.h"
@@ -113,6 +121,38 @@ __device__ __forceinline__ Span tiles_of(int tiles, int splits, int z, int least
   return s;
 }
 
+// Which of the 16 keys from new token `at` on (negative: before the new ones,
+// where all are seen) a row's words name, the first in the lowest bit.
+__device__ __forceinline__ uint32_t tree_bits(const int32_t* words, int count, int at) {
+  if (at <= -16) return 0xffffu;
+  const int k = at >> 5;
+  const uint32_t lo = k < 0 ? 0xffffffffu : k < count ? static_cast<uint32_t>(words[k]) : 0u;
+  const uint32_t hi = k + 1 < count ? static_cast<uint32_t>(words[k + 1]) : 0u;
+  return static_cast<uint32_t>((static_cast<uint64_t>(hi) << 32 | lo) >> (at & 31)) & 0xffffu;
+}
+__device__ __forceinline__ uint32_t first_bits(int n) { return n >= 16 ? 0xffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// Of 16 codes the NaN ones become 0 in v; returned are codes of 1 where they were.
+__device__ __forceinline__ u32x4 take_nan(u32x4& v) {
+  u32x4 ones;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t nan = (((v[w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+    v[w] &= ~(nan * 0xffu);
+    ones[w] = nan * 0x38u;
+  }
+  return ones;
+}
+__device__ __forceinline__ bool has_any(u32x4 v) { return (v[0] | v[1] | v[2] | v[3]) != 0; }
+
+// 8 fp16 values, 1 where the bit is set.
+__device__ __forceinline__ f16x8 ones_of(uint32_t bits) {
+  f16x8 v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (bits >> e) & 1 ? static_cast<f16>(1.f) : static_cast<f16>(0.f);
+  return v;
+}
+
 // The workspace of a split call: for every split and row (token, head) its
 // maximum and sum, then its unnormalised output.
 struct Parts {
@@ -138,11 +178,11 @@ struct Parts {
 // inputs in turn.)
 // ---------------------------------------------------------------------------
 
-template <int D, int kWaves, bool kBf16>
+template <int D, int kWaves, bool kBf16, bool kTree>
 __global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, const uint16_t* __restrict__ q,
                                                                  int64_t q_stride, uint16_t* __restrict__ out,
                                                                  Parts parts, int group, int splits,
-                                                                 float scale_log2) {
+                                                                 float scale_log2, Kv8Tree tree) {
   constexpr int kKs = D / 32, kDt = D / 16;  // k-steps of a score, 16-dimension tiles of the output
   __shared__ float so[kWaves][16][D + 4];
   __shared__ float sm[kWaves][16], sl[kWaves][16];
@@ -176,7 +216,9 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, con
 
   // Keys that some row of this tile sees, in tiles of 64, and this split's.
   const int last_t = min(16 * rt + 15, rows - 1) / group;
-  const int top = min(seq.len - seq.n + last_t, seq.seen - 1);  // the row tile's last key
+  const int top = kTree ? seq.seen - 1 : min(seq.len - seq.n + last_t, seq.seen - 1);  // the row tile's last key
+  const int start = seq.len - seq.n;  // the first new token
+  const int32_t* const words = kTree ? tree.mask + static_cast<int64_t>(seq.row0 + tq) * tree.words : nullptr;
   const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, 4);
   const size_t all_rows = static_cast<size_t>(c.tokens) * heads;
   if (splits > 1 && span.first >= span.end) {  // no keys: sums of zero, whose outputs nobody reads
@@ -257,18 +299,37 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, con
 
     // Tokens 64 tile + 16 h + 4 j + e of this lane: seen up to `limit`.
     const int t0 = 64 * tile + 16 * h;
-    const int see = known(vid) ? limit - t0 : -1;
+    const int see = known(vid) ? (kTree ? min(start, seq.seen) - 1 : limit) - t0 : -1;
     float x[16];
     float mt = kNegInf;
+    uint32_t bits = 0xffffu;  // (of trees) keys that the row sees
+    bool nans = false;        // (of trees) V codes among them may be NaN
     if (__any(see < 15)) {
+      if constexpr (kTree) {
+        bits = known(vid) ? tree_bits(words, tree.words, t0 - start) & first_bits(seq.seen - t0) : 0u;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[e] = e <= see ? fmaf(s[e / 4][e % 4], f, lv) : kNegInf;
-        mt = fmaxf(mt, x[e]);
+        for (int e = 0; e < 16; ++e) {
+          x[e] = (bits >> e) & 1 ? fmaf(s[e / 4][e % 4], f, lv) : kNegInf;
+          mt = fmaxf(mt, x[e]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[e] = e <= see ? fmaf(s[e / 4][e % 4], f, lv) : kNegInf;
+          mt = fmaxf(mt, x[e]);
+        }
       }
       const int count = known(vid) ? top - t0 + 1 : 0;
 #pragma unroll
       for (int d = 0; d < kDt; ++d) vc[d] = first_bytes(vc[d], count);
+      if constexpr (kTree) {
+#pragma unroll
+        for (int d = 0; d < kDt; ++d) {
+          u32x4 v = vc[d];
+          nans |= has_any(take_nan(v));
+        }
+        nans = __any(nans);
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -297,6 +358,16 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, con
     for (int d = 0; d < kDt; ++d) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[d][e] *= shrink;
+      if constexpr (kTree) {
+        if (nans) {
+          const u32x4 ones = take_nan(vc[d]);
+          f32x4 count = {0.f, 0.f, 0.f, 0.f};
+          count = mfma_16x16x32<false>(widen<false>(ones[0], ones[1]), ones_of(bits & 0xffu), count);
+          count = mfma_16x16x32<false>(widen<false>(ones[2], ones[3]), ones_of(bits >> 8), count);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[d][e] = count[e] > 0.f ? __builtin_nanf("") : o[d][e];
+        }
+      }
       o[d] = mfma_16x16x32<false>(widen<false>(vc[d][0], vc[d][1]), p0, o[d]);
       o[d] = mfma_16x16x32<false>(widen<false>(vc[d][2], vc[d][3]), p1, o[d]);
     }
@@ -493,16 +564,17 @@ __device__ __forceinline__ RowTile row_tile(const Kv8Cache& c, int group, int n)
   return {-1, 0};
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kTree>
 __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint16_t* __restrict__ q, int64_t q_stride,
                                                          uint16_t* __restrict__ out, Parts parts, int group,
-                                                         int splits, float scale_log2) {
+                                                         int splits, float scale_log2, Kv8Tree tree) {
   constexpr int kRows = kPromptRows, kKs = D / 16, kDt = D / 32;
   constexpr int kKRow = 2 * D;  // bytes of a widened K row
   constexpr int kKBytes = 64 * kKRow, kVBytes = D * 128;
   constexpr int kBuf = kKBytes + kVBytes;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kBuf];
   lds_u8* const lds = (lds_u8*)(smem);
+  __shared__ int nans;  // (of trees) a V code of a tile with new tokens is NaN
 
   // Heads next to each other (the XCDs take workgroups in turn: one that gets
   // the same head again finds its codes in L2), then sequence by sequence the
@@ -537,7 +609,10 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
   }
 
   const int last_t = min(kRows * rt + kRows - 1, rows - 1) / group;
-  const int top = __builtin_amdgcn_readfirstlane(min(seq.len - seq.n + last_t, seq.seen - 1));  // the last key
+  const int top = __builtin_amdgcn_readfirstlane(
+      kTree ? seq.seen - 1 : min(seq.len - seq.n + last_t, seq.seen - 1));  // the last key
+  const int start = __builtin_amdgcn_readfirstlane(seq.len - seq.n);        // the first new token
+  const int32_t* const words = kTree ? tree.mask + static_cast<int64_t>(seq.row0 + tq) * tree.words : nullptr;
   const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, 2);
   const int first = __builtin_amdgcn_readfirstlane(span.first);
   const int tiles = __builtin_amdgcn_readfirstlane(span.end - span.first);
@@ -635,6 +710,8 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
               __builtin_bit_cast(u32x4, widen<kBf16>(kreg[2 * step], kreg[2 * step + 1]));
       } else if (does_v) {
         if (step == 2 && held < 16) vreg = first_bytes(vreg, held);
+        if (kTree && step == 2 && 64 * (first + j) > start)
+          if (has_any(take_nan(vreg))) nans = 1;
         *(lds_u32x4*)(to + (step == 2 ? vto0 : vto1)) =
             __builtin_bit_cast(u32x4, widen<false>(vreg[2 * step - 4], vreg[2 * step - 3]));
       }
@@ -646,7 +723,8 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 
     const int wave_low = __builtin_amdgcn_readfirstlane(
         min(seq.len - seq.n + min(kRows * rt + 32 * wave, rows - 1) / group, seq.seen - 1));  // first row's last key
-    const int wave_whole = kRows * rt + 32 * wave + 31 < rows ? wave_low : -1;  // keys that every lane sees
+    const int wave_whole =  // keys that every lane sees
+        kTree ? min(start, seq.seen) - 1 : kRows * rt + 32 * wave + 31 < rows ? wave_low : -1;
     const int ktok = (i & 19) | ((i & 4) << 1) | ((i & 8) >> 1);  // bits 2 and 3 exchanged
     int kat[kKs], vat[4];
 #pragma unroll
@@ -700,6 +778,11 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
       }
     };
 
+    // (of trees) Which of this lane's 8 keys of the part at t its row sees.
+    auto row_bits = [&](int t) {
+      return ((tree_bits(words, tree.words, t - start) & first_bits(seq.seen - t)) >> (8 * h)) & 0xffu;
+    };
+
     auto softmax = [&](int j) {
       const int t0 = 64 * (first + j);
       const int part = 4 * (j & 15);
@@ -712,12 +795,19 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
         iv[p] = lane_float(iv0, part + p);
       }
       if (seen != 15 || t0 + 63 > wave_whole) {
+        uint32_t bits = 0;
+        if constexpr (kTree) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) bits |= ((seen >> p) & 1 ? row_bits(t0 + 16 * p) : 0u) << (8 * p);
+        }
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int p = 2 * a + e / 8;
-            s[a][e] = ((seen >> p) & 1) && t0 + 16 * p + 8 * h + e % 8 <= limit ? s[a][e] : kNegInf;
+            const bool mine = kTree ? (bits >> (8 * p + e % 8)) & 1
+                                    : ((seen >> p) & 1) && t0 + 16 * p + 8 * h + e % 8 <= limit;
+            s[a][e] = mine ? s[a][e] : kNegInf;
           }
       }
       float mt = kNegInf;
@@ -755,6 +845,8 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
       }
     };
 
+    if (kTree && threadIdx.x == 0) nans = 0;
+    if constexpr (kTree) phase_end();
     id1 = batch_pages(0);
     ks1 = c.k_scales[unit(id1)];
     vs1 = c.v_scales[unit(id1)];
@@ -784,6 +876,28 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
     }
     products(tiles, 0, std::false_type{});
     if (half == 0) phase_end();  // the second half's last softmax phase
+    if constexpr (kTree) {
+      // (rare, and on its own: those tiles' codes once more, from memory)
+      if (nans) {
+        for (int t0 = max(64 * first, start & ~63); t0 <= min(64 * (first + tiles) - 1, top); t0 += 16) {
+          const int id = table[t0 >> c.page_shift];
+          if (!known(id)) continue;
+          const uint32_t bits = row_bits(t0);
+          const uint8_t* const page = vhead + static_cast<uint64_t>(id) * page_bytes + ((t0 & (c.page - 1)) + 8 * h);
+#pragma unroll 1
+          for (int d = 0; d < kDt; ++d) {
+            const u32x2 codes = *reinterpret_cast<const u32x2*>(page + static_cast<size_t>(32 * d + i) * c.page);
+            u32x4 v = first_bytes(u32x4{codes[0], codes[1], 0u, 0u}, top - t0 - 8 * h + 1);
+            const u32x4 ones = take_nan(v);
+            const f32x16 count = mfma_32x32x16<false>(widen<false>(ones[0], ones[1]), ones_of(bits), f32x16{});
+#pragma unroll
+            for (int k = 0; k < kDt; ++k)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[k][e] = k == d && count[e] > 0.f ? __builtin_nanf("") : o[k][e];
+          }
+        }
+      }
+    }
   }
 
   l += __shfl_xor(l, 32, kWave);
@@ -827,9 +941,9 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 constexpr int kDecodeRows = 64;
 constexpr int64_t kDecodeTiles = 24576;
 
-template <int D, bool kBf16>
-hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, uint16_t* out, int q_heads, float scale,
-                      const Kv8Plan& plan, void* workspace, hipStream_t stream) {
+template <int D, bool kBf16, bool kTree>
+hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, const Kv8Tree& tree, uint16_t* out,
+                      int q_heads, float scale, const Kv8Plan& plan, void* workspace, hipStream_t stream) {
   const int group = q_heads / c.kv_heads;
   const int most = c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
   const int64_t rows = static_cast<int64_t>(most) * group, all = static_cast<int64_t>(c.tokens) * q_heads;
@@ -844,20 +958,32 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, ui
     const int row_tiles = static_cast<int>((rows + 15) / 16);
     const dim3 grid(static_cast<uint32_t>(c.kv_heads * row_tiles), static_cast<uint32_t>(c.batch),
                     static_cast<uint32_t>(plan.splits));
-    e = plan.waves == 8 ? launch_kernel(kv8_decode_kernel<D, 8, kBf16>, grid, dim3(512), 0, stream, c, q, q_stride, out,
-                                        parts, group, plan.splits, scale_log2)
-                        : launch_kernel(kv8_decode_kernel<D, 4, kBf16>, grid, dim3(256), 0, stream, c, q, q_stride, out,
-                                        parts, group, plan.splits, scale_log2);
+    e = plan.waves == 8 ? launch_kernel(kv8_decode_kernel<D, 8, kBf16, kTree>, grid, dim3(512), 0, stream, c, q,
+                                        q_stride, out, parts, group, plan.splits, scale_log2, tree)
+                        : launch_kernel(kv8_decode_kernel<D, 4, kBf16, kTree>, grid, dim3(256), 0, stream, c, q,
+                                        q_stride, out, parts, group, plan.splits, scale_log2, tree);
   } else {
     constexpr int64_t kWide = int64_t{1} << 22;  // a dimension of the grid stays under 2^32 work-items
     const dim3 grid(static_cast<uint32_t>(plan.prompt_blocks < kWide ? plan.prompt_blocks : kWide),
                     static_cast<uint32_t>((plan.prompt_blocks + kWide - 1) / kWide));
-    e = launch_kernel(kv8_prompt_kernel<D, kBf16>, grid, dim3(512), 0, stream, c, q, q_stride, out, parts, group,
-                      plan.splits, scale_log2);
+    e = launch_kernel(kv8_prompt_kernel<D, kBf16, kTree>, grid, dim3(512), 0, stream, c, q, q_stride, out, parts, group,
+                      plan.splits, scale_log2, tree);
   }
   if (e != hipSuccess || plan.splits == 1) return e;
   return launch_kernel(kv8_join_kernel<D, kBf16>, dim3(static_cast<uint32_t>((all + 3) / 4)), dim3(256), 0, stream, c,
                        out, parts, q_heads, plan.splits);
+}
+
+template <bool kTree>
+hipError_t launch(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, const Kv8Tree& tree, uint16_t* out,
+                  int q_heads, float scale, const Kv8Plan& plan, void* workspace, bool bf16, hipStream_t stream) {
+  if (c.head_dim == 128)
+    return bf16 ? launch_dim<128, true, kTree>(c, q, q_stride, tree, out, q_heads, scale, plan, workspace, stream)
+                : launch_dim<128, false, kTree>(c, q, q_stride, tree, out, q_heads, scale, plan, workspace, stream);
+  if (c.head_dim == 64)
+    return bf16 ? launch_dim<64, true, kTree>(c, q, q_stride, tree, out, q_heads, scale, plan, workspace, stream)
+                : launch_dim<64, false, kTree>(c, q, q_stride, tree, out, q_heads, scale, plan, workspace, stream);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -920,13 +1046,15 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
 hipError_t launch_kv8_attention(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, uint16_t* out, int q_heads,
                                 float softmax_scale, const Kv8Plan& plan, void* workspace, bool bf16,
                                 hipStream_t stream) {
-  if (c.head_dim == 128)
-    return bf16 ? launch_dim<128, true>(c, q, q_stride, out, q_heads, softmax_scale, plan, workspace, stream)
-                : launch_dim<128, false>(c, q, q_stride, out, q_heads, softmax_scale, plan, workspace, stream);
-  if (c.head_dim == 64)
-    return bf16 ? launch_dim<64, true>(c, q, q_stride, out, q_heads, softmax_scale, plan, workspace, stream)
-                : launch_dim<64, false>(c, q, q_stride, out, q_heads, softmax_scale, plan, workspace, stream);
-  return hipErrorInvalidValue;
+  return launch<false>(c, q, q_stride, Kv8Tree{}, out, q_heads, softmax_scale, plan, workspace, bf16, stream);
+}
+
+Kv8Plan plan_kv8_tree_attention(const Kv8Cache& c, int q_heads) { return plan_kv8_attention(c, q_heads); }
+
+hipError_t launch_kv8_tree_attention(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, const Kv8Tree& tree,
+                                     uint16_t* out, int q_heads, float softmax_scale, const Kv8Plan& plan,
+                                     void* workspace, bool bf16, hipStream_t stream) {
+  return launch<true>(c, q, q_stride, tree, out, q_heads, softmax_scale, plan, workspace, bf16, stream);
 }
 
 }  // namespace mq

@@ -895,7 +895,7 @@ static mq_status kv8_heads(int64_t Hq, int64_t Hkv) {
 
 // The plan of a call of these sizes; false where it is refused or does nothing.
 static bool kv8_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t table_width,
-                     int64_t max_q_len, mq::Kv8Plan& plan) {
+                     int64_t max_q_len, mq::Kv8Plan& plan, bool tree = false) {
   // any addresses do: only sizes are looked at
   static const float some[4] = {};
   const uint8_t* const p = reinterpret_cast<const uint8_t*>(16);
@@ -904,7 +904,7 @@ static bool kv8_plan(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, i
   if (kv8_cache(p, p, some, some, t, t, t, T, B, Hkv, D, page, 1, table_width, max_q_len, c) != MQ_OK ||
       kv8_heads(Hq, Hkv) != MQ_OK || T == 0 || B == 0)
     return false;
-  plan = mq::plan_kv8_attention(c, static_cast<int>(Hq));
+  plan = tree ? mq::plan_kv8_tree_attention(c, static_cast<int>(Hq)) : mq::plan_kv8_attention(c, static_cast<int>(Hq));
   return true;
 }
 
@@ -922,12 +922,24 @@ int32_t mq_kv8_attention_form(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int
                                                                         : MQ_KV8_FORM_PROMPT;
 }
 
+// Words of a tree's masks, 32 new tokens each.
+static mq_status kv8_tree_words(const int32_t* mask, int64_t T, int64_t words, int64_t max_q_len) {
+  if (max_q_len < 1 || max_q_len > mq::kKv8MaxTree)
+    return fail(MQ_ERR_SHAPE, "max_q_len=%lld: a tree has at most %d nodes", (long long)max_q_len, mq::kKv8MaxTree);
+  if (words < (max_q_len + 31) / 32 || words > kMaxDim)
+    return fail(MQ_ERR_SHAPE, "tree_width=%lld words do not hold max_q_len=%lld bits", (long long)words, (long long)max_q_len);
+  MQ_TRY(need(mask, T, "tree"));
+  if (!aligned(mask, 4)) return fail(MQ_ERR_ALIGN, "tree must be 4-byte aligned");
+  return MQ_OK;
+}
+
 static mq_status kv8_attention_impl(const uint16_t* q, int64_t q_stride, const uint8_t* k_cache, const uint8_t* v_cache,
                                     const float* k_scales, const float* v_scales, const int32_t* block_table,
                                     const int32_t* cu_q, const int32_t* kv_lens, uint16_t* out, int64_t T, int64_t B,
                                     int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t num_pages,
                                     int64_t table_width, int64_t max_q_len, float softmax_scale, void* workspace,
-                                    size_t workspace_bytes, bool bf16, void* stream) {
+                                    size_t workspace_bytes, bool bf16, void* stream,
+                                    const mq::Kv8Tree* tree = nullptr) {
   mq::Kv8Cache c;
   MQ_TRY(kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, T, B, Hkv, D, page, num_pages,
                    table_width, max_q_len, c));
@@ -938,7 +950,9 @@ static mq_status kv8_attention_impl(const uint16_t* q, int64_t q_stride, const u
   MQ_TRY(kv8_rows(q, T, Hq * D, q_stride, "q", qb));
   MQ_TRY(need(out, T, "out"));
   if (!aligned(out, 16)) return fail(MQ_ERR_ALIGN, "out must be 16-byte aligned");
-  const mq::Kv8Plan plan = mq::plan_kv8_attention(c, static_cast<int>(Hq));
+  if (tree) MQ_TRY(kv8_tree_words(tree->mask, T, tree->words, max_q_len));
+  const mq::Kv8Plan plan = tree ? mq::plan_kv8_tree_attention(c, static_cast<int>(Hq))
+                                : mq::plan_kv8_attention(c, static_cast<int>(Hq));
   const bool empty = T == 0 || B == 0;
   const size_t ws = empty ? 0 : plan.workspace_bytes;
   MQ_TRY(check_workspace(workspace, workspace_bytes, ws));
@@ -950,10 +964,15 @@ static mq_status kv8_attention_impl(const uint16_t* q, int64_t q_stride, const u
                       {v_scales, sc, "v_scales"},
                       {block_table, static_cast<size_t>(B * table_width) * 4, "block_table"},
                       {cu_q, static_cast<size_t>(B + 1) * 4, "cu_q"},
-                      {kv_lens, static_cast<size_t>(B) * 4, "kv_lens"}};
+                      {kv_lens, static_cast<size_t>(B) * 4, "kv_lens"},
+                      {tree ? tree->mask : nullptr, tree ? static_cast<size_t>(T) * tree->words * 4 : 0, "tree"}};
   const Range outs[] = {{out, static_cast<size_t>(T) * Hq * D * 2, "out"}, {ws ? workspace : nullptr, ws, "workspace"}};
   MQ_TRY(check_alias(in, outs));
   if (empty) return ok();
+  if (tree)
+    return hip_status(mq::launch_kv8_tree_attention(c, q, q_stride, *tree, out, static_cast<int>(Hq), softmax_scale,
+                                                    plan, ws ? workspace : nullptr, bf16, as_stream(stream)),
+                      "kv8_tree_attention launch");
   return hip_status(mq::launch_kv8_attention(c, q, q_stride, out, static_cast<int>(Hq), softmax_scale, plan,
                                              ws ? workspace : nullptr, bf16, as_stream(stream)),
                     "kv8_attention launch");
@@ -978,6 +997,258 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
   return kv8_attention_impl(q, q_stride, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, out, T, B, Hq,
                             Hkv, D, page, num_pages, table_width, max_q_len, softmax_scale, workspace, workspace_bytes,
                             true, stream);
+}
+
+// ---- drafted tokens over the paged cache -----------------------------------
+
+size_t mq_kv8_tree_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
+                                             int64_t table_width, int64_t max_q_len) {
+  mq::Kv8Plan plan;
+  return max_q_len <= mq::kKv8MaxTree && kv8_plan(T, B, Hq, Hkv, D, page, table_width, max_q_len, plan, true)
+             ? plan.workspace_bytes
+             : 0;
+}
+
+mq_status mq_kv8_tree_attention(const uint16_t* q, int64_t q_stride, const int32_t* tree, int64_t tree_width,
+                                const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scales,
+                                const float* v_scales, const int32_t* block_table, const int32_t* cu_q,
+                                const int32_t* kv_lens, uint16_t* out, int64_t T, int64_t B, int64_t Hq, int64_t Hkv,
+                                int64_t D, int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len,
+                                float softmax_scale, void* workspace, size_t workspace_bytes, void* stream) {
+  MQ_TRY(kv8_tree_words(tree, T, tree_width, max_q_len));
+  const mq::Kv8Tree t = {tree, static_cast<int>(tree_width)};
+  return kv8_attention_impl(q, q_stride, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, out, T, B, Hq,
+                            Hkv, D, page, num_pages, table_width, max_q_len, softmax_scale, workspace, workspace_bytes,
+                            false, stream, &t);
+}
+
+mq_status mq_kv8_tree_attention_bf16(const uint16_t* q, int64_t q_stride, const int32_t* tree, int64_t tree_width,
+                                     const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scales,
+                                     const float* v_scales, const int32_t* block_table, const int32_t* cu_q,
+                                     const int32_t* kv_lens, uint16_t* out, int64_t T, int64_t B, int64_t Hq,
+                                     int64_t Hkv, int64_t D, int64_t page, int64_t num_pages, int64_t table_width,
+                                     int64_t max_q_len, float softmax_scale, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  MQ_TRY(kv8_tree_words(tree, T, tree_width, max_q_len));
+  const mq::Kv8Tree t = {tree, static_cast<int>(tree_width)};
+  return kv8_attention_impl(q, q_stride, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, out, T, B, Hq,
+                            Hkv, D, page, num_pages, table_width, max_q_len, softmax_scale, workspace, workspace_bytes,
+                            true, stream, &t);
+}
+
+mq_status mq_kv8_tree_mask(const int32_t* parents, const int32_t* cu_q, const int32_t* kv_lens, int32_t* tree,
+                           int32_t* positions, int64_t T, int64_t B, int64_t tree_width, int64_t max_q_len,
+                           void* stream) {
+  if (T < 0 || T > (int64_t{1} << 26)) return fail(MQ_ERR_SHAPE, "T=%lld out of range", (long long)T);
+  if (B < 0 || B > 65535) return fail(MQ_ERR_SHAPE, "B=%lld must lie in [0, 65535]", (long long)B);
+  MQ_TRY(kv8_tree_words(tree, T, tree_width, max_q_len));
+  MQ_TRY(need(parents, T, "parents"));
+  MQ_TRY(need(positions, T, "positions"));
+  MQ_TRY(need(cu_q, B, "cu_q"));
+  MQ_TRY(need(kv_lens, B, "kv_lens"));
+  if (!aligned(parents, 4) || !aligned(positions, 4) || !aligned(cu_q, 4) || !aligned(kv_lens, 4))
+    return fail(MQ_ERR_ALIGN, "parents, positions, cu_q and kv_lens must be 4-byte aligned");
+  const Range in[] = {{parents, static_cast<size_t>(T) * 4, "parents"},
+                      {cu_q, static_cast<size_t>(B + 1) * 4, "cu_q"},
+                      {kv_lens, static_cast<size_t>(B) * 4, "kv_lens"}};
+  const Range out[] = {{tree, static_cast<size_t>(T) * tree_width * 4, "tree"}, {positions, static_cast<size_t>(T) * 4, "positions"}};
+  MQ_TRY(check_alias(in, out));
+  if (T == 0 || B == 0) return ok();
+  return hip_status(mq::launch_kv8_tree_mask(parents, cu_q, kv_lens, tree, positions, static_cast<int>(T),
+                                             static_cast<int>(B), static_cast<int>(tree_width),
+                                             static_cast<int>(max_q_len), as_stream(stream)),
+                    "kv8_tree_mask launch");
+}
+
+mq_status mq_kv8_tree_keep(uint8_t* k_cache, uint8_t* v_cache, float* k_scales, float* v_scales,
+                           const int32_t* block_table, const int32_t* cu_q, const int32_t* kv_lens,
+                           const int32_t* path, const int32_t* kept, int64_t layers, int64_t B, int64_t Hkv, int64_t D,
+                           int64_t page, int64_t num_pages, int64_t table_width, int64_t path_width, void* stream) {
+  if (path_width < 1 || path_width > mq::kKv8MaxTree)
+    return fail(MQ_ERR_SHAPE, "path_width=%lld: a tree has 1 to %d nodes", (long long)path_width, mq::kKv8MaxTree);
+  mq::Kv8Cache c;
+  MQ_TRY(kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, 1, B, Hkv, D, page, num_pages,
+                   table_width, path_width, c));
+  if (layers < 0 || layers > 65535) return fail(MQ_ERR_SHAPE, "layers=%lld must lie in [0, 65535]", (long long)layers);
+  MQ_TRY(need(path, B, "path"));
+  MQ_TRY(need(kept, B, "kept"));
+  if (!aligned(path, 4) || !aligned(kept, 4)) return fail(MQ_ERR_ALIGN, "path and kept must be 4-byte aligned");
+  const size_t cache = static_cast<size_t>(layers) * num_pages * Hkv * page * D,
+               sc = static_cast<size_t>(layers) * num_pages * Hkv * 4;
+  const Range in[] = {{block_table, static_cast<size_t>(B * table_width) * 4, "block_table"},
+                      {cu_q, static_cast<size_t>(B + 1) * 4, "cu_q"},
+                      {kv_lens, static_cast<size_t>(B) * 4, "kv_lens"},
+                      {path, static_cast<size_t>(B * path_width) * 4, "path"},
+                      {kept, static_cast<size_t>(B) * 4, "kept"}};
+  const Range out[] = {{k_cache, cache, "k_cache"}, {v_cache, cache, "v_cache"}, {k_scales, sc, "k_scales"}, {v_scales, sc, "v_scales"}};
+  MQ_TRY(check_alias(in, out));
+  if (layers == 0 || B == 0) return ok();
+  if (B * Hkv >= (int64_t{1} << 23))
+    return fail(MQ_ERR_SHAPE, "B * Hkv = %lld must stay below 2^23", (long long)(B * Hkv));
+  return hip_status(mq::launch_kv8_tree_keep(c, static_cast<int>(layers), path, kept, static_cast<int>(path_width),
+                                             as_stream(stream)),
+                    "kv8_tree_keep launch");
+}
+
+// q_out over q in place: the rows are the same, and no row of k or v may lie
+// between the heads that are written.
+static mq_status kv8_in_place(const uint16_t* q, int64_t stride, int64_t width, size_t bytes, const uint16_t* x,
+                              int64_t x_stride, int64_t x_width, size_t x_bytes, const char* name) {
+  if (!overlap({q, bytes, ""}, {x, x_bytes, ""})) return MQ_OK;
+  const int64_t apart = (reinterpret_cast<intptr_t>(x) - reinterpret_cast<intptr_t>(q)) / 2;  // (both 16-byte aligned)
+  const int64_t at = ((apart % stride) + stride) % stride;
+  if (x_stride != stride || at < width || at + x_width > stride)
+    return fail(MQ_ERR_ALIAS, "output q_out overlaps input %s", name);
+  return MQ_OK;
+}
+
+static mq_status kv8_rope_append_impl(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t q_stride,
+                                      int64_t k_stride, int64_t v_stride, uint16_t* q_out, int64_t q_out_stride,
+                                      const float* cos_sin, const int32_t* positions, const uint16_t* q_weight,
+                                      const uint16_t* k_weight, double eps, int64_t max_pos, int64_t rot,
+                                      int32_t interleaved, uint8_t* k_cache, uint8_t* v_cache, float* k_scales,
+                                      float* v_scales, const int32_t* block_table, const int32_t* cu_q,
+                                      const int32_t* kv_lens, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                                      int64_t page, int64_t num_pages, int64_t table_width, int64_t max_q_len,
+                                      bool bf16, void* stream) {
+  mq::Kv8Cache c;
+  MQ_TRY(kv8_cache(k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, T, B, Hkv, D, page, num_pages,
+                   table_width, max_q_len, c));
+  MQ_TRY(kv8_heads(Hq, Hkv));
+  if (rot < 16 || rot > D || rot % 16)
+    return fail(MQ_ERR_UNSUPPORTED, "rot=%lld must be a multiple of 16 in [16, head_dim]", (long long)rot);
+  if (max_pos < 1 || max_pos > (int64_t{1} << 30)) return fail(MQ_ERR_SHAPE, "max_pos=%lld out of range", (long long)max_pos);
+  if (interleaved != 0 && interleaved != 1) return fail(MQ_ERR_UNSUPPORTED, "interleaved must be 0 or 1");
+  if (!(eps >= 0.0 && eps <= 1.0)) return fail(MQ_ERR_UNSUPPORTED, "eps=%g must lie in [0, 1]", eps);
+  if (!q_weight != !k_weight) return fail(MQ_ERR_NULL, "q_weight and k_weight go together");
+  size_t qb = 0, kb = 0, vb = 0, ob = 0;
+  MQ_TRY(kv8_rows(q, T, Hq * D, q_stride, "q", qb));
+  MQ_TRY(kv8_rows(k, T, Hkv * D, k_stride, "k", kb));
+  MQ_TRY(kv8_rows(v, T, Hkv * D, v_stride, "v", vb));
+  MQ_TRY(kv8_rows(q_out, T, Hq * D, q_out_stride, "q_out", ob));
+  MQ_TRY(need(cos_sin, 1, "cos_sin"));
+  if (!aligned(cos_sin, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 4))
+    return fail(MQ_ERR_ALIGN, "cos_sin and the weights must be 16-byte, positions 4-byte aligned");
+  const bool in_place = q_out == q;
+  if (in_place && T > 1 && q_out_stride != q_stride)
+    return fail(MQ_ERR_ALIAS, "q_out in place of q needs its stride");
+  const size_t cache = static_cast<size_t>(num_pages) * Hkv * page * D, sc = static_cast<size_t>(num_pages) * Hkv * 4;
+  const size_t wb = q_weight ? static_cast<size_t>(D) * 2 : 0;
+  const Range in[] = {{q, qb, "q"},
+                      {k, kb, "k"},
+                      {v, vb, "v"},
+                      {cos_sin, static_cast<size_t>(max_pos) * rot * 4, "cos_sin"},
+                      {positions, positions ? static_cast<size_t>(T) * 4 : 0, "positions"},
+                      {q_weight, wb, "q_weight"},
+                      {k_weight, wb, "k_weight"},
+                      {block_table, static_cast<size_t>(B * table_width) * 4, "block_table"},
+                      {cu_q, static_cast<size_t>(B + 1) * 4, "cu_q"},
+                      {kv_lens, static_cast<size_t>(B) * 4, "kv_lens"}};
+  const Range caches[] = {{k_cache, cache, "k_cache"}, {v_cache, cache, "v_cache"}, {k_scales, sc, "k_scales"}, {v_scales, sc, "v_scales"}};
+  MQ_TRY(check_alias(in, caches));
+  const Range rotated = {q_out, ob, "q_out"};
+  for (const Range& r : caches)
+    if (overlap(rotated, r)) return fail(MQ_ERR_ALIAS, "output q_out overlaps output %s", r.name);
+  for (size_t i = in_place ? 3 : 0; i < sizeof(in) / sizeof(in[0]); ++i)
+    if (overlap(rotated, in[i])) return fail(MQ_ERR_ALIAS, "output q_out overlaps input %s", in[i].name);
+  if (in_place) {
+    MQ_TRY(kv8_in_place(q, q_stride, Hq * D, qb, k, k_stride, Hkv * D, kb, "k"));
+    MQ_TRY(kv8_in_place(q, q_stride, Hq * D, qb, v, v_stride, Hkv * D, vb, "v"));
+  }
+  if (T == 0 || B == 0) return ok();
+  if (mq::kv8_rope_append_blocks(c, static_cast<int>(Hq)) >= (int64_t{1} << 24))
+    return fail(MQ_ERR_SHAPE, "B * pages of max_q_len tokens * (Hq + 2 Hkv) = %lld must stay below 2^24",
+                (long long)mq::kv8_rope_append_blocks(c, static_cast<int>(Hq)));
+  mq::Kv8Turn t = {};
+  t.q = q;
+  t.q_out = q_out;
+  t.q_stride = q_stride;
+  t.q_out_stride = q_out_stride;
+  t.cos_sin = cos_sin;
+  t.positions = positions;
+  t.q_weight = q_weight;
+  t.k_weight = k_weight;
+  t.eps = eps;
+  t.q_heads = static_cast<int>(Hq);
+  t.max_pos = static_cast<int>(max_pos);
+  t.rot = static_cast<int>(rot);
+  t.next = interleaved != 0;
+  return hip_status(mq::launch_kv8_rope_append(c, k, v, k_stride, v_stride, t, bf16, as_stream(stream)),
+                    "kv8_rope_append launch");
+}
+
+#define MQ_ROPE_APPEND(NAME, BF16)                                                                                      \
+  mq_status NAME(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t q_stride, int64_t k_stride,          \
+                 int64_t v_stride, uint16_t* q_out, int64_t q_out_stride, const float* cos_sin,                        \
+                 const int32_t* positions, const uint16_t* q_weight, const uint16_t* k_weight, double eps,             \
+                 int64_t max_pos, int64_t rot, int32_t interleaved, uint8_t* k_cache, uint8_t* v_cache,                \
+                 float* k_scales, float* v_scales, const int32_t* block_table, const int32_t* cu_q,                    \
+                 const int32_t* kv_lens, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,       \
+                 int64_t num_pages, int64_t table_width, int64_t max_q_len, void* stream) {                            \
+    return kv8_rope_append_impl(q, k, v, q_stride, k_stride, v_stride, q_out, q_out_stride, cos_sin, positions,        \
+                                q_weight, k_weight, eps, max_pos, rot, interleaved, k_cache, v_cache, k_scales,        \
+                                v_scales, block_table, cu_q, kv_lens, T, B, Hq, Hkv, D, page, num_pages, table_width,  \
+                                max_q_len, BF16, stream);                                                              \
+  }
+MQ_ROPE_APPEND(mq_kv8_rope_append, false)
+MQ_ROPE_APPEND(mq_kv8_rope_append_bf16, true)
+#undef MQ_ROPE_APPEND
+
+static bool verify_sizes(int64_t T, int64_t B, int64_t V, int64_t max_q_len) {
+  return T >= 0 && T <= (int64_t{1} << 26) && B >= 0 && B <= 65535 && V >= 1 && V <= (int64_t{1} << 24) &&
+         max_q_len >= 1 && max_q_len <= mq::kKv8MaxTree;
+}
+
+size_t mq_draft_verify_workspace_bytes(int64_t B, int64_t V, int64_t max_q_len) {
+  return verify_sizes(0, B, V, max_q_len) ? mq::verify_workspace(static_cast<int>(B), static_cast<int>(V), static_cast<int>(max_q_len)) : 0;
+}
+
+mq_status mq_draft_verify(const float* probs, const float* draft_probs, const int32_t* tokens, const int32_t* parents,
+                          const float* uniform, const int32_t* cu_q, int32_t* kept, int32_t* path, int32_t* next_token,
+                          int64_t T, int64_t B, int64_t V, int64_t max_q_len, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  if (!verify_sizes(T, B, V, max_q_len))
+    return fail(MQ_ERR_SHAPE, "T=%lld, B=%lld, V=%lld or max_q_len=%lld out of range", (long long)T, (long long)B,
+                (long long)V, (long long)max_q_len);
+  if (draft_probs && parents)
+    return fail(MQ_ERR_UNSUPPORTED, "draft_probs goes with chains: a tree's drafts are taken as given (no parents, or no draft_probs)");
+  MQ_TRY(need(probs, T, "probs"));
+  MQ_TRY(need(tokens, T, "tokens"));
+  MQ_TRY(need(uniform, T, "uniform"));
+  MQ_TRY(need(cu_q, B, "cu_q"));
+  MQ_TRY(need(kept, B, "kept"));
+  MQ_TRY(need(path, B, "path"));
+  MQ_TRY(need(next_token, B, "next_token"));
+  for (const void* p : {static_cast<const void*>(probs), static_cast<const void*>(draft_probs), static_cast<const void*>(tokens),
+                        static_cast<const void*>(parents), static_cast<const void*>(uniform), static_cast<const void*>(cu_q),
+                        static_cast<const void*>(kept), static_cast<const void*>(path), static_cast<const void*>(next_token)})
+    if (!aligned(p, 4)) return fail(MQ_ERR_ALIGN, "all pointers must be 4-byte aligned");
+  const size_t ws = B ? mq_draft_verify_workspace_bytes(B, V, max_q_len) : 0;
+  MQ_TRY(check_workspace(workspace, workspace_bytes, ws));
+  const size_t rows = static_cast<size_t>(T) * V * 4, t = static_cast<size_t>(T) * 4, b = static_cast<size_t>(B) * 4;
+  const Range in[] = {{probs, rows, "probs"},
+                      {draft_probs, draft_probs ? rows : 0, "draft_probs"},
+                      {tokens, t, "tokens"},
+                      {parents, parents ? t : 0, "parents"},
+                      {uniform, t, "uniform"},
+                      {cu_q, b + 4, "cu_q"}};
+  const Range out[] = {{kept, b, "kept"}, {path, b * max_q_len, "path"}, {next_token, b, "next_token"}, {ws ? workspace : nullptr, ws, "workspace"}};
+  MQ_TRY(check_alias(in, out));
+  if (B == 0) return ok();
+  mq::VerifyArgs a = {};
+  a.probs = probs;
+  a.draft = draft_probs;
+  a.token = tokens;
+  a.parents = parents;
+  a.uniform = uniform;
+  a.cu = cu_q;
+  a.kept = kept;
+  a.path = path;
+  a.next = next_token;
+  a.tokens = static_cast<int>(T);
+  a.vocab = static_cast<int>(V);
+  a.max_q_len = static_cast<int>(max_q_len);
+  return hip_status(mq::launch_draft_verify(a, static_cast<int>(B), workspace, as_stream(stream)), "draft_verify launch");
 }
 
 }  // extern "C"

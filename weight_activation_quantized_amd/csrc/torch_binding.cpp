@@ -1,5 +1,5 @@
-// Native half of the Python wrappers of the RMS norm, e4m3 and KV-cache entry
-// points: the checks of the tensors' metadata, the outputs' allocation and the
+// Native half of the Python wrappers of the RMS norm, e4m3, KV-cache and drafted
+// tokens' entry points: the checks of the tensors' metadata, the outputs' allocation and the
 // call into libmq, which in Python cost 12-21 us a call, several times what
 // the smaller kernels take. Same checks, messages and exceptions as the
 // wrappers written in Python; the computation is libmq's alone.
@@ -21,6 +21,7 @@
 #include <cstdio>
 #include <cstring>
 #include <string>
+#include <vector>
 
 #include "mq.h"
 
@@ -37,6 +38,13 @@ struct Library {
   decltype(&mq_kv8_append) kv8_append[2];
   decltype(&mq_kv8_attention_workspace_bytes) kv8_attention_workspace_bytes;
   decltype(&mq_kv8_attention) kv8_attention[2];
+  decltype(&mq_kv8_rope_append) kv8_rope_append[2];
+  decltype(&mq_kv8_tree_mask) kv8_tree_mask;
+  decltype(&mq_kv8_tree_attention_workspace_bytes) kv8_tree_attention_workspace_bytes;
+  decltype(&mq_kv8_tree_attention) kv8_tree_attention[2];
+  decltype(&mq_draft_verify_workspace_bytes) draft_verify_workspace_bytes;
+  decltype(&mq_draft_verify) draft_verify;
+  decltype(&mq_kv8_tree_keep) kv8_tree_keep;
 } lib;
 
 PyObject* check_fn = nullptr;  // the package's _check(status): raises MqError
@@ -401,6 +409,196 @@ PyObject* kv8_attention(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// cu_q [B + 1] and kv_lens [B].
+int64_t sequences(const at::Tensor& cu, const at::Tensor& lens) {
+  if (cu.size(0) < 1 || lens.size(0) != cu.size(0) - 1) value_error("cu_q must be [B + 1] and kv_lens [B]");
+  same_device(cu, lens);
+  return lens.size(0);
+}
+
+// (q, k, v, the cache's seven, max_q_len, cos_sin, positions, q_weight, k_weight, eps, interleaved, out)
+PyObject* kv8_rope_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  MQ_ARGS(18)
+  const at::ScalarType dt = half_dtype(a[0], "q");
+  const Cache c = kv8_cache(a + 3);
+  const at::Tensor &q = any_tensor(a[0], "q"), &k = any_tensor(a[1], "k"), &v = any_tensor(a[2], "v");
+  const int64_t qs = kv8_rows(q, "q", dt, c.D), ks = kv8_rows(k, "k", dt, c.D), vs = kv8_rows(v, "v", dt, c.D);
+  const int64_t T = q.size(0), Hq = q.size(1), most = integer(a[10], "max_q_len");
+  if (k.sizes() != v.sizes() || k.size(1) != c.H || k.size(0) != T)
+    value_error("q must be [T, Hq, D] and k and v [T, Hkv, D]");
+  const at::Tensor& cs = tensor(a[11], "cos_sin", at::kFloat, 2);
+  const int32_t* positions = nullptr;
+  if (a[12] != Py_None) {
+    const at::Tensor& p = tensor(a[12], "positions", at::kInt, 1);
+    if (p.size(0) != T) value_error("positions must be [T]");
+    same_device(c.k, p);
+    positions = data<int32_t>(p);
+  }
+  const uint16_t* weights[2] = {nullptr, nullptr};
+  if ((a[13] == Py_None) != (a[14] == Py_None)) value_error("q_weight and k_weight go together");
+  for (int i = 0; i < 2 && a[13] != Py_None; ++i) {
+    const at::Tensor& w = tensor(a[13 + i], i ? "k_weight" : "q_weight", dt, 1);
+    if (w.size(0) != c.D) value_error("q_weight and k_weight must be [D]");
+    same_device(c.k, w);
+    weights[i] = data<uint16_t>(w);
+  }
+  const double eps = number(a[15], "eps");
+  for (const at::Tensor* t : {&q, &k, &v, &cs}) same_device(c.k, *t);
+  const c10::DeviceGuard guard(c.k.device());
+  at::Tensor o;
+  int64_t os = Hq * c.D;
+  if (a[17] == Py_None) {
+    o = at::empty({T, Hq, c.D}, at::TensorOptions().dtype(dt).device(q.device()));
+  } else {
+    o = any_tensor(a[17], "out");
+    os = kv8_rows(o, "out", dt, c.D);
+    if (o.sizes() != q.sizes()) value_error("out must have q's shape");
+    same_device(c.k, o);
+  }
+  if (!passed(lib.kv8_rope_append[dt == at::kBFloat16](
+          data<uint16_t>(q), data<uint16_t>(k), data<uint16_t>(v), qs, ks, vs, data<uint16_t>(o), os, data<float>(cs),
+          positions, weights[0], weights[1], eps, cs.size(0), cs.size(1), a[16] == Py_True, data<uint8_t>(c.k),
+          data<uint8_t>(c.v), data<float>(c.ks), data<float>(c.vs), data<int32_t>(c.table), data<int32_t>(c.cu),
+          data<int32_t>(c.lens), T, c.B, Hq, c.H, c.D, c.page, c.P, c.width, most, stream_of(c.k))))
+    return nullptr;
+  return THPVariable_Wrap(std::move(o));
+  END_HANDLE_TH_ERRORS
+}
+
+// (parents, cu_q, kv_lens, max_q_len, mask, positions)
+PyObject* kv8_tree_mask(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  MQ_ARGS(6)
+  const at::Tensor& parents = tensor(a[0], "parents", at::kInt, 1);
+  const at::Tensor &cu = tensor(a[1], "cu_q", at::kInt, 1), &lens = tensor(a[2], "kv_lens", at::kInt, 1);
+  const int64_t T = parents.size(0), B = sequences(cu, lens), most = integer(a[3], "max_q_len");
+  if (most < 1 || most > 1024) value_error("max_q_len must lie in [1, 1024]");
+  same_device(parents, cu);
+  const c10::DeviceGuard guard(parents.device());
+  at::Tensor mask = output(a[4], "mask", {T, (most + 31) / 32}, at::kInt, parents);
+  at::Tensor positions = output(a[5], "positions", {T}, at::kInt, parents);
+  if (!passed(lib.kv8_tree_mask(data<int32_t>(parents), data<int32_t>(cu), data<int32_t>(lens), data<int32_t>(mask),
+                                data<int32_t>(positions), T, B, mask.size(1), most, stream_of(parents))))
+    return nullptr;
+  PyObject* r = PyTuple_New(2);
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(mask)));
+  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(positions)));
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, tree, the cache's seven, max_q_len, softmax_scale, out, workspace)
+PyObject* kv8_tree_attention(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  MQ_ARGS(13)
+  const at::ScalarType dt = half_dtype(a[0], "q");
+  const at::Tensor& tree = tensor(a[1], "tree", at::kInt, 2);
+  const Cache c = kv8_cache(a + 2);
+  const at::Tensor& q = any_tensor(a[0], "q");
+  const int64_t qs = kv8_rows(q, "q", dt, c.D);
+  const int64_t T = q.size(0), Hq = q.size(1), most = integer(a[9], "max_q_len");
+  if (tree.size(0) != T) value_error("tree must be [T, words]");
+  const float scale = static_cast<float>(a[10] == Py_None ? 1.0 / std::sqrt(static_cast<double>(c.D))
+                                                          : number(a[10], "softmax_scale"));
+  same_device(q, c.k);
+  same_device(q, tree);
+  const c10::DeviceGuard guard(q.device());
+  at::Tensor o = output(a[11], "out", {T, Hq, c.D}, dt, q);
+  const Workspace w =
+      workspace(a[12], lib.kv8_tree_attention_workspace_bytes(T, c.B, Hq, c.H, c.D, c.page, c.width, most), q);
+  if (!passed(lib.kv8_tree_attention[dt == at::kBFloat16](
+          data<uint16_t>(q), qs, data<int32_t>(tree), tree.size(1), data<uint8_t>(c.k), data<uint8_t>(c.v),
+          data<float>(c.ks), data<float>(c.vs), data<int32_t>(c.table), data<int32_t>(c.cu), data<int32_t>(c.lens),
+          data<uint16_t>(o), T, c.B, Hq, c.H, c.D, c.page, c.P, c.width, most, scale, w.p, w.bytes, stream_of(q))))
+    return nullptr;
+  return THPVariable_Wrap(std::move(o));
+  END_HANDLE_TH_ERRORS
+}
+
+// (probs, tokens, uniform, cu_q, max_q_len, parents, draft_probs, kept, path, next_token, workspace)
+PyObject* draft_verify(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  MQ_ARGS(11)
+  const at::Tensor& probs = tensor(a[0], "probs", at::kFloat, 2);
+  const at::Tensor &tokens = tensor(a[1], "tokens", at::kInt, 1), &uniform = tensor(a[2], "uniform", at::kFloat, 1);
+  const at::Tensor& cu = tensor(a[3], "cu_q", at::kInt, 1);
+  const int64_t T = probs.size(0), V = probs.size(1), B = cu.size(0) - 1, most = integer(a[4], "max_q_len");
+  if (tokens.size(0) != T || uniform.size(0) != T || B < 0)
+    value_error("probs must be [T, V], tokens and uniform [T], cu_q [B + 1]");
+  if (most < 1 || most > 1024) value_error("max_q_len must lie in [1, 1024]");
+  const int32_t* parents = nullptr;
+  if (a[5] != Py_None) {
+    const at::Tensor& p = tensor(a[5], "parents", at::kInt, 1);
+    if (p.size(0) != T) value_error("parents must be [T]");
+    same_device(probs, p);
+    parents = data<int32_t>(p);
+  }
+  const float* draft = nullptr;
+  if (a[6] != Py_None) {
+    if (parents) value_error("draft_probs goes with chains: give parents or draft_probs");
+    const at::Tensor& d = tensor(a[6], "draft_probs", at::kFloat, 2);
+    if (d.sizes() != probs.sizes()) value_error("draft_probs must have probs' shape");
+    same_device(probs, d);
+    draft = data<float>(d);
+  }
+  for (const at::Tensor* t : {&tokens, &uniform, &cu}) same_device(probs, *t);
+  const c10::DeviceGuard guard(probs.device());
+  at::Tensor kept = output(a[7], "kept", {B}, at::kInt, probs), path = output(a[8], "path", {B, most}, at::kInt, probs);
+  at::Tensor next = output(a[9], "next_token", {B}, at::kInt, probs);
+  const Workspace w = workspace(a[10], B ? lib.draft_verify_workspace_bytes(B, V, most) : 0, probs);
+  if (!passed(lib.draft_verify(data<float>(probs), draft, data<int32_t>(tokens), parents, data<float>(uniform),
+                               data<int32_t>(cu), data<int32_t>(kept), data<int32_t>(path), data<int32_t>(next), T, B,
+                               V, most, w.p, w.bytes, stream_of(probs))))
+    return nullptr;
+  PyObject* r = PyTuple_New(3);
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(std::move(kept)));
+  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(std::move(path)));
+  PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(std::move(next)));
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
+// (k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, path, kept): the caches of one layer or, with one
+// dimension more, of several
+PyObject* kv8_tree_keep(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  MQ_ARGS(9)
+  const int64_t more = any_tensor(a[0], "k_cache").dim() == 5;
+  const at::Tensor &k = tensor(a[0], "k_cache", at::kFloat8_e4m3fn, 4 + more),
+                   &v = tensor(a[1], "v_cache", at::kFloat8_e4m3fn, 4 + more);
+  const at::Tensor &ks = tensor(a[2], "k_scales", at::kFloat, 2 + more), &vs = tensor(a[3], "v_scales", at::kFloat, 2 + more);
+  const at::Tensor& table = tensor(a[4], "block_table", at::kInt, 2);
+  const at::Tensor &cu = tensor(a[5], "cu_q", at::kInt, 1), &lens = tensor(a[6], "kv_lens", at::kInt, 1);
+  const at::Tensor &path = tensor(a[7], "path", at::kInt, 2), &kept = tensor(a[8], "kept", at::kInt, 1);
+  const int64_t layers = more ? k.size(0) : 1, P = k.size(more), H = k.size(more + 1), page = k.size(more + 2),
+                D = k.size(more + 3);
+  const int64_t lead[2] = {layers, P};
+  const at::IntArrayRef front(lead + 1 - more, 1 + more);
+  auto shape = [&](std::initializer_list<int64_t> tail) {
+    std::vector<int64_t> all(front.begin(), front.end());
+    all.insert(all.end(), tail);
+    return all;
+  };
+  if (v.sizes() != at::IntArrayRef(shape({H, D, page})))
+    value_error("k_cache must be [(layers,) P, Hkv, page, D] and v_cache [(layers,) P, Hkv, D, page]");
+  if (ks.sizes() != at::IntArrayRef(shape({H})) || vs.sizes() != ks.sizes())
+    value_error("k_scales and v_scales must be [(layers,) P, Hkv]");
+  const int64_t B = sequences(cu, lens);
+  if (table.size(0) != B || path.size(0) != B || kept.size(0) != B)
+    value_error("block_table must be [B, width], path [B, nodes] and kept [B]");
+  for (const at::Tensor* t : {&v, &ks, &vs, &table, &cu, &path, &kept}) same_device(k, *t);
+  const c10::DeviceGuard guard(k.device());
+  if (!passed(lib.kv8_tree_keep(data<uint8_t>(k), data<uint8_t>(v), data<float>(ks), data<float>(vs), data<int32_t>(table),
+                                data<int32_t>(cu), data<int32_t>(lens), data<int32_t>(path), data<int32_t>(kept), layers,
+                                B, H, D, page, P, table.size(1), path.size(1), stream_of(k))))
+    return nullptr;
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 // bind(addresses in the order of Library, check): once, when the package loads libmq.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   MQ_ARGS(2)
@@ -428,7 +626,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
 #define MQ_METHOD(NAME) {#NAME, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(NAME)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {MQ_METHOD(bind),       MQ_METHOD(rmsnorm),    MQ_METHOD(quant_fp8_blocks),
                          MQ_METHOD(fp8_block_mm), MQ_METHOD(fp8_linear), MQ_METHOD(kv8_append),
-                         MQ_METHOD(kv8_attention), {nullptr, nullptr, 0, nullptr}};
+                         MQ_METHOD(kv8_attention), MQ_METHOD(kv8_rope_append), MQ_METHOD(kv8_tree_mask),
+                         MQ_METHOD(kv8_tree_attention), MQ_METHOD(draft_verify), MQ_METHOD(kv8_tree_keep), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mq_torch", "Native half of the package's torch wrappers.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
