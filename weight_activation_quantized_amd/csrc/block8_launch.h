@@ -92,6 +92,7 @@ struct Kv8Plan {
   int waves;    // wavefronts of a workgroup
   int splits;
   int64_t prompt_blocks;  // workgroups of the other form (under 2^29 within the entry's limits)
+  int least;              // (of trees) tiles of keys that such a workgroup takes at least
   size_t workspace_bytes;
 };
 Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads);

@@ -41,72 +41,10 @@
 
 #include "block8_launch.h"
 #include "device_common.h"
+#include "kv8_attention.h"
 
 namespace mq {
 namespace {
-
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kNegInf = -__builtin_inff();
-// Scales outside what the append writes would carry sums out of binary32.
-constexpr float kMinScale = 0x1p-100f, kMaxScale = 0x1p120f;
-// What the decode form's weights are raised by, as an exponent and as the
-// factor that takes it back.
-constexpr float kRaise = 15.f, kLower = 0x1p-15f;
-
-typedef float f32x8 __attribute__((ext_vector_type(8)));
-
-// 8 e4m3 codes as 8 fp16 or bf16 values (exact).
-template <bool kBf16>
-__device__ __forceinline__ f16x8 widen(uint32_t lo, uint32_t hi) {
-  if constexpr (kBf16) {
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
-    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
-    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
-    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
-    const u32x4 w = {__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
-                     __builtin_bit_cast(uint32_t, d)};
-    return __builtin_bit_cast(f16x8, w);
-  } else {
-    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false);
-    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true);
-    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false);
-    const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true);
-    return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-  }
-}
-
-__device__ __forceinline__ f16x8 to_f16(f32x8 v) { return __builtin_convertvector(v, f16x8); }
-
-// 16 codes of which only the first n count: the others become 0.
-__device__ __forceinline__ u32x4 first_bytes(u32x4 v, int n) {
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const int k = n - 4 * w;
-    v[w] = k >= 4 ? v[w] : k <= 0 ? 0u : v[w] & ((1u << (8 * k)) - 1u);
-  }
-  return v;
-}
-
-__device__ __forceinline__ float held_scale(float s) { return fminf(fmaxf(s, kMinScale), kMaxScale); }
-// The logarithm of a held scale; a NaN, which held_scale hides, stays one here.
-__device__ __forceinline__ float log_scale(float s) {
-  const float l = __builtin_amdgcn_logf(held_scale(s));
-  return s == s ? l : s;
-}
-
-// A sequence as the kernels see it.
-struct Seq {
-  int row0, n, len, seen;  // first row, new tokens, tokens, tokens that the table can hold
-};
-
-__device__ __forceinline__ Seq sequence(const Kv8Cache& c, int b) {
-  Seq s;
-  s.row0 = max(c.cu[b], 0);
-  s.n = max(min(min(c.cu[b + 1], c.tokens) - s.row0, c.max_q_len), 0);
-  s.len = c.lens[b];
-  s.seen = static_cast<int>(min(static_cast<int64_t>(max(s.len, 0)), static_cast<int64_t>(c.table_width) * c.page));
-  return s;
-}
 
 // Tiles of 64 keys that split `z` of `splits` takes of a sequence: [first,
 // first + count). Every split gets the same number, at least `least`.
@@ -120,45 +58,6 @@ __device__ __forceinline__ Span tiles_of(int tiles, int splits, int z, int least
   s.end = min(s.first + per, tiles);
   return s;
 }
-
-// Which of the 16 keys from new token `at` on (negative: before the new ones,
-// where all are seen) a row's words name, the first in the lowest bit.
-__device__ __forceinline__ uint32_t tree_bits(const int32_t* words, int count, int at) {
-  if (at <= -16) return 0xffffu;
-  const int k = at >> 5;
-  const uint32_t lo = k < 0 ? 0xffffffffu : k < count ? static_cast<uint32_t>(words[k]) : 0u;
-  const uint32_t hi = k + 1 < count ? static_cast<uint32_t>(words[k + 1]) : 0u;
-  return static_cast<uint32_t>((static_cast<uint64_t>(hi) << 32 | lo) >> (at & 31)) & 0xffffu;
-}
-__device__ __forceinline__ uint32_t first_bits(int n) { return n >= 16 ? 0xffffu : n <= 0 ? 0u : (1u << n) - 1u; }
-
-// Of 16 codes the NaN ones become 0 in v; returned are codes of 1 where they were.
-__device__ __forceinline__ u32x4 take_nan(u32x4& v) {
-  u32x4 ones;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const uint32_t nan = (((v[w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
-    v[w] &= ~(nan * 0xffu);
-    ones[w] = nan * 0x38u;
-  }
-  return ones;
-}
-__device__ __forceinline__ bool has_any(u32x4 v) { return (v[0] | v[1] | v[2] | v[3]) != 0; }
-
-// 8 fp16 values, 1 where the bit is set.
-__device__ __forceinline__ f16x8 ones_of(uint32_t bits) {
-  f16x8 v;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = (bits >> e) & 1 ? static_cast<f16>(1.f) : static_cast<f16>(0.f);
-  return v;
-}
-
-// The workspace of a split call: for every split and row (token, head) its
-// maximum and sum, then its unnormalised output.
-struct Parts {
-  float* ml;  // [splits, rows, 2]
-  float* o;   // [splits, rows, head_dim]
-};
 
 // ---------------------------------------------------------------------------
 // Decode: the rows of one kv head (its query heads times the new tokens) stand
@@ -431,6 +330,7 @@ __global__ __launch_bounds__(64 * kWaves) void kv8_decode_kernel(Kv8Cache c, con
 // ---------------------------------------------------------------------------
 
 constexpr int kMaxSplits = 64;
+constexpr int kPromptRows = 256;  // rows of a row tile of prompts
 
 template <int D, bool kBf16>
 __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __restrict__ out, Parts parts, int heads,
@@ -478,6 +378,58 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
   for (int e = 0; e < kE; e += 2) to[e / 2] = half_bits<kBf16>(v[e]) | (static_cast<uint32_t>(half_bits<kBf16>(v[e + 1])) << 16);
 }
 
+// The same for shared-out trees: D / 4 lanes take a row, whose parts, eight at a
+// time, and their maxima and sums are all requested at once (an empty share's are
+// zeros).
+template <int D, bool kBf16>
+__global__ __launch_bounds__(256) void kv8_tree_join_kernel(Kv8Cache c, uint16_t* __restrict__ out, Parts parts,
+                                                            int heads) {
+  constexpr int kLanes = D / 4, kRowsOf = 256 / kLanes;
+  const size_t rows = static_cast<size_t>(c.tokens) * heads;
+  const size_t row = static_cast<size_t>(blockIdx.x) * kRowsOf + threadIdx.x / kLanes;
+  if (row >= rows) return;
+  const int token = static_cast<int>(row / heads);
+  const u32x2 where = parts.where[row];
+  if (token < c.cu[0] || token >= c.cu[c.batch]) return;
+  const size_t step = static_cast<size_t>(c.kv_heads) * kPromptRows;
+  const int splits = static_cast<int>(where[1]);
+  // (one share: written already; more than there are: cu_q and max_q_len do not fit)
+  if (splits < 2 || splits > kMaxSplits || where[0] + (splits - 1) * step >= parts.rows) return;
+  const int d = 4 * (static_cast<int>(threadIdx.x) % kLanes);
+  float m = kNegInf, total = 0.f;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int z0 = 0; z0 < splits; z0 += 8) {
+    f32x2 ml[8];
+    f32x4 p[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const size_t at = where[0] + min(z0 + u, splits - 1) * step;
+      ml[u] = *reinterpret_cast<const f32x2*>(parts.ml + 2 * at);
+      p[u] = *reinterpret_cast<const f32x4*>(parts.o + at * D + d);
+    }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) top = fmaxf(top, ml[u][0]);
+    const float from = top == kNegInf ? 0.f : top, old = __builtin_amdgcn_exp2f(m - from);
+    m = top;
+    total *= old;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] *= old;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (z0 + u >= splits) continue;
+      const float f = __builtin_amdgcn_exp2f(ml[u][0] - from);
+      total = fmaf(ml[u][1], f, total);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = fmaf(p[u][e], f, v[e]);
+    }
+  }
+  const float inv = total == 0.f ? 0.f : 1.f / total;  // (a NaN stays one)
+  const uint32_t lo = half_bits<kBf16>(v[0] * inv) | (static_cast<uint32_t>(half_bits<kBf16>(v[1] * inv)) << 16);
+  const uint32_t hi = half_bits<kBf16>(v[2] * inv) | (static_cast<uint32_t>(half_bits<kBf16>(v[3] * inv)) << 16);
+  *reinterpret_cast<u32x2*>(out + row * D + d) = u32x2{lo, hi};
+}
+
 // ---------------------------------------------------------------------------
 // Prompts: a workgroup of eight wavefronts takes 256 rows of one kv head (the
 // query heads of the group side by side, so that one K/V tile serves all of
@@ -518,22 +470,6 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
 // of the softmax behind the products.
 // ---------------------------------------------------------------------------
 
-typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-
-constexpr float kLazy = 4.f, kLazyRaise = kRaise - kLazy, kLazyLower = 0x1p-11f;
-
-// The larger of x in lanes l and l ^ 32, in both: the swap leaves the lower
-// half's values in one register and the upper half's in the other. (Written
-// out: the compiler drops the second result of the builtin.)
-__device__ __forceinline__ float halves_max(float x) {
-  float lower = x, upper = x;
-  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\ts_nop 1" : "+v"(lower), "+v"(upper));
-  return fmaxf(lower, upper);
-}
-
-constexpr int kPromptRows = 256;  // rows of a row tile
-
 // The n-th row tile of the call: its sequence (-1: there are fewer) and its
 // number within it. Every wavefront counts the sequences' tiles, 64 sequences
 // at a time, so that the workgroups that have work are the first of the grid:
@@ -564,10 +500,104 @@ __device__ __forceinline__ RowTile row_tile(const Kv8Cache& c, int group, int n)
   return {-1, 0};
 }
 
+// ---------------------------------------------------------------------------
+// Shares of trees. Sequences' lengths are known on the GPU only, and a prompt
+// workgroup has its compute unit to itself: with the keys of every sequence in
+// the same number of splits, the longest sequence's take as long as they are and
+// the others' units wait. So trees are shared out there: `per` tiles of 64 keys a
+// share, the fewest with which all shares, sum ceil(tiles / per) over row tiles and
+// kv heads, are at most `target`; each sequence's keys are cut evenly into
+// ceil(tiles / per). Every workgroup finds its own share by that count, the
+// joining kernel those of its rows where the first share left them. (8 trees of up
+// to 64 nodes over up to 8192 keys, 32 query heads on 8 of 128: 72 us; every
+// sequence in four splits 86.)
+// ---------------------------------------------------------------------------
+
+// Sum over this lane and those before it.
+__device__ __forceinline__ int wave_prefix(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15: rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31: rows 2 and 3
+  return v;
+}
+__device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
+
+struct Shares {
+  int target, least;  // workgroups at most, tiles of a share at least
+};
+
+// Row tiles and tiles of keys of sequence b (0 and 0 behind the last one).
+__device__ __forceinline__ void extent(const Kv8Cache& c, int group, int b, int& row_tiles, int& tiles) {
+  row_tiles = tiles = 0;
+  if (b >= c.batch) return;
+  const Seq s = sequence(c, b);
+  row_tiles = (s.n * group + kPromptRows - 1) / kPromptRows;
+  tiles = (s.seen + 63) / 64;
+}
+
+__device__ __forceinline__ int splits_of(int tiles, int per) { return min(max((tiles + per - 1) / per, 1), kMaxSplits); }
+
+// Tiles of a share. W = work, R = shares if nothing is split: W / (target - R)
+// tiles are always enough; for up to 64 sequences fewer are tried first. (In
+// binary32, which all workgroups of both kernels form alike; up by more than its
+// errors.)
+__device__ __forceinline__ int per_share(const Kv8Cache& c, const Shares& w, int group) {
+  const int lane = threadIdx.x & 63;
+  float work = 0.f;
+  int rows = 0, rt, tiles;
+  for (int b0 = 0; b0 < c.batch; b0 += 64) {
+    extent(c, group, b0 + lane, rt, tiles);
+    float sum = static_cast<float>(rt) * static_cast<float>(tiles);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, kWave);
+    work += sum;
+    rows += last_lane(wave_prefix(rt));
+  }
+  work *= static_cast<float>(c.kv_heads) * 1.0001f;
+  const float least = static_cast<float>(w.least);
+  if (c.batch <= 64) {
+    const int room = w.target / c.kv_heads;  // shares of one head
+    int per = static_cast<int>(fmaxf(fminf(work / static_cast<float>(w.target), 0x1p26f) + 1.f, least));
+    for (int step = 0; step < 16; ++step) {
+      const int used = last_lane(wave_prefix(rt * splits_of(tiles, per)));
+      if (used <= room) return per;
+      per += max(per * (used - room) / (2 * max(room, 1)), 1);
+    }
+  }
+  const float room = static_cast<float>(max(static_cast<int64_t>(w.target) - static_cast<int64_t>(rows) * c.kv_heads, int64_t{1}));
+  return static_cast<int>(fmaxf(fminf(work / room, 0x1p26f) + 1.f, least));
+}
+
+struct Share {
+  int b, rt, split, splits;  // b < 0: there is none
+};
+
+// The n-th share (of one kv head).
+__device__ __forceinline__ Share find_share(const Kv8Cache& c, int group, int per, int n) {
+  const int lane = threadIdx.x & 63;
+  for (int b0 = 0; b0 < c.batch; b0 += 64) {
+    int rt, tiles;
+    extent(c, group, b0 + lane, rt, tiles);
+    const int splits = splits_of(tiles, per), sum = wave_prefix(rt * splits);
+    const uint64_t behind = __ballot(sum > n);
+    if (behind) {
+      const int at = __builtin_ctzll(behind);
+      const int s = __builtin_amdgcn_readlane(splits, at);
+      const int local = n - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(rt, at) * s);
+      return {b0 + at, local / s, local % s, s};
+    }
+    n -= last_lane(sum);
+  }
+  return {-1, 0, 0, 1};
+}
+
 template <int D, bool kBf16, bool kTree>
 __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint16_t* __restrict__ q, int64_t q_stride,
                                                          uint16_t* __restrict__ out, Parts parts, int group,
-                                                         int splits, float scale_log2, Kv8Tree tree) {
+                                                         int splits, float scale_log2, Kv8Tree tree, Shares shares) {
   constexpr int kRows = kPromptRows, kKs = D / 16, kDt = D / 32;
   constexpr int kKRow = 2 * D;  // bytes of a widened K row
   constexpr int kKBytes = 64 * kKRow, kVBytes = D * 128;
@@ -583,8 +613,18 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
   unsigned at = blockIdx.y * gridDim.x + blockIdx.x;
   const int head = static_cast<int>(at % c.kv_heads);
   at /= c.kv_heads;
-  const int split = static_cast<int>(at % splits);  // (few: prompts that need splits have few row tiles)
-  const RowTile tile = row_tile(c, group, static_cast<int>(at / splits));
+  const int slot = static_cast<int>(blockIdx.y * gridDim.x + blockIdx.x);  // (of trees) its part in the workspace
+  int split;
+  RowTile tile;
+  if constexpr (kTree) {
+    const Share share = find_share(c, group, per_share(c, shares, group), static_cast<int>(at));
+    tile = {share.b, share.rt};
+    split = share.split;
+    splits = share.splits;
+  } else {
+    split = static_cast<int>(at % splits);  // (few: prompts that need splits have few row tiles)
+    tile = row_tile(c, group, static_cast<int>(at / splits));
+  }
   if (tile.b < 0) return;
   const int b = tile.b, rt = tile.rt;
   const Seq seq = sequence(c, b);
@@ -597,6 +637,8 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 
   const int r = kRows * rt + 32 * wave + i;
   const bool live = r < rows;
+  // (of trees, whose rows often leave some wavefronts none: those only fill)
+  const bool works = !kTree || kRows * rt + 32 * wave < rows;
   const int tq = live ? r / group : 0, g = live ? r - tq * group : 0;
   const int limit = live ? min(seq.len - seq.n + tq, seq.seen - 1) : -1;  // last key the row sees
   const uint16_t* const qrow = q + static_cast<int64_t>(seq.row0 + tq) * q_stride + (head * group + g) * D;
@@ -613,7 +655,7 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
       kTree ? seq.seen - 1 : min(seq.len - seq.n + last_t, seq.seen - 1));  // the last key
   const int start = __builtin_amdgcn_readfirstlane(seq.len - seq.n);        // the first new token
   const int32_t* const words = kTree ? tree.mask + static_cast<int64_t>(seq.row0 + tq) * tree.words : nullptr;
-  const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, 2);
+  const Span span = tiles_of(top < 0 ? 0 : top / 64 + 1, splits, split, kTree ? 1 : 2);
   const int first = __builtin_amdgcn_readfirstlane(span.first);
   const int tiles = __builtin_amdgcn_readfirstlane(span.end - span.first);
 
@@ -868,13 +910,19 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
         vs1 = c.v_scales[unit(id1)];
       }
       __builtin_amdgcn_s_setprio(1);  // its MFMAs go before the other half's vector work
-      products(j, batch, std::true_type{});
+      if (works) {
+        products(j, batch, std::true_type{});
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) stage(j + 1, e);
+        fetch(j + 2, batch);
+      }
       __builtin_amdgcn_s_setprio(0);
       phase_end();
-      softmax(j);
+      if (works) softmax(j);
       phase_end();
     }
-    products(tiles, 0, std::false_type{});
+    if (works) products(tiles, 0, std::false_type{});
     if (half == 0) phase_end();  // the second half's last softmax phase
     if constexpr (kTree) {
       // (rare, and on its own: those tiles' codes once more, from memory)
@@ -902,6 +950,12 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 
   l += __shfl_xor(l, 32, kWave);
   if (!live) return;
+  if constexpr (kTree) {
+    // where the joining kernel finds the row's parts
+    if (parts.where && split == 0 && h == 0)
+      parts.where[static_cast<size_t>(seq.row0 + tq) * heads + head * group + g] =
+          u32x2{static_cast<uint32_t>(slot) * kRows + 32 * wave + i, static_cast<uint32_t>(splits)};
+  }
 #pragma unroll
   for (int d = 0; d < kDt; ++d)
 #pragma unroll
@@ -919,7 +973,8 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
         *reinterpret_cast<u32x2*>(out + to * D + 32 * d + 8 * e + 4 * h) = u32x2{b4[0] | (b4[1] << 16), b4[2] | (b4[3] << 16)};
       }
   } else {
-    const size_t at = static_cast<size_t>(split) * c.tokens * heads + to;
+    const size_t at = kTree ? static_cast<size_t>(slot) * kRows + 32 * wave + i
+                            : static_cast<size_t>(split) * c.tokens * heads + to;
 #pragma unroll
     for (int d = 0; d < kDt; ++d)
 #pragma unroll
@@ -940,6 +995,9 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 // prompt form, whatever their number.
 constexpr int kDecodeRows = 64;
 constexpr int64_t kDecodeTiles = 24576;
+// Shares of a tree's call: one workgroup per compute unit (the case above: 384
+// shares 95 us, 512 85).
+constexpr int64_t kTreeShares = 256;
 
 template <int D, bool kBf16, bool kTree>
 hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, const Kv8Tree& tree, uint16_t* out,
@@ -948,11 +1006,16 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, co
   const int most = c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
   const int64_t rows = static_cast<int64_t>(most) * group, all = static_cast<int64_t>(c.tokens) * q_heads;
   const float scale_log2 = scale * kLog2e;
-  Parts parts = {nullptr, nullptr};
-  if (plan.splits > 1) {
+  Parts parts = {};
+  const bool shared = kTree && !plan.decode;  // out by the workgroups themselves
+  if (workspace) {
+    const int64_t part_rows = shared ? plan.prompt_blocks * kPromptRows : plan.splits * all;
     parts.o = static_cast<float*>(workspace);
-    parts.ml = parts.o + plan.splits * all * D;
+    parts.ml = parts.o + part_rows * D;
+    parts.rows = part_rows;
+    if (shared) parts.where = reinterpret_cast<u32x2*>(parts.ml + part_rows * 2);
   }
+  const Shares shares = {static_cast<int>(plan.prompt_blocks), plan.least};
   hipError_t e;
   if (plan.decode) {
     const int row_tiles = static_cast<int>((rows + 15) / 16);
@@ -967,11 +1030,16 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, co
     const dim3 grid(static_cast<uint32_t>(plan.prompt_blocks < kWide ? plan.prompt_blocks : kWide),
                     static_cast<uint32_t>((plan.prompt_blocks + kWide - 1) / kWide));
     e = launch_kernel(kv8_prompt_kernel<D, kBf16, kTree>, grid, dim3(512), 0, stream, c, q, q_stride, out, parts, group,
-                      plan.splits, scale_log2, tree);
+                      plan.splits, scale_log2, tree, shares);
   }
-  if (e != hipSuccess || plan.splits == 1) return e;
-  return launch_kernel(kv8_join_kernel<D, kBf16>, dim3(static_cast<uint32_t>((all + 3) / 4)), dim3(256), 0, stream, c,
-                       out, parts, q_heads, plan.splits);
+  if (e != hipSuccess || !workspace) return e;
+  const dim3 join(static_cast<uint32_t>((all + 3) / 4));
+  if constexpr (kTree) {
+    if (shared)
+      return launch_kernel(kv8_tree_join_kernel<D, kBf16>, dim3(static_cast<uint32_t>((all * (D / 4) + 255) / 256)),
+                           dim3(256), 0, stream, c, out, parts, q_heads);
+  }
+  return launch_kernel(kv8_join_kernel<D, kBf16>, join, dim3(256), 0, stream, c, out, parts, q_heads, plan.splits);
 }
 
 template <bool kTree>
@@ -1043,13 +1111,30 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
   return p;
 }
 
+// Trees: the same forms; of the prompt form the workgroups share the keys out.
+Kv8Plan plan_kv8_tree_attention(const Kv8Cache& c, int q_heads) {
+  Kv8Plan p = plan_kv8_attention(c, q_heads);
+  if (p.decode) return p;
+  const int64_t groups = p.prompt_blocks / p.splits;  // at least the row tiles there are, times kv heads
+  const int64_t tiles = (static_cast<int64_t>(c.table_width) * c.page + 63) / 64;
+  p.workspace_bytes = 0;
+  p.prompt_blocks = groups;
+  p.splits = 1;
+  p.least = 1 << 26;
+  if (tiles > 2 && groups < (1 << 22) && static_cast<int64_t>(c.tokens) * q_heads < (int64_t{1} << 26)) {
+    p.least = 2;
+    p.prompt_blocks = 2 * groups > kTreeShares ? 2 * groups : kTreeShares;
+    p.workspace_bytes = static_cast<size_t>(p.prompt_blocks) * kPromptRows * (c.head_dim + 2) * sizeof(float) +
+                        static_cast<size_t>(c.tokens) * q_heads * 8;
+  }
+  return p;
+}
+
 hipError_t launch_kv8_attention(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, uint16_t* out, int q_heads,
                                 float softmax_scale, const Kv8Plan& plan, void* workspace, bool bf16,
                                 hipStream_t stream) {
   return launch<false>(c, q, q_stride, Kv8Tree{}, out, q_heads, softmax_scale, plan, workspace, bf16, stream);
 }
-
-Kv8Plan plan_kv8_tree_attention(const Kv8Cache& c, int q_heads) { return plan_kv8_attention(c, q_heads); }
 
 hipError_t launch_kv8_tree_attention(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, const Kv8Tree& tree,
                                      uint16_t* out, int q_heads, float softmax_scale, const Kv8Plan& plan,

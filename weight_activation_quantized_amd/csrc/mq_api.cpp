@@ -951,6 +951,7 @@ static mq_status kv8_attention_impl(const uint16_t* q, int64_t q_stride, const u
   MQ_TRY(need(out, T, "out"));
   if (!aligned(out, 16)) return fail(MQ_ERR_ALIGN, "out must be 16-byte aligned");
   if (tree) MQ_TRY(kv8_tree_words(tree->mask, T, tree->words, max_q_len));
+  if (tree && T * Hq > (int64_t{1} << 30)) return fail(MQ_ERR_SHAPE, "T * Hq = %lld must not exceed 2^30", (long long)(T * Hq));
   const mq::Kv8Plan plan = tree ? mq::plan_kv8_tree_attention(c, static_cast<int>(Hq))
                                 : mq::plan_kv8_attention(c, static_cast<int>(Hq));
   const bool empty = T == 0 || B == 0;
