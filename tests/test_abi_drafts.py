@@ -150,9 +150,11 @@ def test_draft_verify(lib):
     assert verify(lib, V=0) == SHAPE and verify(lib, V=(1 << 24) + 1) == SHAPE and verify(lib, mq=1025) == SHAPE
     assert verify(lib, T=-1) == SHAPE and verify(lib, B=-1) == SHAPE and verify(lib, mq=0) == SHAPE
     assert verify(lib, kept=AT["probs"] + 400) == ALIAS and verify(lib, path=AT["kept"]) == ALIAS
-    assert verify(lib, next=AT["cu"]) == ALIAS and verify(lib, ws=AT["path"]) == ALIAS
-    need = lib.mq_draft_verify_workspace_bytes(3, 1000, 4)
-    assert need > 0 and verify(lib, n=need - 1) == WS and verify(lib, ws=None) == WS and verify(lib, ws=AT["ws"] + 8) == ALIGN
+    assert verify(lib, next=AT["cu"]) == ALIAS and verify(lib, V=200000, ws=AT["path"]) == ALIAS
+    need = lib.mq_draft_verify_workspace_bytes(3, 200000, 4)
+    assert need > 0 and verify(lib, V=200000, n=need - 1) == WS and verify(lib, V=200000, ws=None) == WS
+    assert verify(lib, V=200000, ws=AT["ws"] + 8) == ALIGN
+    assert lib.mq_draft_verify_workspace_bytes(3, 1000, 4) == 0  # one kernel
     assert lib.mq_draft_verify_workspace_bytes(3, 0, 4) == 0 and lib.mq_draft_verify_workspace_bytes(-1, 10, 4) == 0
     assert verify(lib, B=0, cu=None, kept=None, path=None, next=None, ws=None) == OK
 

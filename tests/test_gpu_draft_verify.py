@@ -78,6 +78,29 @@ def test_chains(V, given):
               most=9 + rep)
 
 
+@pytest.mark.parametrize("V", [65536, 65537, 70001, 140000, 300003])
+def test_long_rows(V):
+    """Rows of more pieces than one workgroup takes, aligned and not."""
+    rng = np.random.default_rng(V)
+    news = [5, 1, 0, 8]
+    for rep in range(2):
+        probs, tokens, uniform, parents = tree_case(rng, news, V, sharp=2.0 + 2 * rep)
+        check(probs, tokens, uniform, news, "long rows", parents=parents, pad=rep)
+        draft = softmax(np.log(probs + 1e-12) + 0.7 * rng.standard_normal(probs.shape))
+        check(probs, tokens, uniform, news, "long rows, chains", draft=draft)
+    flat = np.full((6, V), 1 / V, np.float32)
+    for u in (0.0, 0.25, 0.75, 0.99999994):
+        check(flat, np.array([0, 3, 5, V - 1, 0, 1], np.int32), np.full(6, u, np.float32), [4, 2], "flat")
+
+
+@pytest.mark.parametrize("V", [1000, 66000])
+def test_many_sequences(V):
+    rng = np.random.default_rng(V)
+    news = [int(n) for n in rng.integers(0, 3, 300)]
+    probs, tokens, uniform, parents = tree_case(rng, news, V)
+    check(probs, tokens, uniform, news, "many sequences", parents=parents)
+
+
 def test_large_trees():
     rng = np.random.default_rng(1)
     for news in ([64, 200], [1024, 65]):
@@ -177,7 +200,8 @@ def test_workspace_and_outputs_of_the_caller():
         mq.draft_verify(*args, 8, path=mine[1][:, :7])
     with pytest.raises(TypeError):
         mq.draft_verify(args[0].half(), *args[1:], 8)
+    long = torch.full((13, 200001), 1 / 200001, device="cuda")
     with pytest.raises(mq.MqError):
-        mq.draft_verify(*args, 8, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        mq.draft_verify(long, *args[1:], 8, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     empty = mq.draft_verify(args[0][:0], args[1][:0], args[2][:0], up(np.zeros(3, np.int32)), 4)
     assert empty[0].tolist() == [0, 0] and empty[1].tolist() == [[-1] * 4] * 2 and empty[2].tolist() == [-1, -1]

@@ -137,7 +137,6 @@ struct VerifyArgs {
   void* walks;
   int32_t* lists;
 };
-constexpr int kVerifyPiece = 4096;  // values of a row that a workgroup takes
 size_t verify_workspace(int batch, int vocab, int max_q_len);
 hipError_t launch_draft_verify(VerifyArgs a, int batch, void* workspace, hipStream_t stream);
 
