@@ -624,8 +624,8 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
  *   q_weight, k_weight  [D] of q's type, both or neither (NULL)
  * Requires, beside the append's: rot a multiple of 16 in [16, D]; 1 <= max_pos <=
  * 2^30; 0 <= eps <= 1; interleaved 0 or 1 (else MQ_ERR_UNSUPPORTED);
- * B * (max_q_len / page + 2) * (Hq + 2 Hkv) below about 2^24; cos_sin and weights
- * 16-byte aligned.
+ * 2 B Hkv (max_q_len / page + 2) + B Hq max_q_len / 32 below about 2^24; cos_sin and
+ * weights 16-byte aligned.
  *
  * mq_kv8_tree_mask: node j of a sequence's n new tokens hangs on node
  * parents[cu_q[b] + j] (the sequence's own numbers, less than j; anything else, such

@@ -79,8 +79,13 @@ struct Kv8Turn {
   double eps;
   int q_heads, max_pos, rot;  // rot: a multiple of 16, at most head_dim
   bool next;
+  // by plan_kv8_turn: workgroups of the queries take `tile` tokens and `heads_of` heads,
+  // `tiles` and `parts` of them a sequence
+  int tile, heads_of, tiles, parts;
+  uint32_t share;  // of all workgroups, by the launcher
 };
-int64_t kv8_rope_append_blocks(const Kv8Cache& c, int q_heads);
+Kv8Turn plan_kv8_turn(const Kv8Cache& c, Kv8Turn t);
+int64_t kv8_rope_append_blocks(const Kv8Cache& c, const Kv8Turn& t);  // workgroups of the launch
 hipError_t launch_kv8_rope_append(const Kv8Cache& c, const uint16_t* k, const uint16_t* v, int64_t k_stride,
                                   int64_t v_stride, const Kv8Turn& turning, bool bf16, hipStream_t stream);
 

@@ -23,12 +23,12 @@
 // With the rotation (kTurn) the same launch also norms q and k per head where
 // weights are given, and rotates both by their positions' row of a table of
 // cosines and sines: K on its way into the pages, q into a tensor of its own or
-// in place. A workgroup of q owns (sequence, as many tokens as a page has,
-// query head). A thread reads the 8 values that its own 8 rotate with as well
-// (half the head away; L1 has them), so no lane waits for another but for the
-// norm's sum, which 16 or 8 lanes form by DPP in binary64. All in binary32,
-// every product and sum rounded by itself, so that codes are defined bit for
-// bit; q is rounded once.
+// in place. A lane has two pieces of 8 dimensions that rotate with each other, so
+// nothing is exchanged but the norm's sum, which the 8 or 4 lanes of a row form by
+// DPP in binary64. All in binary32, every product and sum rounded by itself, so
+// that codes are defined bit for bit; q is rounded once. 3 x 2048 tokens, 32 query
+// heads on 8 of 128, with norms: 31.5 us, 4.0 TB/s (q alone 22, k and v alone 16);
+// 64 sequences of one token 4.7, 3.5 of it the launch and q's loads.
 //
 // Bound by latency (lengths, page, rows, maximum, codes follow from each other)
 // for few tokens, 4.0 us for 64 sequences of one; for prompts by that and HBM:
@@ -65,14 +65,20 @@ __device__ __forceinline__ double dpp_f64(double x) {
   return __builtin_bit_cast(double, r);
 }
 
-// Sum over the D / 8 neighbouring lanes that hold a row, in each of them.
+// Sum over the D / 16 neighbouring lanes that hold a row, in each of them.
 template <int D>
 __device__ __forceinline__ double row_sum(double v) {
-  v += dpp_f64<0xB1>(v);   // quad_perm [1, 0, 3, 2]
-  v += dpp_f64<0x4E>(v);   // quad_perm [2, 3, 0, 1]
-  v += dpp_f64<0x141>(v);  // row_half_mirror
-  if constexpr (D == 128) v += dpp_f64<0x140>(v);  // row_mirror
+  v += dpp_f64<0xB1>(v);  // quad_perm [1, 0, 3, 2]
+  v += dpp_f64<0x4E>(v);  // quad_perm [2, 3, 0, 1]
+  if constexpr (D == 128) v += dpp_f64<0x141>(v);  // row_half_mirror
   return v;
+}
+
+// Two binary32 values rounded to 16 bits, the first in the lower half.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+  if constexpr (kBf16) return bf16x2_bits(lo, hi);
+  return as_u32(__builtin_convertvector(f32x2{lo, hi}, f16x2));
 }
 
 template <bool kBf16>
@@ -81,107 +87,143 @@ __device__ __forceinline__ void to_floats(u32x4 w, float (&f)[8]) {
   for (int e = 0; e < 4; ++e) word_to_floats<kBf16>(w[e], f[2 * e], f[2 * e + 1]);
 }
 
-// What a thread needs of the rotation for its 8 dimensions, whatever the token:
-// where the values lie that rotate with its own, and the norm's weights of both.
-template <bool kBf16>
-struct Lane {
-  int d, mate;  // its dimensions; those of the other half of its pairs (d itself where none are needed)
-  float w[8], mate_w[8];
-  __device__ __forceinline__ Lane(const Kv8Turn& t, const uint16_t* weight, int dim) : d(dim), mate(dim) {
+// The two pieces of 8 dimensions of a head that lane k of its D / 16 has: such that
+// rotate with each other, or where nothing rotates or neighbours do any two.
+struct Pieces {
+  int d[2];
+  __device__ __forceinline__ Pieces(const Kv8Turn& t, int k) {
     const int half = t.rot / 2;
-    if (!t.next && d < t.rot) mate = d < half ? d + half : d - half;
-    if (weight) {
-      to_floats<kBf16>(*reinterpret_cast<const u32x4*>(weight + d), w);
-      to_floats<kBf16>(*reinterpret_cast<const u32x4*>(weight + mate), mate_w);
+    if (!t.next && 8 * k < half) {
+      d[0] = 8 * k;
+      d[1] = 8 * k + half;
+    } else {
+      d[0] = 16 * k;
+      d[1] = 16 * k + 8;
     }
   }
 };
 
-// 8 values x of a token's head and their mates, normed and rotated. Every lane
-// of a row takes part.
+// Cosines and sines of a token's position for those pieces (NaN: no such position).
+struct Angles {
+  f32x4 c[2], s[2];  // pairs half a head apart: 8 of each; neighbours: 4 for each piece
+  __device__ __forceinline__ void load(const Kv8Turn& t, const Pieces& at, int pos) {
+    const int half = t.rot / 2;
+    if (at.d[0] >= t.rot) return;
+    const bool known = static_cast<uint32_t>(pos) < static_cast<uint32_t>(t.max_pos);
+    const float* const row = t.cos_sin + static_cast<int64_t>(known ? pos : 0) * t.rot + (t.next ? at.d[0] / 2 : at.d[0]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      c[q] = *reinterpret_cast<const f32x4*>(row + 4 * q);
+      s[q] = *reinterpret_cast<const f32x4*>(row + half + 4 * q);
+    }
+    if (!known) {
+      const float none = __builtin_nanf("");
+      c[0] = c[1] = f32x4{none, none, none, none};
+    }
+  }
+};
+
+// 1 / sqrt(m) within 2^-50 of itself: the instruction's estimate and two steps of
+// Newton's iteration (a square root and a division take four times as long).
+__device__ __forceinline__ double inverse_root(double m) {
+#pragma clang fp contract(fast)
+  const double y0 = __builtin_amdgcn_rsq(m);
+  double y = y0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = fma(y * 0.5, fma(-(m * y), y, 1.0), y);
+  return m > 0.0 && m < __builtin_inf() ? y : y0;  // (0 for infinity, infinity for 0, NaN)
+}
+
+// Two pieces x of a token's head, normed (w: the weights of both) and rotated.
+// Every lane of a row takes part.
 template <int D, bool kBf16>
-__device__ __forceinline__ void turn(const Kv8Turn& t, const Lane<kBf16>& at, bool norm, u32x4 x, u32x4 mate, int pos,
-                                     float (&f)[8]) {
+__device__ __forceinline__ void turn(const Kv8Turn& t, const Pieces& at, const u32x4 (&w)[2], bool norm,
+                                     const u32x4 (&x)[2], const Angles& angle, float (&f)[2][8]) {
 #pragma clang fp contract(off)
-  to_floats<kBf16>(x, f);
-  float m[8];
-  to_floats<kBf16>(mate, m);
+  to_floats<kBf16>(x[0], f[0]);
+  to_floats<kBf16>(x[1], f[1]);
   if (norm) {
     double sum = 0.;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum += static_cast<double>(f[e]) * static_cast<double>(f[e]);
-    const float r = static_cast<float>(1.0 / sqrt(row_sum<D>(sum) / D + t.eps));
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += static_cast<double>(f[q][e]) * static_cast<double>(f[q][e]);
+    const float r = static_cast<float>(inverse_root(row_sum<D>(sum) / D + t.eps));
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float g[8];
+      to_floats<kBf16>(w[q], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[q][e] = (f[q][e] * r) * g[e];
+    }
+  }
+  if (at.d[0] >= t.rot) return;
+  if (t.next) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = f[q][2 * e], b = f[q][2 * e + 1];
+        f[q][2 * e] = a * angle.c[q][e] - b * angle.s[q][e];
+        f[q][2 * e + 1] = b * angle.c[q][e] + a * angle.s[q][e];
+      }
+  } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      f[e] = (f[e] * r) * at.w[e];
-      m[e] = (m[e] * r) * at.mate_w[e];
-    }
-  }
-  if (at.d >= t.rot) return;
-  const int half = t.rot / 2;
-  const bool known = static_cast<uint32_t>(pos) < static_cast<uint32_t>(t.max_pos);
-  const float* const row = t.cos_sin + static_cast<int64_t>(known ? pos : 0) * t.rot;
-  const float none = __builtin_nanf("");
-  if (t.next) {
-    const f32x4 c = *reinterpret_cast<const f32x4*>(row + at.d / 2), s = *reinterpret_cast<const f32x4*>(row + half + at.d / 2);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float a = f[2 * e], b = f[2 * e + 1], ce = known ? c[e] : none;
-      f[2 * e] = a * ce - b * s[e];
-      f[2 * e + 1] = b * ce + a * s[e];
-    }
-    return;
-  }
-  const bool upper = at.d >= half;
-  const int i = upper ? at.mate : at.d;
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const f32x4 c = *reinterpret_cast<const f32x4*>(row + i + 4 * q), s = *reinterpret_cast<const f32x4*>(row + half + i + 4 * q);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // (x - y and x + -y are the same, bit for bit)
-      const float ce = known ? c[e] : none, se = upper ? s[e] : -s[e];
-      f[4 * q + e] = f[4 * q + e] * ce + m[4 * q + e] * se;
+      const float a = f[0][e], b = f[1][e], c = angle.c[e / 4][e % 4], s = angle.s[e / 4][e % 4];
+      f[0][e] = a * c - b * s;
+      f[1][e] = b * c + a * s;
     }
   }
 }
 
-// The rows of one query head and as many tokens as a page has.
-template <int D, int kThreads, int CPT, bool kBf16>
-__device__ __forceinline__ void turn_queries(const Kv8Cache& c, const Kv8Turn& t, int b, int tile, int head) {
-  constexpr int kDc = D / 8;
+// Queries: a workgroup takes `tile` tokens of a sequence (a power of two) and
+// `heads_of` query heads, D / 16 lanes a row; lanes beyond the tokens take other
+// heads. A token's angles are read once for all heads of its lanes, four heads'
+// values are on their way at a time.
+template <int D, int kThreads, bool kBf16>
+__device__ __forceinline__ void turn_queries(const Kv8Cache& c, const Kv8Turn& t, int b, int tile, int part) {
+  constexpr int kL = D / 16, kAtOnce = kThreads == 64 ? 2 : 4;
   const int first_row = max(c.cu[b], 0), n = min(min(c.cu[b + 1], c.tokens) - first_row, c.max_q_len);
-  const int t0 = tile * c.page, count = min(n - t0, c.page);
-  if (count <= 0) return;
+  if (tile * t.tile >= n) return;
   const int start = c.lens[b] - (c.cu[b + 1] - c.cu[b]);
-  const Lane<kBf16> lane(t, t.q_weight, 8 * (static_cast<int>(threadIdx.x) % kDc));
-  u32x4 x[CPT], mate[CPT];
-  int pos[CPT];
-#pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int at = (static_cast<int>(threadIdx.x) + kThreads * i) / kDc;
-    x[i] = mate[i] = u32x4{0u, 0u, 0u, 0u};
-    pos[i] = 0;
-    if (at < count) {
-      const int64_t row = first_row + t0 + at;
-      const uint16_t* const from = t.q + row * t.q_stride + head * D;
-      x[i] = *reinterpret_cast<const u32x4*>(from + lane.d);
-      mate[i] = *reinterpret_cast<const u32x4*>(from + lane.mate);
-      pos[i] = t.positions ? t.positions[row] : start + t0 + at;
-    }
+  const int slot = static_cast<int>(threadIdx.x) / kL, token = tile * t.tile + slot % t.tile;
+  const int step = kThreads / kL / t.tile, end = min((part + 1) * t.heads_of, t.q_heads);
+  const bool live = token < n;
+  const int64_t row = first_row + (live ? token : 0);
+  const Pieces at(t, static_cast<int>(threadIdx.x) % kL);
+  const bool norm = t.q_weight != nullptr;
+  u32x4 w[2];
+  if (norm) {
+    w[0] = *reinterpret_cast<const u32x4*>(t.q_weight + at.d[0]);
+    w[1] = *reinterpret_cast<const u32x4*>(t.q_weight + at.d[1]);
   }
+  Angles angle;
+  angle.load(t, at, t.positions ? t.positions[row] : start + token);
+  const uint16_t* const from = t.q + row * t.q_stride;
+  uint16_t* const to = t.q_out + row * t.q_out_stride;
+  for (int h0 = part * t.heads_of + slot / t.tile; h0 < end; h0 += kAtOnce * step) {
+    u32x4 x[kAtOnce][2];
 #pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int at = (static_cast<int>(threadIdx.x) + kThreads * i) / kDc;
-    float f[8];
-    turn<D, kBf16>(t, lane, t.q_weight != nullptr, x[i], mate[i], pos[i], f);
-    u32x4 w;
+    for (int i = 0; i < kAtOnce; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = half_bits<kBf16>(f[2 * e]) | (static_cast<uint32_t>(half_bits<kBf16>(f[2 * e + 1])) << 16);
-    // (in place too: what this wavefront rotates was read above, and no other reads it)
-    if (at < count)
-      *reinterpret_cast<u32x4*>(t.q_out + (first_row + t0 + at) * t.q_out_stride + head * D + lane.d) = w;
+      for (int q = 0; q < 2; ++q)
+        x[i][q] = *reinterpret_cast<const u32x4*>(from + min(h0 + i * step, end - 1) * D + at.d[q]);
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      float f[2][8];
+      turn<D, kBf16>(t, at, w, norm, x[i], angle, f);
+      // (in place too: a row's lanes are of one wavefront, which has read it)
+      if (live && h0 + i * step < end)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          u32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = half_pair<kBf16>(f[q][2 * e], f[q][2 * e + 1]);
+          *reinterpret_cast<u32x4*>(to + (h0 + i * step) * D + at.d[q]) = v;
+        }
+    }
   }
 }
 
@@ -200,26 +242,32 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, const 
   constexpr bool kQuads = CPT % 4 == 0;
   // V of the page as [D, page], 16 bytes of padding after every 8 rows: lanes
   // that write the same token of rows 8 apart meet no bank twice
-  __shared__ __attribute__((aligned(16))) uint8_t tile[(kThreads == 64 ? kSmallPage : D * 128) + D / 8 * 16];
+  // (not where few tokens are rotated: their V codes go out one by one)
+  constexpr bool kDirect = kTurn && kThreads == 64;
+  __shared__ __attribute__((aligned(16))) uint8_t tile[kDirect ? 16 : (kThreads == 64 ? kSmallPage : D * 128) + D / 8 * 16];
 
   // blockIdx.x = ((sequence * span + page) * kv_heads + head) * 2 + (0: K, 1: V),
-  // with the rotation the query heads behind a page's kv heads
+  // with the rotation without the workgroups of the queries
   unsigned at = blockIdx.x;
-  unsigned unit_of_page = 0;
   if constexpr (kTurn) {
-    const unsigned units = 2 * c.kv_heads + turning.q_heads;
-    unit_of_page = at % units;
-    at /= units;
-    if (unit_of_page >= 2u * c.kv_heads) {
-      turn_queries<D, kThreads, CPT, kBf16>(c, turning, static_cast<int>(at / span), static_cast<int>(at % span),
-                                            static_cast<int>(unit_of_page) - 2 * c.kv_heads);
+    // Evenly among each other: those of the queries stream, those of the keys and
+    // values wait for one load after the other (3 x 2048 tokens: 32.9 us, one kind
+    // behind the other 36.5). Of few tokens the queries first (256 x 1: 8.7, else 10.7).
+    const unsigned queries = static_cast<unsigned>(c.batch) * turning.tiles * turning.parts;
+    const unsigned before = kThreads == 64 ? min(at, queries) : __umulhi(at, turning.share);
+    const unsigned behind = kThreads == 64 ? min(at + 1, queries) : __umulhi(at + 1, turning.share);
+    if (behind != before) {
+      const unsigned tile = before / turning.parts;
+      turn_queries<D, kThreads, kBf16>(c, turning, static_cast<int>(tile / turning.tiles),
+                                       static_cast<int>(tile % turning.tiles), static_cast<int>(before % turning.parts));
       return;
     }
+    at -= before;
   }
-  const bool is_v = (kTurn ? unit_of_page : at) & 1;
-  if constexpr (!kTurn) at >>= 1;
-  const int head = static_cast<int>(kTurn ? unit_of_page >> 1 : at % c.kv_heads);
-  if constexpr (!kTurn) at /= c.kv_heads;
+  const bool is_v = at & 1;
+  at >>= 1;
+  const int head = static_cast<int>(at % c.kv_heads);
+  at /= c.kv_heads;
   const int b = static_cast<int>(at / span);
   const int first_row = c.cu[b], n = c.cu[b + 1] - first_row, len = c.lens[b];
   if (n <= 0 || len <= 0) return;
@@ -249,46 +297,48 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, const 
   const int d = 8 * (static_cast<int>(threadIdx.x) % kDc);  // (kDc divides kThreads)
   const uint16_t* const x = is_v ? v : k;
   const int64_t stride = is_v ? v_stride : k_stride;
-  u32x4 w[CPT];
-#pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int t = token(i);
-    const int64_t row = row0 + t;
-    w[i] = u32x4{0u, 0u, 0u, 0u};
-    if (t >= lo && t < hi && row >= 0 && row < c.tokens)
-      w[i] = *reinterpret_cast<const u32x4*>(x + row * stride + head * D + d);
-  }
   // The largest finite magnitude, and whether some value of this thread is not
-  // finite. Rotated keys are binary32 values from here on.
+  // finite. Rotated keys are binary32 values from here on, two pieces of 8 that a
+  // lane of the row has.
   const bool turned_k = kTurn && !is_v;
-  float f[kTurn ? CPT : 1][8];
+  constexpr int kL = D / 16, kPairs = kTurn ? (CPT + 1) / 2 : 1;
+  float f[kPairs][2][8];
+  u32x4 w[CPT];
+  const Pieces pieces(turning, static_cast<int>(threadIdx.x) % kL);
+  auto pair_token = [&](int i) { return lo + (static_cast<int>(threadIdx.x) + kThreads * i) / kL; };
   float amax;
   bool odd = false;
   if (turned_k) {
     if constexpr (kTurn) {
-      const Lane<kBf16> lane(turning, turning.k_weight, d);
-      u32x4 mate[CPT];
-      int pos[CPT];
+      const bool norm = turning.k_weight != nullptr;
+      u32x4 weight[2], raw[kPairs][2];
+      Angles angle[kPairs];
+      if (norm) {
+        weight[0] = *reinterpret_cast<const u32x4*>(turning.k_weight + pieces.d[0]);
+        weight[1] = *reinterpret_cast<const u32x4*>(turning.k_weight + pieces.d[1]);
+      }
 #pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        const int t = token(i);
+      for (int i = 0; i < kPairs; ++i) {
+        const int t = pair_token(i);
         const int64_t row = row0 + t;
-        mate[i] = u32x4{0u, 0u, 0u, 0u};
-        pos[i] = 0;
-        if (t >= lo && t < hi && row >= 0 && row < c.tokens) {
-          mate[i] = *reinterpret_cast<const u32x4*>(x + row * stride + head * D + lane.mate);
-          pos[i] = turning.positions ? turning.positions[row] : static_cast<int>(pos0) + t;
+        raw[i][0] = raw[i][1] = u32x4{0u, 0u, 0u, 0u};
+        int pos = static_cast<int>(pos0) + t;
+        if (t < hi && row >= 0 && row < c.tokens) {
+          if (turning.positions) pos = turning.positions[row];
+          raw[i][0] = *reinterpret_cast<const u32x4*>(x + row * stride + head * D + pieces.d[0]);
+          raw[i][1] = *reinterpret_cast<const u32x4*>(x + row * stride + head * D + pieces.d[1]);
         }
+        angle[i].load(turning, pieces, pos);
       }
       if (!known) return;
       uint32_t most = 0;
 #pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        turn<D, kBf16>(turning, lane, turning.k_weight != nullptr, w[i], mate[i], pos[i], f[i]);
-        const bool mine = token(i) >= lo && token(i) < hi;  // (others' rotated zeros may be NaN)
+      for (int i = 0; i < kPairs; ++i) {
+        turn<D, kBf16>(turning, pieces, weight, norm, raw[i], angle[i], f[i]);
+        const bool mine = pair_token(i) < hi;  // (zeros of the others may have become NaN)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t m = mine ? __builtin_bit_cast(uint32_t, f[i][e]) & 0x7fffffffu : 0u;
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t m = mine ? __builtin_bit_cast(uint32_t, f[i][e / 8][e % 8]) & 0x7fffffffu : 0u;
           odd |= m >= 0x7f800000u;
           most = m < 0x7f800000u ? max(most, m) : most;
         }
@@ -296,6 +346,14 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, const 
       amax = __builtin_bit_cast(float, most);
     }
   } else {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int t = token(i);
+      const int64_t row = row0 + t;
+      w[i] = u32x4{0u, 0u, 0u, 0u};
+      if (t >= lo && t < hi && row >= 0 && row < c.tokens)
+        w[i] = *reinterpret_cast<const u32x4*>(x + row * stride + head * D + d);
+    }
     if (!known) return;  // (the page's number was on its way with the rows)
     // as 16-bit patterns, whose order is the values' (with infinity and NaN
     // above all others)
@@ -373,41 +431,52 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(Kv8Cache c, const 
   const bool simple = (sb & 0x7fffffu) == 0 && sb >= 0x01000000u && sb <= 0x7e000000u;
   const float r = 1.f / s;
   auto quotient = [&](float a) { return clamp448(simple ? a * r : a / s); };
-  u32x2 codes[CPT];
+  // 8 codes; of values that are not finite (where some are) that of NaN.
+  auto codes_of = [&](const float (&a)[8]) {
+    float v[8];
 #pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    float a[8];
-    if constexpr (kTurn) {
-      if (turned_k) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = f[i][e];
-      } else {
-        to_floats<kBf16>(w[i], a);
-      }
-    } else {
-      to_floats<kBf16>(w[i], a);
-    }
-    uint32_t bad = 0;
-    if (odd) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        bad |= static_cast<uint32_t>((__builtin_bit_cast(uint32_t, a[e]) & 0x7fffffffu) >= 0x7f800000u) << e;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = quotient(a[e]);
-    codes[i] = u32x2{e4m3x4(a[0], a[1], a[2], a[3]), e4m3x4(a[4], a[5], a[6], a[7])};
+    for (int e = 0; e < 8; ++e) v[e] = quotient(a[e]);
+    u32x2 code = {e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7])};
     if (odd) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t at = 8 * (e % 4);
-        if ((bad >> e) & 1) codes[i][e / 4] = (codes[i][e / 4] & ~(0xffu << at)) | (kNanCode << at);
+        if ((__builtin_bit_cast(uint32_t, a[e]) & 0x7fffffffu) >= 0x7f800000u)
+          code[e / 4] = (code[e / 4] & ~(0xffu << at)) | (kNanCode << at);
       }
     }
+    return code;
+  };
+  if (turned_k) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      if (pair_token(i) >= hi) continue;
+      uint8_t* const to = out + static_cast<size_t>(pair_token(i)) * D;
+      *reinterpret_cast<u32x2*>(to + pieces.d[0]) = codes_of(f[i][0]);
+      *reinterpret_cast<u32x2*>(to + pieces.d[1]) = codes_of(f[i][1]);
+    }
+    return;
+  }
+  u32x2 codes[CPT];
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    float a[8];
+    to_floats<kBf16>(w[i], a);
+    codes[i] = codes_of(a);
   }
   if (!is_v) {
 #pragma unroll
     for (int i = 0; i < CPT; ++i)
       if (token(i) < hi) *reinterpret_cast<u32x2*>(out + static_cast<size_t>(token(i)) * D + d) = codes[i];
+    return;
+  }
+  if constexpr (kDirect) {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i)
+      if (token(i) < hi)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          out[static_cast<size_t>(d + e) * c.page + token(i)] = static_cast<uint8_t>(codes[i][e >> 2] >> (8 * (e & 3)));
     return;
   }
   uint8_t* const rows = tile + d * c.page + 2 * d;  // (16 bytes for every 8 rows)
@@ -456,25 +525,53 @@ int page_span(const Kv8Cache& c) {
   return (most + c.page - 2) / c.page + 1;
 }
 
+// With little to move in a page one wavefront does (64 sequences of one token,
+// pages of 16: 4.0 us, with four wavefronts 4.5). With the rotation, whose rows
+// take half as many lanes: up to 8 tokens of 128 dimensions (256 sequences of one
+// token, pages of 64: 8.7 us, with four wavefronts 19.3), two for up to 16 (8 x 750
+// tokens in pages of 16: 38 us, with four 48).
+int append_threads(const Kv8Cache& c, bool turned) {
+  const int most = c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
+  const int chunks = (most < c.page ? most : c.page) * (c.head_dim / 8);
+  if (turned) return chunks <= 128 ? 64 : chunks <= 256 ? 128 : 256;
+  return chunks <= 64 && c.page * c.head_dim <= kSmallPage ? 64 : 256;
+}
+
 template <int D, bool kBf16, bool kTurn>
 hipError_t launch_dim(const Kv8Cache& c, const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride,
                       const Kv8Turn& turning, hipStream_t stream) {
   const int most = c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
   const int span = page_span(c);
-  const int64_t blocks = kTurn ? kv8_rope_append_blocks(c, turning.q_heads) : kv8_append_blocks(c);
-  if (blocks >= (int64_t{1} << 24)) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<uint32_t>(blocks));
+  int64_t blocks = kv8_append_blocks(c);
   // A call of few tokens per sequence never fills a page: its rows need fewer
-  // registers, and with little to move in a page one wavefront does (64
-  // sequences of one token, pages of 16: 4.0 us, with four wavefronts 4.5).
-  // Three more tokens where threads take four at a time.
+  // registers. Three more tokens where threads take four at a time.
   const int rows = most < c.page ? most : c.page;
   const int chunks = rows * (D / 8), padded = (rows + 3 < c.page ? rows + 3 : c.page) * (D / 8);
+  const int threads = append_threads(c, kTurn);
+  Kv8Turn t = turning;
+  if constexpr (kTurn) {
+    // in 1 / 2^32, up: floor(n share / 2^32) counts from 0 to the queries' workgroups
+    // as n does to all (under 2^24 of them)
+    const uint64_t queries = static_cast<uint64_t>(c.batch) * t.tiles * t.parts;
+    blocks += static_cast<int64_t>(queries);
+    t.share = static_cast<uint32_t>(((queries << 32) + blocks - 1) / blocks);
+  }
+  if (blocks >= (int64_t{1} << 24)) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<uint32_t>(blocks));
 #define MQ_APPEND(TH, CPT)                                                                                          \
   return launch_kernel(kv8_append_kernel<D, TH, CPT, kBf16, kTurn>, grid, dim3(TH), 0, stream, c, k, v, k_stride, \
-                       v_stride, span, turning)
-  if (chunks <= 64 && c.page * D <= kSmallPage) MQ_APPEND(64, 1);
-  if (chunks <= 256) MQ_APPEND(256, 1);
+                       v_stride, span, t)
+  if (threads == 64) {
+    if constexpr (kTurn) {
+      if (chunks > 64) MQ_APPEND(64, 2);
+    }
+    MQ_APPEND(64, 1);
+  }
+  if constexpr (kTurn) {
+    if (threads == 128) MQ_APPEND(128, 2);
+  } else {
+    if (chunks <= 256) MQ_APPEND(256, 1);
+  }
   if (chunks <= 512) MQ_APPEND(256, 2);
   if (padded <= 1024) MQ_APPEND(256, 4);
   MQ_APPEND(256, 8);
@@ -496,8 +593,28 @@ hipError_t launch(const Kv8Cache& c, const uint16_t* k, const uint16_t* v, int64
 }  // namespace
 
 int64_t kv8_append_blocks(const Kv8Cache& c) { return static_cast<int64_t>(c.batch) * page_span(c) * c.kv_heads * 2; }
-int64_t kv8_rope_append_blocks(const Kv8Cache& c, int q_heads) {
-  return static_cast<int64_t>(c.batch) * page_span(c) * (c.kv_heads * 2 + q_heads);
+
+// Workgroups of the queries: as many tokens side by side as there are, the other
+// lanes other heads; a multiple of four heads a lane, and workgroups enough for all
+// compute units where heads allow it (3 x 2048 tokens, 32 heads: 31.5 us with about
+// 2048 workgroups, 32.9 with 1024, 36.2 with 512; 512 tokens of one sequence 7.4,
+// with lanes of any number of heads 8.9).
+Kv8Turn plan_kv8_turn(const Kv8Cache& c, Kv8Turn t) {
+  const int most = c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
+  const int slots = append_threads(c, true) / (c.head_dim / 16);
+  for (t.tile = 1; t.tile < slots && t.tile < most;) t.tile *= 2;
+  t.tiles = (most + t.tile - 1) / t.tile;
+  const int side = slots / t.tile;  // heads side by side
+  const int64_t rows = static_cast<int64_t>(c.batch) * t.tiles;
+  const int64_t want = (2048 + rows - 1) / rows;  // parts of the heads
+  int64_t each = (t.q_heads + want - 1) / want;
+  each = (each + 4 * side - 1) / (4 * side) * (4 * side);
+  t.heads_of = static_cast<int>(each);
+  t.parts = (t.q_heads + t.heads_of - 1) / t.heads_of;
+  return t;
+}
+int64_t kv8_rope_append_blocks(const Kv8Cache& c, const Kv8Turn& t) {
+  return kv8_append_blocks(c) + static_cast<int64_t>(c.batch) * t.tiles * t.parts;
 }
 
 hipError_t launch_kv8_append(const Kv8Cache& c, const uint16_t* k, const uint16_t* v, int64_t k_stride,

@@ -1157,9 +1157,6 @@ static mq_status kv8_rope_append_impl(const uint16_t* q, const uint16_t* k, cons
     MQ_TRY(kv8_in_place(q, q_stride, Hq * D, qb, v, v_stride, Hkv * D, vb, "v"));
   }
   if (T == 0 || B == 0) return ok();
-  if (mq::kv8_rope_append_blocks(c, static_cast<int>(Hq)) >= (int64_t{1} << 24))
-    return fail(MQ_ERR_SHAPE, "B * pages of max_q_len tokens * (Hq + 2 Hkv) = %lld must stay below 2^24",
-                (long long)mq::kv8_rope_append_blocks(c, static_cast<int>(Hq)));
   mq::Kv8Turn t = {};
   t.q = q;
   t.q_out = q_out;
@@ -1174,6 +1171,10 @@ static mq_status kv8_rope_append_impl(const uint16_t* q, const uint16_t* k, cons
   t.max_pos = static_cast<int>(max_pos);
   t.rot = static_cast<int>(rot);
   t.next = interleaved != 0;
+  t = mq::plan_kv8_turn(c, t);
+  if (mq::kv8_rope_append_blocks(c, t) >= (int64_t{1} << 24))
+    return fail(MQ_ERR_SHAPE, "%lld workgroups: B * pages of max_q_len tokens * Hkv and B * max_q_len * Hq are too large",
+                (long long)mq::kv8_rope_append_blocks(c, t));
   return hip_status(mq::launch_kv8_rope_append(c, k, v, k_stride, v_stride, t, bf16, as_stream(stream)),
                     "kv8_rope_append launch");
 }
