@@ -633,7 +633,7 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
  *     tree[r, w] bit e = 1 where node 32 w + e is j itself or above it
  *     positions[r] = kv_lens[b] - n + (nodes above j)
  * Rows of no sequence stay as they are. tree [T, tree_width] int32, positions [T]
- * int32, tree_width >= ceil(max_q_len / 32), 1 <= max_q_len <= 1024.
+ * int32, ceil(max_q_len / 32) <= tree_width <= 65536, 1 <= max_q_len <= 1024.
  *
  * mq_kv8_tree_attention: mq_kv8_attention, but row i of sequence b sees the
  * kv_lens[b] - n tokens before the new ones and of the new ones those j whose bit

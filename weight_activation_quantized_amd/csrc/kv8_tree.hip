@@ -12,46 +12,66 @@ namespace {
 // the sequence's own numbers; anything else: it hangs on the context). It sees
 // itself and all above it:
 //   seen(j) = {j} + seen(parent of j),  position(j) = context + |seen(j)| - 1
-// A workgroup takes a sequence: parents in LDS, every thread walks up from its
-// node. Parents have smaller numbers, so the words of a row come one after the
-// other, the last first. Bound by the launch and the walk, one LDS read per step.
+// A workgroup takes a sequence, a thread a node, which walks up and sets its row's
+// bits in LDS. A word holds the three nodes above one, 10 bits each, so a step of
+// the walk, one LDS read, goes up three. Bound by the launch, the loads and the walk:
+// 8 nodes 2.1 us, 96 trees of 100-200 nodes 5.0 (one node a step, words to memory as
+// they come: 6.4; 4 of 1000 nodes 21, 62).
 // ---------------------------------------------------------------------------
 
-constexpr int kMaskThreads = 256;
+constexpr int kNone = kKv8MaxTree - 1;  // (the last node is above no other)
 
-__global__ __launch_bounds__(kMaskThreads) void kv8_tree_mask_kernel(const int32_t* __restrict__ parents,
-                                                                     const int32_t* __restrict__ cu,
-                                                                     const int32_t* __restrict__ lens,
-                                                                     int32_t* __restrict__ mask,
-                                                                     int32_t* __restrict__ positions, int tokens,
-                                                                     int words, int max_q_len) {
-  __shared__ int up[kKv8MaxTree];
-  const int b = static_cast<int>(blockIdx.x);
+// For trees of up to kNodes nodes.
+template <int kNodes>
+__global__ __launch_bounds__(kNodes) void kv8_tree_mask_kernel(const int32_t* __restrict__ parents,
+                                                               const int32_t* __restrict__ cu,
+                                                               const int32_t* __restrict__ lens,
+                                                               int32_t* __restrict__ mask,
+                                                               int32_t* __restrict__ positions, int tokens, int words,
+                                                               int max_q_len) {
+  constexpr int kWords = kNodes / 32, kPitch = kWords + 1;  // (of different banks)
+  __shared__ uint32_t rows[kNodes * kPitch];
+  __shared__ int up[kNodes];     // parents
+  __shared__ int above[kNodes];  // three of them
+  const int b = static_cast<int>(blockIdx.x), j = static_cast<int>(threadIdx.x);
   const int first = max(cu[b], 0), all = cu[b + 1] - cu[b];
-  const int n = min(min(cu[b + 1], tokens) - first, max_q_len);
+  const int n = min(min(cu[b + 1], tokens) - first, max_q_len);  // (at most kNodes)
   const int start = lens[b] - all;
-  for (int j = threadIdx.x; j < n; j += kMaskThreads) {
-    const int p = parents[first + j];
-    up[j] = p >= 0 && p < j ? p : -1;
+  int p = kNone;
+  if (j < n) {
+    p = parents[first + j];
+    p = p >= 0 && p < j ? p : kNone;
   }
+  up[j] = p;
+  uint32_t* const row = rows + j * kPitch;
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) row[w] = 0;
   __syncthreads();
-  for (int j = threadIdx.x; j < n; j += kMaskThreads) {
-    int32_t* const row = mask + static_cast<int64_t>(first + j) * words;
-    int w = words - 1, depth = -1;
-    uint32_t bits = 0;
-    for (int at = j; at >= 0; at = up[at]) {
-      for (; w > at >> 5; --w) {
-        row[w] = static_cast<int32_t>(bits);
-        bits = 0;
-      }
-      bits |= 1u << (at & 31);
-      ++depth;
-    }
-    for (; w >= 0; --w) {
-      row[w] = static_cast<int32_t>(bits);
-      bits = 0;
+  int q = p == kNone ? kNone : up[p], r = q == kNone ? kNone : up[q];
+  above[j] = p | q << 10 | r << 20;
+  __syncthreads();
+  if (j < n) {
+    auto see = [&](int at) { atomicOr(&row[at >> 5], 1u << (at & 31)); };  // (its own row: no read to wait for)
+    see(j);
+    int depth = 0;
+    for (;;) {
+      depth += (p != kNone) + (q != kNone) + (r != kNone);
+      if (p != kNone) see(p);
+      if (q != kNone) see(q);
+      if (r == kNone) break;
+      const int three = above[r];
+      see(r);
+      p = three & 1023;
+      q = three >> 10 & 1023;
+      r = three >> 20 & 1023;
     }
     positions[first + j] = start + depth;
+  }
+  __syncthreads();
+  int32_t* const to = mask + static_cast<int64_t>(first) * words;
+  for (int i = j; i < n * words; i += kNodes) {
+    const int of = i / words, w = i - of * words;
+    to[i] = w < kWords ? static_cast<int32_t>(rows[of * kPitch + w]) : 0;
   }
 }
 
@@ -66,7 +86,10 @@ __global__ __launch_bounds__(kMaskThreads) void kv8_tree_mask_kernel(const int32
 // codes of the page rne_e4m3(code * s_old / s). NaN codes stay NaN.
 //
 // A workgroup owns one (layer, sequence, head, K or V): all codes that move into
-// a page are in LDS before any of them is written.
+// a page are in LDS before any of them is written. Bound by latency: lengths, path,
+// pages, codes with their scales follow from each other, each from memory that no
+// other workgroup has touched (8 layers of 16 sequences, at most 9 tokens kept: 13.7
+// us; one wavefront for all of it 14.3-16, sources looked up ahead 17).
 // ---------------------------------------------------------------------------
 
 constexpr int kKeepThreads = 256;
@@ -158,8 +181,15 @@ __global__ __launch_bounds__(kKeepThreads) void kv8_tree_keep_kernel(Kv8Cache c,
 hipError_t launch_kv8_tree_mask(const int32_t* parents, const int32_t* cu, const int32_t* lens, int32_t* mask,
                                 int32_t* positions, int tokens, int batch, int words, int max_q_len,
                                 hipStream_t stream) {
-  return launch_kernel(kv8_tree_mask_kernel, dim3(static_cast<uint32_t>(batch)), dim3(kMaskThreads), 0, stream, parents,
-                       cu, lens, mask, positions, tokens, words, max_q_len);
+  const dim3 grid(static_cast<uint32_t>(batch));
+  if (max_q_len <= 64)
+    return launch_kernel(kv8_tree_mask_kernel<64>, grid, dim3(64), 0, stream, parents, cu, lens, mask, positions, tokens,
+                         words, max_q_len);
+  if (max_q_len <= 256)
+    return launch_kernel(kv8_tree_mask_kernel<256>, grid, dim3(256), 0, stream, parents, cu, lens, mask, positions,
+                         tokens, words, max_q_len);
+  return launch_kernel(kv8_tree_mask_kernel<kKv8MaxTree>, grid, dim3(kKv8MaxTree), 0, stream, parents, cu, lens, mask,
+                       positions, tokens, words, max_q_len);
 }
 
 hipError_t launch_kv8_tree_keep(const Kv8Cache& c, int layers, const int32_t* path, const int32_t* kept, int width,

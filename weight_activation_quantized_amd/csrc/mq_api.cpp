@@ -926,8 +926,8 @@ int32_t mq_kv8_attention_form(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int
 static mq_status kv8_tree_words(const int32_t* mask, int64_t T, int64_t words, int64_t max_q_len) {
   if (max_q_len < 1 || max_q_len > mq::kKv8MaxTree)
     return fail(MQ_ERR_SHAPE, "max_q_len=%lld: a tree has at most %d nodes", (long long)max_q_len, mq::kKv8MaxTree);
-  if (words < (max_q_len + 31) / 32 || words > kMaxDim)
-    return fail(MQ_ERR_SHAPE, "tree_width=%lld words do not hold max_q_len=%lld bits", (long long)words, (long long)max_q_len);
+  if (words < (max_q_len + 31) / 32 || words > 65536)
+    return fail(MQ_ERR_SHAPE, "tree_width=%lld words: at least max_q_len=%lld bits, at most 65536 words", (long long)words, (long long)max_q_len);
   MQ_TRY(need(mask, T, "tree"));
   if (!aligned(mask, 4)) return fail(MQ_ERR_ALIGN, "tree must be 4-byte aligned");
   return MQ_OK;
