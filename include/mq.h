@@ -641,7 +641,8 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
  * sees nothing is 0. The new tokens' NaN codes (a branch that went astray) reach
  * only rows that see them: a K code makes the row NaN, a V code its dimension; NaN
  * before the new tokens, in q and in scales as in mq_kv8_attention. tree
- * [T, tree_width] as above, max_q_len <= 1024.
+ * [T, tree_width] as above, max_q_len <= 1024, T * Hq <= 2^30; workspace as there, of
+ * mq_kv8_tree_attention_workspace_bytes. Sums and weights as there.
  *
  * mq_draft_verify: a sequence's node 0 is its last certain token; probs[r] is the
  * target's distribution of the token after row r (each sums to 1 but for rounding),
@@ -650,7 +651,7 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
  * taken iff, with p and q of the row of the last node taken,
  *     uniform[c] * (1 - sum of p over the tokens of siblings rejected before) < p(x)
  *         (draft_probs NULL: the drafts are taken as given; a token rejected before has
- *         p = 0)
+ *         p = 0, the difference is at least 0)
  *     uniform[c] * q(x) < p(x)
  *         (draft_probs [T, V]: chains whose tokens were drawn from draft_probs)
  * The token after the last one taken comes from the rest that the rejections leave of
@@ -667,7 +668,9 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
  *   mq_kv8_tree_mask; NULL: chains, j hangs on j - 1), uniform [T] fp32, kept,
  *   next_token [B], path [B, max_q_len] int32. 1 <= V <= 2^24, max_q_len <= 1024,
  *   T <= 2^26, B <= 65535; workspace >= mq_draft_verify_workspace_bytes(B, V,
- *   max_q_len) bytes, 16-byte aligned; draft_probs and parents exclude each other.
+ *   max_q_len) bytes (0: may be NULL), 16-byte aligned, overlapping no operand, contents
+ *   on entry do not matter, calls sharing it must be ordered; draft_probs and parents
+ *   exclude each other.
  *
  * mq_kv8_tree_keep: in each of `layers` caches (k_cache [layers, P, Hkv, page, D],
  * v_cache [layers, P, Hkv, D, page], scales [layers, P, Hkv], one block_table), new

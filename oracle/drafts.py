@@ -67,7 +67,7 @@ def verify_ref(probs, tokens, uniform, cu, width, parents=None, draft=None):
                 continue
             x = int(tokens[first + j])
             px = p[cur][x] if 0 <= x < V and x not in gone else 0.0
-            odds = left if draft is None else (float(draft[first + cur, x]) if 0 <= x < V else 1.0)
+            odds = max(left, 0.0) if draft is None else (mass(draft[first + cur])[x] if 0 <= x < V else 1.0)
             if float(uniform[first + j]) * odds < px:
                 cur, gone, left = j, [], 1.0
                 taken.append(j)
@@ -76,9 +76,7 @@ def verify_ref(probs, tokens, uniform, cu, width, parents=None, draft=None):
                 left -= px
         r = p[cur].copy()
         if draft is not None and gone:
-            with np.errstate(invalid="ignore"):
-                d = r - draft[first + cur].astype(np.float64)
-                r = np.where(d > 0, d, 0.0)
+            r = np.maximum(r - mass(draft[first + cur]), 0.0)
         elif gone:
             r[[x for x in gone if 0 <= x < V]] = 0.0
         if not r.sum() > 0:

@@ -174,6 +174,25 @@ def test_odd_rows():
     assert all(0 <= int(t) < V for t in got[2].cpu())  # (which one is not defined)
 
 
+def test_tokens_without_mass_are_not_taken():
+    """Siblings whose probabilities add up to more than 1 by rounding, then one of
+    probability 0 and one rejected before: neither is taken."""
+    V = 50
+    probs = np.zeros((5, V), np.float32)
+    probs[:, 3], probs[:, 4] = 0.6, np.float32(0.4) + np.float32(2.0 ** -20)
+    parents = np.array([-1, 0, 0, 0, 0], np.int32)
+    tokens = np.array([9, 3, 4, 7, 3], np.int32)
+    u = np.array([0.5, 0.999, 0.99999994, 0.5, 0.5], np.float32)
+    u[2] = 1.5  # (no number of [0, 1): both siblings with mass are rejected)
+    want = check(probs, tokens, u, [5], "no mass", parents=parents)
+    assert want[0].tolist() == [1] and want[2].tolist() == [3]  # nothing is left: the row itself
+    draft = probs.copy()
+    draft[:, ::5] = np.nan
+    draft[:, 1::5] = -1
+    for x in (3, 5, 6):
+        check(probs, np.full(5, x, np.int32), np.full(5, 0.25, np.float32), [5], "odd drafts", draft=draft)
+
+
 def test_rejected_token_is_not_drawn():
     """All but a rejected token have next to nothing: it still is not drawn again."""
     V = 9000

@@ -91,7 +91,7 @@ __device__ __forceinline__ Walk walk_tree(const VerifyArgs& a, Nodes& s, int b, 
     s.token[j] = x;
     s.parent[j] = real ? up : -1;
     s.p[j] = known ? a.probs[at] : 0.f;
-    s.q[j] = known && a.draft ? a.draft[at] : 1.f;
+    s.q[j] = known && a.draft ? fmaxf(a.draft[at], 0.f) : 1.f;  // (NaN: 0)
     s.u[j] = a.uniform[first + j];
   }
   __syncthreads();
@@ -110,7 +110,8 @@ __device__ __forceinline__ Walk walk_tree(const VerifyArgs& a, Nodes& s, int b, 
         bool again = false;  // the token of a rejected sibling
         for (int r0 = 0; r0 < rejected; r0 += 64) again |= __any(r0 + lane < rejected && s.gone[r0 + lane] == x);
         const double p = again ? 0. : mass(s.p[child]);
-        const bool yes = static_cast<double>(s.u[child]) * (a.draft ? static_cast<double>(s.q[child]) : left) < p;
+        // (what is left may have fallen below 0 by the row's rounding: a token of p = 0 stays out)
+        const bool yes = static_cast<double>(s.u[child]) * (a.draft ? static_cast<double>(s.q[child]) : fmax(left, 0.)) < p;
         if (yes) {
           if (tells && lane == 0) path[taken] = child;
           ++taken;
@@ -158,7 +159,7 @@ struct Row {
   }
 };
 __device__ __forceinline__ double rest_of(double p, float q) {
-  const double d = p - static_cast<double>(q);
+  const double d = p - mass(q);
   return d > 0. ? d : 0.;
 }
 
