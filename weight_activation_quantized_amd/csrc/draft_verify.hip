@@ -21,7 +21,7 @@
 // Bound by HBM for many long rows (64 chains of 6 with the draft's probabilities,
 // 128000 values: 19.0 us, 3.4 TB/s with the walk), else by the chain of dependent
 // loads: offsets, nodes, their probabilities, the row, the piece (one tree of 8 over
-// 32000: 7.5 us).
+// 32000: 8.5 us).
 #include "block8_launch.h"
 #include "device_common.h"
 
