@@ -41,10 +41,131 @@
 
 #include "block8_launch.h"
 #include "device_common.h"
-#include "kv8_attention.h"
 
 namespace mq {
 namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kNegInf = -__builtin_inff();
+// Scales outside what the append writes would carry sums out of binary32.
+constexpr float kMinScale = 0x1p-100f, kMaxScale = 0x1p120f;
+// What the decode form's weights are raised by, as an exponent and as the
+// factor that takes it back.
+constexpr float kRaise = 15.f, kLower = 0x1p-15f;
+
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
+// 8 e4m3 codes as 8 fp16 or bf16 values (exact).
+template <bool kBf16>
+__device__ __forceinline__ f16x8 widen(uint32_t lo, uint32_t hi) {
+  if constexpr (kBf16) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+    const u32x4 w = {__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
+                     __builtin_bit_cast(uint32_t, d)};
+    return __builtin_bit_cast(f16x8, w);
+  } else {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false);
+    const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true);
+    return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+  }
+}
+
+__device__ __forceinline__ f16x8 to_f16(f32x8 v) { return __builtin_convertvector(v, f16x8); }
+
+// 16 codes of which only the first n count: the others become 0.
+__device__ __forceinline__ u32x4 first_bytes(u32x4 v, int n) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int k = n - 4 * w;
+    v[w] = k >= 4 ? v[w] : k <= 0 ? 0u : v[w] & ((1u << (8 * k)) - 1u);
+  }
+  return v;
+}
+
+__device__ __forceinline__ float held_scale(float s) { return fminf(fmaxf(s, kMinScale), kMaxScale); }
+// The logarithm of a held scale; a NaN, which held_scale hides, stays one here.
+__device__ __forceinline__ float log_scale(float s) {
+  const float l = __builtin_amdgcn_logf(held_scale(s));
+  return s == s ? l : s;
+}
+
+// A sequence as the kernels see it.
+struct Seq {
+  int row0, n, len, seen;  // first row, new tokens, tokens, tokens that the table can hold
+};
+
+__device__ __forceinline__ Seq sequence(const Kv8Cache& c, int b) {
+  Seq s;
+  s.row0 = max(c.cu[b], 0);
+  s.n = max(min(min(c.cu[b + 1], c.tokens) - s.row0, c.max_q_len), 0);
+  s.len = c.lens[b];
+  s.seen = static_cast<int>(min(static_cast<int64_t>(max(s.len, 0)), static_cast<int64_t>(c.table_width) * c.page));
+  return s;
+}
+
+// Which of the 16 keys from new token `at` on (negative: before the new ones,
+// where all are seen) a row's words name, the first in the lowest bit.
+__device__ __forceinline__ uint32_t tree_bits(const int32_t* words, int count, int at) {
+  if (at <= -16) return 0xffffu;
+  const int k = at >> 5;
+  const uint32_t lo = k < 0 ? 0xffffffffu : k < count ? static_cast<uint32_t>(words[k]) : 0u;
+  const uint32_t hi = k + 1 < count ? static_cast<uint32_t>(words[k + 1]) : 0u;
+  return static_cast<uint32_t>((static_cast<uint64_t>(hi) << 32 | lo) >> (at & 31)) & 0xffffu;
+}
+__device__ __forceinline__ uint32_t first_bits(int n) { return n >= 16 ? 0xffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// Of 16 codes the NaN ones become 0 in v; returned are codes of 1 where they were.
+__device__ __forceinline__ u32x4 take_nan(u32x4& v) {
+  u32x4 ones;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t nan = (((v[w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+    v[w] &= ~(nan * 0xffu);
+    ones[w] = nan * 0x38u;
+  }
+  return ones;
+}
+__device__ __forceinline__ bool has_any(u32x4 v) { return (v[0] | v[1] | v[2] | v[3]) != 0; }
+
+// 8 fp16 values, 1 where the bit is set.
+__device__ __forceinline__ f16x8 ones_of(uint32_t bits) {
+  f16x8 v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (bits >> e) & 1 ? static_cast<f16>(1.f) : static_cast<f16>(0.f);
+  return v;
+}
+
+// The workspace of a split call: for every split and row (token, head) its
+// maximum and sum, then its unnormalised output.
+struct Parts {
+  float* ml;  // [splits, rows, 2]
+  float* o;   // [splits, rows, head_dim]
+  // of shared-out trees [shares, kPromptRows] rows, the shares of a row tile kv_heads
+  // apart, and for every row (token, head) the first one's and how many there are
+  size_t rows;
+  u32x2* where;
+};
+
+// The larger of x in lanes l and l ^ 32, in both: the swap leaves the lower
+// half's values in one register and the upper half's in the other. (Written
+// out: the compiler drops the second result of the builtin.)
+__device__ __forceinline__ float halves_max(float x) {
+  float lower = x, upper = x;
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\ts_nop 1" : "+v"(lower), "+v"(upper));
+  return fmaxf(lower, upper);
+}
+
+// The prompt and tree forms' reference of the exponentials follows the maximum
+// lazily: it moves when a score passes it by more than 2^kLazy.
+constexpr float kLazy = 4.f, kLazyRaise = kRaise - kLazy, kLazyLower = 0x1p-11f;
 
 // Tiles of 64 keys that split `z` of `splits` takes of a sequence: [first,
 // first + count). Every split gets the same number, at least `least`.
@@ -403,7 +524,10 @@ __global__ __launch_bounds__(256) void kv8_tree_join_kernel(Kv8Cache c, uint16_t
     f32x4 p[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const size_t at = where[0] + min(z0 + u, splits - 1) * step;
+      ml[u] = f32x2{kNegInf, 0.f};
+      p[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (z0 + u >= splits) continue;
+      const size_t at = where[0] + (z0 + u) * step;
       ml[u] = *reinterpret_cast<const f32x2*>(parts.ml + 2 * at);
       p[u] = *reinterpret_cast<const f32x4*>(parts.o + at * D + d);
     }
@@ -949,13 +1073,46 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
   }
 
   l += __shfl_xor(l, 32, kWave);
-  if (!live) return;
   if constexpr (kTree) {
     // where the joining kernel finds the row's parts
-    if (parts.where && split == 0 && h == 0)
+    if (live && parts.where && split == 0 && h == 0)
       parts.where[static_cast<size_t>(seq.row0 + tq) * heads + head * group + g] =
           u32x2{static_cast<uint32_t>(slot) * kRows + 32 * wave + i, static_cast<uint32_t>(splits)};
+    if (splits > 1) {
+      // A part's rows through LDS, half of the dimensions at a time, so that they go
+      // out whole (8 trees over up to 4096 keys: 45.2 us, 16 bytes of 32 rows at a time
+      // 47.3). Chunks of 16 bytes are XOR-ed by the row, as above.
+      bare_barrier();  // the other wavefronts have read their last tile
+      constexpr int kChunks = D / 8;  // of half a row
+      lds_u8* const mine = lds + wave * (32 * D * 2);
+      const size_t at = static_cast<size_t>(slot) * kRows + 32 * wave;
+      const int count = rows - (kRows * rt + 32 * wave);  // rows of this wavefront
+      if (count <= 0) return;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int d = 0; d < kDt / 2; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const f32x16& v = o[p * (kDt / 2) + d];
+            const f32x4 x = {v[4 * e] * kLazyLower, v[4 * e + 1] * kLazyLower, v[4 * e + 2] * kLazyLower,
+                             v[4 * e + 3] * kLazyLower};
+            *(lds_f32x4*)(mine + 16 * (i * kChunks + ((8 * d + 2 * e + h) ^ (i & (kChunks - 1))))) = x;
+          }
+        wait_counts<63, 0>();  // (the wavefront's own rows: no other waits for them)
+#pragma unroll
+        for (int k = 0; k < 32 * kChunks / 64; ++k) {
+          const int row = (64 * k + lane) / kChunks, chunk = lane % kChunks;
+          const f32x4 x = *(const lds_f32x4*)(mine + 16 * (row * kChunks + (chunk ^ (row & (kChunks - 1)))));
+          if (row < count) *reinterpret_cast<f32x4*>(parts.o + (at + row) * D + p * (D / 2) + 4 * chunk) = x;
+        }
+        wait_counts<63, 0>();
+      }
+      if (live && h == 0) *reinterpret_cast<f32x2*>(parts.ml + 2 * (at + i)) = f32x2{base, l};
+      return;
+    }
   }
+  if (!live) return;
 #pragma unroll
   for (int d = 0; d < kDt; ++d)
 #pragma unroll
@@ -973,8 +1130,7 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
         *reinterpret_cast<u32x2*>(out + to * D + 32 * d + 8 * e + 4 * h) = u32x2{b4[0] | (b4[1] << 16), b4[2] | (b4[3] << 16)};
       }
   } else {
-    const size_t at = kTree ? static_cast<size_t>(slot) * kRows + 32 * wave + i
-                            : static_cast<size_t>(split) * c.tokens * heads + to;
+    const size_t at = static_cast<size_t>(split) * c.tokens * heads + to;
 #pragma unroll
     for (int d = 0; d < kDt; ++d)
 #pragma unroll
@@ -1111,7 +1267,10 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
   return p;
 }
 
-// Trees: the same forms; of the prompt form the workgroups share the keys out.
+// Trees: the same forms, by the same rule (with at most 16 or 32 rows a kv head
+// in the decode form 16 x 16 drafts over up to 4096 keys took 65 us instead of 60,
+// 64 x 8 206 instead of 111); of the prompt form the workgroups share the keys out,
+// two tiles or more a share.
 Kv8Plan plan_kv8_tree_attention(const Kv8Cache& c, int q_heads) {
   Kv8Plan p = plan_kv8_attention(c, q_heads);
   if (p.decode) return p;

@@ -181,6 +181,7 @@ __global__ __launch_bounds__(kKeepThreads) void kv8_tree_keep_kernel(Kv8Cache c,
 hipError_t launch_kv8_tree_mask(const int32_t* parents, const int32_t* cu, const int32_t* lens, int32_t* mask,
                                 int32_t* positions, int tokens, int batch, int words, int max_q_len,
                                 hipStream_t stream) {
+  // the smallest workgroup that holds a tree (its rows take 1, 11 or 143 KB of LDS)
   const dim3 grid(static_cast<uint32_t>(batch));
   if (max_q_len <= 64)
     return launch_kernel(kv8_tree_mask_kernel<64>, grid, dim3(64), 0, stream, parents, cu, lens, mask, positions, tokens,
