@@ -231,6 +231,52 @@ def test_agrees_with_causal_attention():
         assert np.all(np.abs(got - causal) <= 2 * bound)
 
 
+@pytest.mark.parametrize("page,width", [(16, None), (64, 512)])
+def test_many_sequences(page, width):
+    """More sequences than a wavefront has lanes, so that shares are counted in
+    several steps: some without new tokens, a few large trees over long contexts."""
+    rng = np.random.default_rng(12)
+    news = [int(n) for n in rng.integers(0, 30, 150)]
+    news[0], news[70], news[149] = 0, 300, 200
+    totals = [n + int(t) for n, t in zip(news, rng.integers(0, 60, 150))]
+    for b in (3, 64, 70, 149):
+        totals[b] += 2500
+    check(rng, news, totals, 1, 4, 64, page, "bf16", "many sequences", pad=2, width=width)
+    check(rng, news[60:130], totals[60:130], 2, 3, 128, page, "fp16", "many sequences", width=width)
+
+
+def test_pages_past_4_gb():
+    """The same step on pages at the end of a cache of 4.8 GB and on a small one."""
+    import torch
+    rng = np.random.default_rng(13)
+    H, page, D, news, totals = 8, 128, 128, [40, 3], [300, 200]
+    cu, tree = offsets(news), words_of(random_trees(rng, news), news, totals)
+    T, used, P = 43, 5, 36700
+    qkv, _ = half_tensor(rng.standard_normal((T, 32 + 2 * H, D)), "bf16")
+    angles = rng.uniform(0, 6, (400, 64))
+    cs = up(np.concatenate([np.cos(angles), np.sin(angles)], 1).astype(np.float32))
+    path, kept = up(np.array([[0, 3, 9, 20], [0, 2, -1, -1]], np.int32)), up(np.array([4, 2], np.int32))
+    codes = [torch.from_numpy(rng.integers(0, 120, (used, H, page, D)).astype(np.uint8)).cuda() for _ in "kv"]
+    results = []
+    for pages, first in ((used, 0), (P, P - used)):
+        dev = [torch.zeros((pages, H, page, D), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn),
+               torch.zeros((pages, H, D, page), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn),
+               torch.full((pages, H), 2.0 ** -6, device="cuda"), torch.full((pages, H), 2.0 ** -6, device="cuda")]
+        dev[0].view(torch.uint8)[first:] = codes[0]
+        dev[1].view(torch.uint8)[first:] = codes[1].transpose(2, 3)
+        table = up((np.array([[0, 1, 2], [3, 4, 2 ** 20]]) + first).astype(np.int32))
+        b = table, up(cu), up(np.array(totals, np.int32))
+        announce(f"drafts on pages from {first} on")
+        q, k, v = qkv.split([32, H, H], 1)
+        q = mq.kv8_rope_append(q, k, v, *dev, *b, 40, cs)
+        o = mq.kv8_tree_attention(q, up(tree), *dev, *b, max_q_len=40)
+        mq.kv8_tree_keep(*dev, *b, path, kept)
+        results.append([q, o] + [t.view(torch.uint8)[first:].clone() for t in dev])
+        assert not dev[0].view(torch.uint8)[:first].any() and not dev[1].view(torch.uint8)[:first].any()
+        del dev
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
 def test_strided_queries_and_workspace():
     import torch
     rng = np.random.default_rng(10)
