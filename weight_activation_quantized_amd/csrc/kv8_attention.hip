@@ -633,7 +633,7 @@ __device__ __forceinline__ RowTile row_tile(const Kv8Cache& c, int group, int n)
 // kv heads, are at most `target`; each sequence's keys are cut evenly into
 // ceil(tiles / per). Every workgroup finds its own share by that count, the
 // joining kernel those of its rows where the first share left them. (8 trees of up
-// to 64 nodes over up to 8192 keys, 32 query heads on 8 of 128: 72 us; every
+// to 64 nodes over up to 8192 keys, 32 query heads on 8 of 128: 71 us; every
 // sequence in four splits 86.)
 // ---------------------------------------------------------------------------
 
