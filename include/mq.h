@@ -682,7 +682,8 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
  *     s = max(s_old, smallest 2^e with a <= 448 * 2^e, -100 <= e <= 120)
  *     moved codes    e4m3_rne(clamp(fl32(code * (s_source / s))))
  *     others         unchanged if s = s_old, else e4m3_rne(code * (s_old / s))
- * NaN codes stay. Where a token's own page or its new one is none of the pool's it
+ * NaN codes stay; a token whose source's scale is NaN or infinite gets the code 0x7F,
+ * and a NaN scale stays. Where a token's own page or its new one is none of the pool's it
  * does not move. kept[b] <= 1, or a path 0, 1, 2, ..., changes nothing. Each page
  * written must belong to one sequence only. path_width <= 1024, layers <= 65535,
  * B * Hkv < 2^23.

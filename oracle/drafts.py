@@ -120,6 +120,8 @@ def keep_ref(k_cache, v_cache, k_scales, v_scales, table, cu, lens, path, kept):
                         tile = c[layer, p, h].T if tr else c[layer, p, h]
                         codes = [(c[layer, q, h].T if tr else c[layer, q, h])[t].copy() for _, q, t in move]
                         from_s = [np.float32(s[layer, q, h]) for _, q, _ in move]
+                        codes = [x if np.isfinite(f) else np.full_like(x, 0x7F) for x, f in zip(codes, from_s)]
+                        from_s = [f if np.isfinite(f) else np.float32(1) for f in from_s]
                         amax = max(np.max(np.where((x & 0x7F) == 0x7F, 0.0, np.abs(np.nan_to_num(e4m3_decode(x))))) * float(f)
                                    for x, f in zip(codes, from_s))
                         old = np.float32(s[layer, p, h])

@@ -89,6 +89,21 @@ def test_scales_far_apart_and_nan():
               table=table)
 
 
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_sources_of_scales_that_are_not_finite(bad):
+    """A token that its page's scale makes NaN or infinite is NaN where it moves to."""
+    rng = np.random.default_rng(7)
+    news, totals = [40, 40], [45, 52]
+    cache, table = layered(rng, 2, totals, 2, 16, 64)
+    for s in cache[2:]:
+        s[:, table[0, 2], 0] = bad
+        s[:, table[1, 3], 1] = bad
+    paths = [[0, 5, 30, 33, 36], [0, 6, 7, 20, 38, 39]]
+    want = check(rng, news, totals, paths, 2, 64, 16, f"scales of {bad}", cache=cache, table=table)
+    assert (want[0][:, table[0, 0], 0, 7:10] == 0x7F).all()  # from nodes 30, 33 and 36, of page 2
+    assert (want[1][:, table[1, 1], 1, :, :2] == 0x7F).all()  # from nodes 38 and 39, of page 3
+
+
 def test_unknown_pages():
     rng = np.random.default_rng(4)
     news, totals = [30, 30], [40, 60]

@@ -83,7 +83,8 @@ __global__ __launch_bounds__(kNodes) void kv8_tree_mask_kernel(const int32_t* __
 // into it,
 //   s = max(s_old, smallest 2^e with a <= 448 2^e)
 // moved codes become rne_e4m3(code * s_source / s), and where s grew all other
-// codes of the page rne_e4m3(code * s_old / s). NaN codes stay NaN.
+// codes of the page rne_e4m3(code * s_old / s). NaN codes stay NaN, and what a
+// scale makes NaN or infinite arrives as the code of NaN.
 //
 // A workgroup owns one (layer, sequence, head, K or V): all codes that move into
 // a page are in LDS before any of them is written. Bound by latency: lengths, path,
@@ -98,7 +99,7 @@ template <int D>
 __global__ __launch_bounds__(kKeepThreads) void kv8_tree_keep_kernel(Kv8Cache c, const int32_t* __restrict__ path,
                                                                      const int32_t* __restrict__ kept, int width) {
   __shared__ uint8_t tile[128 * D];  // codes by token
-  __shared__ float from[128];        // scale of each token's source; below 0: it does not move
+  __shared__ float from[128];        // scale of each token's source; NaN: it does not move
   __shared__ int end;
   __shared__ float wmax[kKeepThreads / 64];
   unsigned at = blockIdx.x;
@@ -139,15 +140,19 @@ __global__ __launch_bounds__(kKeepThreads) void kv8_tree_keep_kernel(Kv8Cache c,
       const int t = lo + i / D, d = i % D;
       const int node = way[pos0 + t - start];
       const int src = start + node, page = page_of(src);
-      float s = -1.f;
+      float s = __builtin_nanf("");
       if (page >= 0 && src != pos0 + t) {
         const size_t u = layer_unit + static_cast<size_t>(page) * c.kv_heads;
         s = scales[u];
-        const uint8_t code = codes[u * c.page * D + (src & (c.page - 1)) * by_token + d * by_dim];
+        uint8_t code = codes[u * c.page * D + (src & (c.page - 1)) * by_token + d * by_dim];
+        if (!(fabsf(s) < __builtin_inff())) {
+          code = kNanCode;
+          s = 1.f;
+        }
         tile[t * D + d] = code;
         if ((code & 0x7f) != kNanCode) {
           const f32x2 v = __builtin_amdgcn_cvt_pk_f32_fp8(code, false);
-          amax = fmaxf(amax, fabsf(v[0]) * s);
+          amax = fmaxf(amax, fabsf(v[0] * s));
         }
       }
       if (d == 0) from[t] = s;
@@ -158,8 +163,9 @@ __global__ __launch_bounds__(kKeepThreads) void kv8_tree_keep_kernel(Kv8Cache c,
 #pragma unroll
     for (int i = 0; i < kKeepThreads / 64; ++i) amax = fmaxf(amax, wmax[i]);
     const float need = page_scale(amax);
-    const float s = amax > 0.f && need > old ? need : old;
-    if (s != old) {
+    const bool grows = amax > 0.f && need > old;
+    const float s = grows ? need : old;
+    if (grows) {
       const float ratio = old / s;
       for (int i = threadIdx.x; i < c.page * D / 4; i += kKeepThreads) {
         uint32_t* const w = reinterpret_cast<uint32_t*>(out) + i;
@@ -170,7 +176,7 @@ __global__ __launch_bounds__(kKeepThreads) void kv8_tree_keep_kernel(Kv8Cache c,
     if (threadIdx.x == 0) scales[unit] = s;
     for (int i = threadIdx.x; i < (hi - lo) * D; i += kKeepThreads) {
       const int t = lo + i / D, d = i % D;
-      if (from[t] >= 0.f) out[t * by_token + d * by_dim] = static_cast<uint8_t>(moved(tile[t * D + d], from[t] / s));
+      if (from[t] == from[t]) out[t * by_token + d * by_dim] = static_cast<uint8_t>(moved(tile[t * D + d], from[t] / s));
     }
     __syncthreads();
   }
