@@ -1151,6 +1151,12 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
 // prompt form, whatever their number.
 constexpr int kDecodeRows = 64;
 constexpr int64_t kDecodeTiles = 24576;
+// Of trees, whose prompt form shares keys out better but joins more, in that
+// measure: head dimension 64, 14300 (4 x 60 drafts over 2048) 18.3 us, as a prompt
+// 22.4; 21100 (32 x 40 over 2048) 25.4, 23.8; 25300 (16 x 26 over 2048) 28.4, 25.5;
+// 128, 8700 (4 x 64 over 1024) 17.9, 29.1; 13100 (16 x 26 over 1024) 28.5, 25.7;
+// 16900 (4 x 64 over 2048) 35.1, 30.4.
+constexpr int64_t tree_decode_tiles(int head_dim) { return head_dim == 64 ? 20480 : 12288; }
 // Shares of a tree's call: one workgroup per compute unit (the case above: 384
 // shares 95 us, 512 85).
 constexpr int64_t kTreeShares = 256;
@@ -1227,7 +1233,7 @@ hipError_t launch(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, const 
 // - until 2048 where 32 tiles are left to each, which evens out sequences of
 //   different lengths (64 of up to 8192 keys: four splits 135 us, one 141-146).
 // How long the sequences are is known on the GPU only: there each is cut evenly.
-Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
+static Kv8Plan plan_with(const Kv8Cache& c, int q_heads, int64_t decode_tiles) {
   Kv8Plan p;
   const int group = q_heads / c.kv_heads;
   const int most = c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
@@ -1241,7 +1247,7 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
     return even < bound ? even : bound;
   };
   // (what its grid covers counts, the longest sequence's row tiles for every one)
-  p.decode = rows <= kDecodeRows || c.batch * ((rows + 15) / 16) * c.kv_heads * tiles <= kDecodeTiles;
+  p.decode = rows <= kDecodeRows || c.batch * ((rows + 15) / 16) * c.kv_heads * tiles <= decode_tiles;
   p.waves = p.decode ? 4 : 8;
   const int64_t groups = row_tiles(p.decode ? 16 : kPromptRows) * c.kv_heads;
   auto until = [&](int64_t workgroups, int64_t least) {
@@ -1267,12 +1273,14 @@ Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) {
   return p;
 }
 
-// Trees: the same forms, by the same rule (with at most 16 or 32 rows a kv head
+Kv8Plan plan_kv8_attention(const Kv8Cache& c, int q_heads) { return plan_with(c, q_heads, kDecodeTiles); }
+
+// Trees: the same forms, by the same rule with limits of their own (with at most 16 or 32 rows a kv head
 // in the decode form 16 x 16 drafts over up to 4096 keys took 65 us instead of 60,
 // 64 x 8 206 instead of 111); of the prompt form the workgroups share the keys out,
 // two tiles or more a share.
 Kv8Plan plan_kv8_tree_attention(const Kv8Cache& c, int q_heads) {
-  Kv8Plan p = plan_kv8_attention(c, q_heads);
+  Kv8Plan p = plan_with(c, q_heads, tree_decode_tiles(c.head_dim));
   if (p.decode) return p;
   const int64_t groups = p.prompt_blocks / p.splits;  // at least the row tiles there are, times kv heads
   const int64_t tiles = (static_cast<int64_t>(c.table_width) * c.page + 63) / 64;
