@@ -203,6 +203,31 @@ def test_rejected_token_is_not_drawn():
     assert want[0].tolist() == [1] and want[2][0] != 4321
 
 
+def test_rows_past_2_31_values():
+    """The same drafts in the last rows of 9.4 GB of probabilities and in a small tensor."""
+    import torch
+    rng = np.random.default_rng(14)
+    V, T, news = 2 ** 24, 140, [4, 3]
+    first = T - sum(news)
+    rows = torch.zeros((sum(news), V), device="cuda")
+    at = rng.integers(0, V, (sum(news), 50))
+    rows.scatter_(1, up(at), up(softmax(rng.standard_normal(at.shape))))
+    tokens, uniform = np.zeros(T, np.int32), rng.random(T).astype(np.float32)
+    for j in (1, 2, 3, 5, 6):
+        tokens[first + j] = at[j - 1 if j != 6 else 4][j]
+    parents = np.zeros(T, np.int32)
+    parents[first:] = [-1, 0, 1, 2, -1, 0, 0]
+    uniform[first + 1:first + 3] = 0  # these two are taken: their tokens have some mass
+    probs = torch.zeros((T, V), device="cuda")
+    probs[first:] = rows
+    announce("draft_verify 140 rows of 2^24")
+    got = mq.draft_verify(probs, up(tokens), up(uniform), up(np.array([first, first + 4, T], np.int32)), 4, parents=up(parents))
+    want = mq.draft_verify(rows, up(tokens[first:]), up(uniform[first:]), up(offsets(news)), 4, parents=up(parents[first:]))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert host(got[0]).max() > 1 and host(got[2]).min() >= 0
+    assert all(int(t) in at[p] for t, p in zip(host(got[2]), [int(host(got[1])[0][host(got[0])[0] - 1]), 4 + int(host(got[1])[1][host(got[0])[1] - 1])]))
+
+
 def test_workspace_and_outputs_of_the_caller():
     import torch
     rng = np.random.default_rng(4)

@@ -190,6 +190,32 @@ def test_agrees_with_the_plain_append():
     assert all(torch.equal(s, t) for s, t in zip(*sides))
 
 
+def test_rows_and_angles_past_2_31_values():
+    """q, k, v and out with rows 2^26 values apart, a table of 2^24 + 40 positions:
+    as with dense rows and a small table."""
+    import torch
+    rng = np.random.default_rng(15)
+    T, Hq, H, D, page, far, max_pos = 36, 8, 2, 128, 16, 2 ** 26, 2 ** 24 + 40
+    results = []
+    t, _ = half_tensor(rng.standard_normal((T, Hq + 2 * H, D)), "bf16")
+    cs = up(table_of_angles(rng, 40, D))
+    wide = torch.zeros((T * far,), dtype=torch.bfloat16, device="cuda").view(T, far)[:, :t[0].numel()]
+    wide.copy_(t.view(T, -1))
+    angles = torch.zeros((max_pos, D), device="cuda")
+    angles[-40:] = cs
+    cache, table = _cache(rng, [T], [50], H, page, D)
+    for rows, turns, pos in ((t, cs, 0), (wide.unflatten(1, t.shape[1:]), angles, max_pos - 40)):
+        q, k, v = rows.split([Hq, H, H], 1)
+        out = torch.zeros_like(q) if rows is t else torch.zeros(T * far, dtype=q.dtype, device="cuda").view(T, far)[:, :Hq * D].unflatten(1, (Hq, D))
+        dev = codes_tensor(cache[0]), codes_tensor(cache[1]), up(cache[2]), up(cache[3])
+        announce(f"kv8_rope_append rows {rows.stride(0)} apart, {turns.shape[0]} positions")
+        mq.kv8_rope_append(q, k, v, *dev, up(table), up(np.array([0, T], np.int32)), up(np.array([50], np.int32)), T, turns,
+                           positions=up(np.arange(pos, pos + T, dtype=np.int32)), out=out)
+        results.append([out.clone()] + [x.view(torch.uint8).clone() for x in dev])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    assert results[0][0].abs().max() > 1
+
+
 def test_nothing_to_do():
     import torch
     rng = np.random.default_rng(12)
