@@ -151,6 +151,18 @@ def test_rows_that_see_nothing(width):
             assert np.all(got[0:news[0]:2] == 0)
 
 
+@pytest.mark.parametrize("width", [None, 4096])
+@pytest.mark.parametrize("D", [64, 128])
+def test_more_new_tokens_than_cached(D, width):
+    """The first of the new tokens then have no place, and no row sees them."""
+    rng = np.random.default_rng(16)
+    news, totals = [20, 9, 70, 70, 1], [12, 0, 30, 70, 0]
+    for tree in (words_of(random_trees(rng, news), news, totals, 4),
+                 rng.integers(-2 ** 31, 2 ** 31, (170, 4), dtype=np.int64).astype(np.int32)):
+        got = check(rng, news, totals, 2, 4, D, 16, "bf16", "more new than cached", width=width, tree=tree, most=100, pad=3)
+        assert not got[20:29].any() and not got[169:170].any()
+
+
 def test_unknown_pages():
     rng = np.random.default_rng(5)
     for news, G, width in (([4, 2], 4, None), ([90, 40], 2, 4096)):
