@@ -501,15 +501,18 @@ __global__ __launch_bounds__(256) void kv8_join_kernel(Kv8Cache c, uint16_t* __r
 
 // The same for shared-out trees: D / 4 lanes take a row, whose parts, eight at a
 // time, and their maxima and sums are all requested at once (an empty share's are
-// zeros).
+// zeros). Workgroups take the kv heads in turn, as those that wrote the parts did: for
+// 8 heads, or a multiple, the XCD that joins a part has it in its L2 (8 trees over up
+// to 2048 keys: 32.8 us, rows in order 34.2).
 template <int D, bool kBf16>
 __global__ __launch_bounds__(256) void kv8_tree_join_kernel(Kv8Cache c, uint16_t* __restrict__ out, Parts parts,
                                                             int heads) {
   constexpr int kLanes = D / 4, kRowsOf = 256 / kLanes;
-  const size_t rows = static_cast<size_t>(c.tokens) * heads;
-  const size_t row = static_cast<size_t>(blockIdx.x) * kRowsOf + threadIdx.x / kLanes;
-  if (row >= rows) return;
-  const int token = static_cast<int>(row / heads);
+  const int group = heads / c.kv_heads, head = static_cast<int>(blockIdx.x % c.kv_heads);
+  const int of_head = static_cast<int>(blockIdx.x / c.kv_heads) * kRowsOf + static_cast<int>(threadIdx.x) / kLanes;
+  const int token = of_head / group;
+  if (token >= c.tokens) return;
+  const size_t row = static_cast<size_t>(token) * heads + head * group + of_head % group;
   const u32x2 where = parts.where[row];
   if (token < c.cu[0] || token >= c.cu[c.batch]) return;
   const size_t step = static_cast<size_t>(c.kv_heads) * kPromptRows;
@@ -633,7 +636,7 @@ __device__ __forceinline__ RowTile row_tile(const Kv8Cache& c, int group, int n)
 // kv heads, are at most `target`; each sequence's keys are cut evenly into
 // ceil(tiles / per). Every workgroup finds its own share by that count, the
 // joining kernel those of its rows where the first share left them. (8 trees of up
-// to 64 nodes over up to 8192 keys, 32 query heads on 8 of 128: 71 us; every
+// to 64 nodes over up to 8192 keys, 32 query heads on 8 of 128: 69 us; every
 // sequence in four splits 86.)
 // ---------------------------------------------------------------------------
 
@@ -1198,7 +1201,7 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, co
   const dim3 join(static_cast<uint32_t>((all + 3) / 4));
   if constexpr (kTree) {
     if (shared)
-      return launch_kernel(kv8_tree_join_kernel<D, kBf16>, dim3(static_cast<uint32_t>((all * (D / 4) + 255) / 256)),
+      return launch_kernel(kv8_tree_join_kernel<D, kBf16>, dim3(static_cast<uint32_t>((all / c.kv_heads * (D / 4) + 255) / 256 * c.kv_heads)),
                            dim3(256), 0, stream, c, out, parts, q_heads);
   }
   return launch_kernel(kv8_join_kernel<D, kBf16>, join, dim3(256), 0, stream, c, out, parts, q_heads, plan.splits);
