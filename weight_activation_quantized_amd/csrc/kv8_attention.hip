@@ -148,8 +148,9 @@ __device__ __forceinline__ f16x8 ones_of(uint32_t bits) {
 struct Parts {
   float* ml;  // [splits, rows, 2]
   float* o;   // [splits, rows, head_dim]
-  // of shared-out trees [shares, kPromptRows] rows, the shares of a row tile kv_heads
-  // apart, and for every row (token, head) the first one's and how many there are
+  // of shared-out trees [kept shares, kPromptRows] rows, the shares of a row tile
+  // kv_heads apart, and for every row (token, head) the first one's and how many
+  // there are
   size_t rows;
   u32x2* where;
 };
@@ -633,12 +634,27 @@ __device__ __forceinline__ RowTile row_tile(const Kv8Cache& c, int group, int n)
 // the same number of splits, the longest sequence's take as long as they are and
 // the others' units wait. So trees are shared out there: `per` tiles of 64 keys a
 // share, the fewest with which all shares, sum ceil(tiles / per) over row tiles and
-// kv heads, are at most `target`; each sequence's keys are cut evenly into
-// ceil(tiles / per). Every workgroup finds its own share by that count, the
-// joining kernel those of its rows where the first share left them. (8 trees of up
-// to 64 nodes over up to 8192 keys, 32 query heads on 8 of 128: 69 us; every
-// sequence in four splits 86.)
+// kv heads, are at most tree_shares(row tiles times kv heads); each sequence's keys
+// are cut evenly into ceil(tiles / per). Every workgroup finds its own share by that
+// count, the joining kernel those of its rows where the first share left them. (8
+// trees of up to 64 nodes over up to 8192 keys, 32 query heads on 8 of 128: 69 us;
+// every sequence in four splits 86.)
+//
+// Only row tiles in more than one share leave parts, and their s >= 2 shares are at
+// most twice the s - 1 that splitting adds, so kKeptShares parts hold all of them.
 // ---------------------------------------------------------------------------
+
+// Shares of a call of that many row tiles times kv heads, at most: a workgroup per
+// compute unit, or twice the row tiles, or kMoreShares more than these (32 query
+// heads on 8 of 128: 300 trees of up to 64 nodes over up to 1024 keys 400 us, twice
+// the row tiles at any number 466; 1000 of 17 over 1024 1185, 1523; 100 of 64 over
+// 2048 210, 223; 150 of 17 over 4096 485, 452; with half of kMoreShares 40 of 64 over
+// 4096 186 for 170).
+constexpr int64_t kTreeShares = 256, kMoreShares = 512, kKeptShares = 2 * kMoreShares;
+__host__ __device__ constexpr int64_t tree_shares(int64_t row_tiles) {
+  const int64_t all = row_tiles + (row_tiles < kMoreShares ? row_tiles : kMoreShares);
+  return all > kTreeShares ? all : kTreeShares;
+}
 
 // Sum over this lane and those before it.
 __device__ __forceinline__ int wave_prefix(int v) {
@@ -652,10 +668,6 @@ __device__ __forceinline__ int wave_prefix(int v) {
 }
 __device__ __forceinline__ int last_lane(int v) { return __builtin_amdgcn_readlane(v, 63); }
 
-struct Shares {
-  int target, least;  // workgroups at most, tiles of a share at least
-};
-
 // Row tiles and tiles of keys of sequence b (0 and 0 behind the last one).
 __device__ __forceinline__ void extent(const Kv8Cache& c, int group, int b, int& row_tiles, int& tiles) {
   row_tiles = tiles = 0;
@@ -667,11 +679,10 @@ __device__ __forceinline__ void extent(const Kv8Cache& c, int group, int b, int&
 
 __device__ __forceinline__ int splits_of(int tiles, int per) { return min(max((tiles + per - 1) / per, 1), kMaxSplits); }
 
-// Tiles of a share. W = work, R = shares if nothing is split: W / (target - R)
-// tiles are always enough; for up to 64 sequences fewer are tried first. (In
-// binary32, which all workgroups of both kernels form alike; up by more than its
-// errors.)
-__device__ __forceinline__ int per_share(const Kv8Cache& c, const Shares& w, int group) {
+// Tiles of a share, `fewest` at least. W = work, R = shares if nothing is split: W /
+// (target - R) tiles are always enough; for up to 64 sequences fewer are tried first.
+// (In binary32, which all workgroups form alike; up by more than its errors.)
+__device__ __forceinline__ int per_share(const Kv8Cache& c, int fewest, int group) {
   const int lane = threadIdx.x & 63;
   float work = 0.f;
   int rows = 0, rt, tiles;
@@ -684,47 +695,53 @@ __device__ __forceinline__ int per_share(const Kv8Cache& c, const Shares& w, int
     rows += last_lane(wave_prefix(rt));
   }
   work *= static_cast<float>(c.kv_heads) * 1.0001f;
-  const float least = static_cast<float>(w.least);
+  const float least = static_cast<float>(fewest);
+  const int64_t unsplit = static_cast<int64_t>(rows) * c.kv_heads, target = tree_shares(unsplit);
   if (c.batch <= 64) {
-    const int room = w.target / c.kv_heads;  // shares of one head
-    int per = static_cast<int>(fmaxf(fminf(work / static_cast<float>(w.target), 0x1p26f) + 1.f, least));
+    const int room = static_cast<int>(target / c.kv_heads);  // shares of one head
+    int per = static_cast<int>(fmaxf(fminf(work / static_cast<float>(target), 0x1p26f) + 1.f, least));
     for (int step = 0; step < 16; ++step) {
       const int used = last_lane(wave_prefix(rt * splits_of(tiles, per)));
       if (used <= room) return per;
-      per += max(per * (used - room) / (2 * max(room, 1)), 1);
+      // (in binary32: the product of both passes 2^31 for the longest tables)
+      const float more = static_cast<float>(per) * static_cast<float>(used - room) / static_cast<float>(2 * room);
+      per += max(static_cast<int>(fminf(more, 0x1p26f)), 1);
     }
   }
-  const float room = static_cast<float>(max(static_cast<int64_t>(w.target) - static_cast<int64_t>(rows) * c.kv_heads, int64_t{1}));
-  return static_cast<int>(fmaxf(fminf(work / room, 0x1p26f) + 1.f, least));
+  return static_cast<int>(fmaxf(fminf(work / static_cast<float>(target - unsplit), 0x1p26f) + 1.f, least));
 }
 
 struct Share {
   int b, rt, split, splits;  // b < 0: there is none
+  int kept;                  // (of a split row tile) shares before it that leave parts
 };
 
 // The n-th share (of one kv head).
 __device__ __forceinline__ Share find_share(const Kv8Cache& c, int group, int per, int n) {
   const int lane = threadIdx.x & 63;
+  int kept = 0;
   for (int b0 = 0; b0 < c.batch; b0 += 64) {
     int rt, tiles;
     extent(c, group, b0 + lane, rt, tiles);
-    const int splits = splits_of(tiles, per), sum = wave_prefix(rt * splits);
+    const int splits = splits_of(tiles, per), mine = rt * splits, parts = splits > 1 ? mine : 0;
+    const int sum = wave_prefix(mine), parts_sum = wave_prefix(parts);
     const uint64_t behind = __ballot(sum > n);
     if (behind) {
       const int at = __builtin_ctzll(behind);
       const int s = __builtin_amdgcn_readlane(splits, at);
-      const int local = n - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(rt, at) * s);
-      return {b0 + at, local / s, local % s, s};
+      const int local = n - __builtin_amdgcn_readlane(sum - mine, at);
+      return {b0 + at, local / s, local % s, s, kept + __builtin_amdgcn_readlane(parts_sum - parts, at) + local};
     }
     n -= last_lane(sum);
+    kept += last_lane(parts_sum);
   }
-  return {-1, 0, 0, 1};
+  return {-1, 0, 0, 1, 0};
 }
 
 template <int D, bool kBf16, bool kTree>
 __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint16_t* __restrict__ q, int64_t q_stride,
                                                          uint16_t* __restrict__ out, Parts parts, int group,
-                                                         int splits, float scale_log2, Kv8Tree tree, Shares shares) {
+                                                         int splits, float scale_log2, Kv8Tree tree, int least) {
   constexpr int kRows = kPromptRows, kKs = D / 16, kDt = D / 32;
   constexpr int kKRow = 2 * D;  // bytes of a widened K row
   constexpr int kKBytes = 64 * kKRow, kVBytes = D * 128;
@@ -740,14 +757,16 @@ __global__ __launch_bounds__(512) void kv8_prompt_kernel(Kv8Cache c, const uint1
   unsigned at = blockIdx.y * gridDim.x + blockIdx.x;
   const int head = static_cast<int>(at % c.kv_heads);
   at /= c.kv_heads;
-  const int slot = static_cast<int>(blockIdx.y * gridDim.x + blockIdx.x);  // (of trees) its part in the workspace
-  int split;
+  int split, slot = 0;  // (of split trees) its part in the workspace
   RowTile tile;
   if constexpr (kTree) {
-    const Share share = find_share(c, group, per_share(c, shares, group), static_cast<int>(at));
+    const Share share = find_share(c, group, per_share(c, least, group), static_cast<int>(at));
     tile = {share.b, share.rt};
     split = share.split;
     splits = share.splits;
+    slot = share.kept * c.kv_heads + head;
+    // (only where cu_q does not ascend are there more than the workspace holds)
+    if (splits > 1 && static_cast<size_t>(slot) >= parts.rows / kRows) return;
   } else {
     split = static_cast<int>(at % splits);  // (few: prompts that need splits have few row tiles)
     tile = row_tile(c, group, static_cast<int>(at / splits));
@@ -1160,9 +1179,9 @@ constexpr int64_t kDecodeTiles = 24576;
 // 128, 8700 (4 x 64 over 1024) 17.9, 29.1; 13100 (16 x 26 over 1024) 28.5, 25.7;
 // 16900 (4 x 64 over 2048) 35.1, 30.4.
 constexpr int64_t tree_decode_tiles(int head_dim) { return head_dim == 64 ? 20480 : 12288; }
-// Shares of a tree's call: one workgroup per compute unit (the case above: 384
-// shares 95 us, 512 85).
-constexpr int64_t kTreeShares = 256;
+
+// Shares of a tree's call that leave parts, at most.
+int64_t kept_shares(const Kv8Plan& p) { return p.prompt_blocks < kKeptShares ? p.prompt_blocks : kKeptShares; }
 
 template <int D, bool kBf16, bool kTree>
 hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, const Kv8Tree& tree, uint16_t* out,
@@ -1174,13 +1193,12 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, co
   Parts parts = {};
   const bool shared = kTree && !plan.decode;  // out by the workgroups themselves
   if (workspace) {
-    const int64_t part_rows = shared ? plan.prompt_blocks * kPromptRows : plan.splits * all;
+    const int64_t part_rows = shared ? kept_shares(plan) * kPromptRows : plan.splits * all;
     parts.o = static_cast<float*>(workspace);
     parts.ml = parts.o + part_rows * D;
     parts.rows = part_rows;
     if (shared) parts.where = reinterpret_cast<u32x2*>(parts.ml + part_rows * 2);
   }
-  const Shares shares = {static_cast<int>(plan.prompt_blocks), plan.least};
   hipError_t e;
   if (plan.decode) {
     const int row_tiles = static_cast<int>((rows + 15) / 16);
@@ -1195,7 +1213,7 @@ hipError_t launch_dim(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, co
     const dim3 grid(static_cast<uint32_t>(plan.prompt_blocks < kWide ? plan.prompt_blocks : kWide),
                     static_cast<uint32_t>((plan.prompt_blocks + kWide - 1) / kWide));
     e = launch_kernel(kv8_prompt_kernel<D, kBf16, kTree>, grid, dim3(512), 0, stream, c, q, q_stride, out, parts, group,
-                      plan.splits, scale_log2, tree, shares);
+                      plan.splits, scale_log2, tree, plan.least);
   }
   if (e != hipSuccess || !workspace) return e;
   const dim3 join(static_cast<uint32_t>((all + 3) / 4));
@@ -1293,8 +1311,8 @@ Kv8Plan plan_kv8_tree_attention(const Kv8Cache& c, int q_heads) {
   p.least = 1 << 26;
   if (tiles > 2 && groups < (1 << 22) && static_cast<int64_t>(c.tokens) * q_heads < (int64_t{1} << 26)) {
     p.least = 2;
-    p.prompt_blocks = 2 * groups > kTreeShares ? 2 * groups : kTreeShares;
-    p.workspace_bytes = static_cast<size_t>(p.prompt_blocks) * kPromptRows * (c.head_dim + 2) * sizeof(float) +
+    p.prompt_blocks = tree_shares(groups);
+    p.workspace_bytes = static_cast<size_t>(kept_shares(p)) * kPromptRows * (c.head_dim + 2) * sizeof(float) +
                         static_cast<size_t>(c.tokens) * q_heads * 8;
   }
   return p;
