@@ -1255,7 +1255,7 @@ hipError_t launch(const Kv8Cache& c, const uint16_t* q, int64_t q_stride, const 
 //   different lengths (64 of up to 8192 keys: four splits 135 us, one 141-146).
 // How long the sequences are is known on the GPU only: there each is cut evenly.
 static Kv8Plan plan_with(const Kv8Cache& c, int q_heads, int64_t decode_tiles) {
-  Kv8Plan p;
+  Kv8Plan p = {};
   const int group = q_heads / c.kv_heads;
   const int most = c.max_q_len < c.tokens ? c.max_q_len : c.tokens;
   const int64_t rows = static_cast<int64_t>(most) * group;
