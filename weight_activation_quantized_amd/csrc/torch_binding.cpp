@@ -10,8 +10,11 @@
 // GPU's current stream.
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -129,8 +132,12 @@ void same_device(const at::Tensor& a, const at::Tensor& b) {
 }
 
 // An unset tensor on `like`'s GPU: at::empty without the dispatcher, which costs
-// as much again (a call with two outputs: 5.2 us of host time, so 4.5).
+// as much again (a call with two outputs: 5.2 us of host time, so 4.5). Not where a
+// dispatch mode watches or replaces the calls, nor where new tensors are filled for
+// the sake of the same results every time: at::empty itself does that.
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType dtype, const at::Tensor& like) {
+  if (c10::impl::TorchDispatchModeTLS::any_modes_set() || at::globalContext().deterministicAlgorithms())
+    return at::empty(shape, at::TensorOptions().dtype(dtype).device(like.device()));
   return at::Tensor(at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt));
 }
 
