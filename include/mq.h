@@ -643,6 +643,8 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
  * before the new tokens, in q and in scales as in mq_kv8_attention. tree
  * [T, tree_width] as above, max_q_len <= 1024, T * Hq <= 2^30; workspace as there, of
  * mq_kv8_tree_attention_workspace_bytes. Sums and weights as there.
+ * mq_kv8_tree_attention_form says which form a call takes, as
+ * mq_kv8_attention_form does of that one; the limits differ.
  *
  * mq_draft_verify: a sequence's node 0 is its last certain token; probs[r] is the
  * target's distribution of the token after row r (each sums to 1 but for rounding),
@@ -709,6 +711,8 @@ mq_status mq_kv8_tree_mask(const int32_t* parents, const int32_t* cu_q, const in
                            void* stream);
 size_t mq_kv8_tree_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
                                              int64_t table_width, int64_t max_q_len);
+int32_t mq_kv8_tree_attention_form(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
+                                   int64_t table_width, int64_t max_q_len);
 mq_status mq_kv8_tree_attention(const uint16_t* q, int64_t q_stride, const int32_t* tree, int64_t tree_width,
                                 const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scales,
                                 const float* v_scales, const int32_t* block_table, const int32_t* cu_q,

@@ -40,6 +40,7 @@ Entry points (same names as the C ABI, without the ``mq_`` prefix):
                                                      k likewise and v written into the cache
     kv8_tree_attention(q, tree, <cache>, <batch>, max_q_len) -> out [T, Hq, D]: attention under the tree's mask
     kv8_tree_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len) -> int
+    kv8_tree_attention_form(T, B, Hq, Hkv, D, page, table_width, max_q_len) -> "decode", "prompt" or None
     draft_verify(probs, tokens, uniform, cu_q, max_q_len) -> (kept, path, next_token) of every sequence
     draft_verify_workspace_bytes(B, V, max_q_len)    -> int
     kv8_tree_keep(<cache>, <batch>, path, kept)      moves the kept drafts together, in all layers' caches
@@ -79,6 +80,7 @@ __all__ = [
     "rmsnorm_int8", "rmsnorm_fp8", "quant_fp8_blocks", "fp8_block_mm", "fp8_block_mm_workspace_bytes", "fp8_linear", "fp8_linear_workspace_bytes",
     "kv8_append", "kv8_attention", "kv8_attention_workspace_bytes", "kv8_attention_form",
     "kv8_rope_append", "kv8_tree_mask", "kv8_tree_attention", "kv8_tree_attention_workspace_bytes",
+    "kv8_tree_attention_form",
     "draft_verify", "draft_verify_workspace_bytes", "kv8_tree_keep",
 ]
 
@@ -164,6 +166,7 @@ _PROTOTYPES = {
     "mq_kv8_rope_append_bf16": (ctypes.c_int, _KV8_ROPE_APPEND),
     "mq_kv8_tree_mask": (ctypes.c_int, [_P] * 5 + [_I64] * 4 + [_P]),
     "mq_kv8_tree_attention_workspace_bytes": (ctypes.c_size_t, [_I64] * 8),
+    "mq_kv8_tree_attention_form": (ctypes.c_int32, [_I64] * 8),
     "mq_kv8_tree_attention": (ctypes.c_int, _KV8_TREE_ATTENTION),
     "mq_kv8_tree_attention_bf16": (ctypes.c_int, _KV8_TREE_ATTENTION),
     "mq_draft_verify_workspace_bytes": (ctypes.c_size_t, [_I64] * 3),
@@ -724,6 +727,12 @@ def kv8_tree_mask(parents, cu_q, kv_lens, max_q_len, mask=None, positions=None, 
 def kv8_tree_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len):
     """Workspace bytes ``kv8_tree_attention`` needs (0 if none)."""
     return int(library().mq_kv8_tree_attention_workspace_bytes(T, B, Hq, Hkv, D, page, table_width, max_q_len))
+
+
+def kv8_tree_attention_form(T, B, Hq, Hkv, D, page, table_width, max_q_len):
+    """The form that a ``kv8_tree_attention`` call of these sizes takes, as
+    ``kv8_attention_form``."""
+    return (None, "decode", "prompt")[library().mq_kv8_tree_attention_form(T, B, Hq, Hkv, D, page, table_width, max_q_len)]
 
 
 def kv8_tree_attention(q, tree, k_cache, v_cache, k_scales, v_scales, block_table, cu_q, kv_lens, max_q_len,

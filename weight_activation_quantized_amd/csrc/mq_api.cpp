@@ -922,6 +922,15 @@ int32_t mq_kv8_attention_form(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int
                                                                         : MQ_KV8_FORM_PROMPT;
 }
 
+int32_t mq_kv8_tree_attention_form(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
+                                   int64_t table_width, int64_t max_q_len) {
+  mq::Kv8Plan plan;
+  return max_q_len > mq::kKv8MaxTree || !kv8_plan(T, B, Hq, Hkv, D, page, table_width, max_q_len, plan, true)
+             ? MQ_KV8_FORM_NONE
+         : plan.decode ? MQ_KV8_FORM_DECODE
+                       : MQ_KV8_FORM_PROMPT;
+}
+
 // Words of a tree's masks, 32 new tokens each.
 static mq_status kv8_tree_words(const int32_t* mask, int64_t T, int64_t words, int64_t max_q_len) {
   if (max_q_len < 1 || max_q_len > mq::kKv8MaxTree)
