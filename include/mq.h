@@ -612,7 +612,8 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
  *     x_a' = x_a c_i - x_b s_i,  x_b' = x_b c_i + x_a s_i      for i < rot/2,
  *         (a, b) = (i, i + rot/2), interleaved: (2 i, 2 i + 1); others unchanged
  * q_out gets q' rounded once to 16 bits; k' (not rounded before) and v go into the
- * cache as mq_kv8_append writes them, bit-exact to that definition. A position
+ * cache as mq_kv8_append writes them, bit-exact to that definition (with norms: but
+ * for rows whose r lies within 2^-46 of a rounding border). A position
  * outside [0, max_pos) makes the rotated values NaN. q is rotated for every row of
  * a sequence, also where its k and v are skipped; rows of no sequence stay as they
  * are.
@@ -660,9 +661,12 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
  * its row: r = p without the rejected tokens, or max(0, p - q); r = p where nothing
  * was rejected or nothing is left. It is the smallest v with
  *     sum_{w <= v} r(w) > uniform[node 0] * sum_w r(w).
- * All in binary64, each test exact; the sums' order moves the token only within some
- * 2^-40 of a border. Both rules draw from the target's distribution whatever the
- * drafts. NaN and negative probabilities count as 0; a row without mass gives token
+ * All in binary64. A first child's test and the chains' are exact; the difference of a
+ * later sibling is formed term by term in that order, it and the product rounded each
+ * time (by at most 2^-54 a term, 2^-53 of the product). The sums' order moves the
+ * token only within some 2^-40 of a border. The first rule draws from the target's
+ * distribution whatever the drafts, the second where they were drawn from draft_probs.
+ * NaN and negative probabilities count as 0; a row without mass gives token
  * -1; tokens outside [0, V) are not taken. One-hot rows make it greedy.
  *     kept[b] = nodes taken, node 0 among them (0: the sequence has no rows)
  *     path[b, i] = the i-th of them, -1 from kept[b] on;  next_token[b]

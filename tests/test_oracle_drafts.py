@@ -2,6 +2,8 @@
 multiplication, trees by hand, verification against the distribution that it has
 to draw from, the cache's clean-up by hand."""
 
+from fractions import Fraction
+
 import numpy as np
 import pytest
 
@@ -90,6 +92,40 @@ def test_verification_by_hand():
     # nothing left of the row after its only token was rejected: the row itself
     one = np.array([[0, 1, 0, 0]] * 2, np.float32)
     assert od.verify_ref(one, np.array([0, 1]), np.float32([0.0, 1.0]), np.array([0, 2]), 2)[2].tolist() == [1]
+
+
+def test_which_tests_of_a_draft_are_exact():
+    """Products of two binary32 values have 48 bits: exact in binary64. What rejected
+    siblings leave, and its product, are rounded: 2^-54 a term, 2^-53 of the product."""
+    rng = np.random.default_rng(4)
+    u, q = rng.random((2, 500)).astype(np.float32).astype(np.float64)
+    assert all(Fraction(a * b) == Fraction(a) * Fraction(b) for a, b in zip(u, q))
+    rounded = 0
+    for i in range(500):
+        p = (rng.dirichlet(np.ones(6))[:5]).astype(np.float32).astype(np.float64)
+        left, exact = 1.0, Fraction(1)
+        for k, x in enumerate(p):
+            left, exact = left - x, exact - Fraction(x)
+            assert abs(Fraction(left) - exact) <= (k + 1) * Fraction(1, 2 ** 54)
+        got = u[i] * left
+        assert abs(Fraction(got) - Fraction(u[i]) * Fraction(left)) <= Fraction(got) / 2 ** 53
+        rounded += Fraction(got) != Fraction(u[i]) * exact
+    assert rounded > 0  # one is enough: such a test cannot be called exact
+
+
+def test_norm_factor_next_to_a_rounding_border():
+    """The factor of two orders of the sum differs by 2^-46 of itself at most, and so
+    by one step of binary32 only where a border lies that near."""
+    rng = np.random.default_rng(5)
+    for _ in range(300):
+        x = (rng.standard_normal(128) * np.exp2(rng.integers(-12, 8, 128))).astype(np.float16).astype(np.float64)
+        want = sum(Fraction(v) ** 2 for v in x) / 128 + Fraction(1e-6)
+        for order in (np.arange(128), rng.permutation(128)):
+            total = 0.0
+            for v in x[order]:
+                total += v * v
+            r = 1.0 / np.sqrt(total / 128 + 1e-6)
+            assert abs(Fraction(r) ** 2 * want - 1) <= Fraction(1, 2 ** 45)
 
 
 def test_keep_by_hand():

@@ -10,9 +10,10 @@
 // rejected tokens, or max(0, p - q); from p where nothing was rejected or
 // nothing is left. With r that rest, it is the smallest v with
 //   sum_{w <= v} r(w) > u_0 sum_w r(w)
-// All products and sums in binary64: tests of binary32 values are then exact, and
-// the drawn token does not depend on the order of a sum but within 2^-40 or so
-// of a border.
+// All products and sums in binary64: a first child's test and the chains' are then
+// exact (a product of two binary32 values has 48 bits), what is left to a later
+// sibling is rounded by 2^-54 a term and its product once, and the drawn token does
+// not depend on the order of a sum but within 2^-40 or so of a border.
 //
 // Whether a child is taken depends on single values of two rows: every node's
 // are loaded at once, and one wavefront walks the tree by ballots. Only the last
