@@ -645,7 +645,10 @@ mq_status mq_kv8_attention_bf16(const uint16_t* q, int64_t q_stride, const uint8
  * [T, tree_width] as above, max_q_len <= 1024, T * Hq <= 2^30; workspace as there, of
  * mq_kv8_tree_attention_workspace_bytes. Sums and weights as there.
  * mq_kv8_tree_attention_form says which form a call takes, as
- * mq_kv8_attention_form does of that one; the limits differ.
+ * mq_kv8_attention_form does of that one; the limits differ. Both go by what the host
+ * knows, B, the heads, max_q_len and the table's width: a table much wider than its
+ * sequences need moves calls of more than 64 rows (max_q_len * Hq / Hkv) to the
+ * prompt form.
  *
  * mq_draft_verify: a sequence's node 0 is its last certain token; probs[r] is the
  * target's distribution of the token after row r (each sums to 1 but for rounding),

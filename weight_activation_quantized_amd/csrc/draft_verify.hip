@@ -22,7 +22,7 @@
 // Bound by HBM for many long rows (64 chains of 6 with the draft's probabilities,
 // 128000 values: 19.0 us, 3.4 TB/s with the walk), else by the chain of dependent
 // loads: offsets, nodes, their probabilities, the row, the piece (one tree of 8 over
-// 32000: 8.5 us).
+// 32000: 8.6 us, without drafts 7.7).
 #include "block8_launch.h"
 #include "device_common.h"
 
@@ -377,10 +377,11 @@ int pieces_of(int vocab) { return (vocab + kPiece - 1) / kPiece; }
 
 // One workgroup for a sequence where its 16 wavefronts have a piece each, or where
 // there are sequences for all compute units; otherwise workgroups of four
-// wavefronts, as many as make 512, and a second launch (both measured, in us: 1 row
-// of 16000 6.6, with two launches 7.2; 1 of 32000 7.5, in one 8.9; 64 of 128000 with
-// the draft's 19.0, in one 25.8, with 256 or 2048 workgroups 19.9 and 20.3; 256 of
-// 128000 31.7, in two launches 40.7).
+// wavefronts, as many as make 512, and a second launch (both measured, in us: one
+// sequence without drafts, 16000 values, 7.0, with two launches 7.6; 32000 7.7, in
+// one 9.0; a tree of 8 over 16000 8.1, in two 8.4; over 32000 8.6, in one 10.4; 64
+// chains of 6 over 128000 with the draft's 19.0, in one 25.8, with 256 or 2048
+// workgroups 19.9 and 20.3; 256 of 2 over 128000 31.7, in two launches 40.7).
 constexpr int kOwnPieces = 16, kManyRows = 256, kWorkgroups = 512;
 bool in_one(int batch, int vocab) { return pieces_of(vocab) <= (batch >= kManyRows ? kMaxKept : kOwnPieces); }
 

@@ -87,10 +87,12 @@ __global__ __launch_bounds__(kNodes) void kv8_tree_mask_kernel(const int32_t* __
 // scale makes NaN or infinite arrives as the code of NaN.
 //
 // A workgroup owns one (layer, sequence, head, K or V): all codes that move into
-// a page are in LDS before any of them is written. Bound by latency: lengths, path,
-// pages, codes with their scales follow from each other, each from memory that no
-// other workgroup has touched (8 layers of 16 sequences, at most 9 tokens kept: 13.7
-// us; one wavefront for all of it 14.3-16, sources looked up ahead 17).
+// a page are in LDS before any of them is written. Bound by latency: lengths, the
+// path's end, the page and its scale, and then for every 256 codes, a byte a lane,
+// path, page and the code with its scale, which follow from each other and are waited
+// for in each turn: five turns for nine tokens of 128 dimensions (8 layers of 16
+// sequences, at most 9 tokens kept: 13.7 us; one wavefront for all of it 14.3-16,
+// sources looked up ahead, still by bytes, 17).
 // ---------------------------------------------------------------------------
 
 constexpr int kKeepThreads = 256;
